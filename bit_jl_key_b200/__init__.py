@@ -18,6 +18,12 @@ Functions (same names as the C entry points):
   jl_turbo_rotation_init(d, seed)       -> (Pi bf16 [d, d], Pinv fp32 [d, d])
   jl_turbo_quantize_keys(K, Pi, S, mse_bits) -> (codes int32 [n, words], norms fp16 [n, 2])
   jl_turbo_decode_attention(Q, Pinv, S, codes, norms, V, mse_bits, ...) -> out bf16
+  jl_rotary_frequencies(rot_dim, base, scaling, ...) -> inv_freq (fp32 [rot_dim/2])
+  jl_rotary(Q, positions, inv_freq, K=None, ...) -> out_q, or (out_q, out_k)
+  jl_store_paged(codes, norms, V, cu_seqlens, pools, block_table, seq_lens)
+  jl_accumulate_attention(scores, mass, seq_lens, softmax_scale, decay) -> mass
+  jl_evict_paged(mass, seq_lens, keep, pools, src_table, dst_table, ...)
+      -> (index, mass, lens)
 
 Sign codes are returned as torch.int32 tensors holding the uint32 words bit
 for bit (torch has no general uint32 arithmetic); word w of a key holds sketch
@@ -25,6 +31,7 @@ rows 32w..32w+31, LSB first, bit = 1 iff (S k)_i >= 0.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -57,13 +64,16 @@ EXPORTED = ("jl_status_string", "jl_sketch_init", "jl_quantize_keys",
             "jl_turbo_decode_attention", "jl_turbo_decode_paged_workspace_bytes",
             "jl_turbo_decode_attention_paged", "jl_turbo_dequant_basis",
             "jl_turbo_dequantize_keys", "jl_test_drop_copies", "jl_build_flags",
-            "jl_decode_attention_state", "jl_merge_attention_states")
+            "jl_decode_attention_state", "jl_merge_attention_states",
+            "jl_rotary_frequencies", "jl_rotary", "jl_store_paged", "jl_accumulate_attention",
+            "jl_evict_paged")
 
 # device error codes (jl_device_error)
 JL_DERR_TC_WAIT_TIMEOUT = 1
 JL_DERR_DECODE_PLAN = 3
 JL_DERR_DECODE_WAIT_TIMEOUT = 4
 JL_DERR_INDEX = 5
+JL_DERR_PAGE = 6
 JL_BUILD_INDEX_CHECKS = 1
 
 _lib = None
@@ -144,6 +154,20 @@ def load():
     L.jl_turbo_dequant_basis.argtypes = [vp, vp, i32, i32, vp, vp]
     L.jl_turbo_dequantize_keys.restype = i32
     L.jl_turbo_dequantize_keys.argtypes = [vp, vp, i64, vp, i32, i32, i32, vp, vp]
+    f32, f64 = ctypes.c_float, ctypes.c_double
+    L.jl_rotary_frequencies.restype = i32
+    L.jl_rotary_frequencies.argtypes = [i32, f64, i32, f64, i64, f64, f64, vp]
+    L.jl_rotary.restype = i32
+    L.jl_rotary.argtypes = [vp, vp, i32, i64, i32, i32, i32, i32, i64, i64, i64, i64, vp, vp,
+                            i32, i32, f32, vp, i64, i64, vp, i64, i64, vp]
+    L.jl_store_paged.restype = i32
+    L.jl_store_paged.argtypes = [vp, vp, vp, i64, i64, i64, i32, i32, i32, i32, vp, i32, vp, vp,
+                                 vp, i32, i32, vp, i32, vp, vp]
+    L.jl_accumulate_attention.restype = i32
+    L.jl_accumulate_attention.argtypes = [vp, vp, vp, i32, i32, i32, i64, f32, f32, vp, vp]
+    L.jl_evict_paged.restype = i32
+    L.jl_evict_paged.argtypes = [vp, vp, i32, i32, i64, i32, i32, i32, i32, i32, i32, vp, vp, vp,
+                                 i32, i32, vp, i32, vp, i32, vp, vp, vp, vp]
     L.jl_device_error.restype = i32
     L.jl_device_error.argtypes = [ctypes.POINTER(i32), vp]
     L.jl_build_flags.restype = i32
@@ -740,3 +764,222 @@ def jl_turbo_decode_attention_paged(Q, Pinv, S, code_pages, norm_pages, value_pa
         ctypes.c_float(softmax_scale), _ptr(out), _ptr(scores), _ptr(workspace),
         workspace.numel(), _stream(Q, stream)), "jl_turbo_decode_attention_paged")
     return (out, scores) if scores is not None else out
+
+
+# --------------------------------------------------------------------------
+# The serving loop around a paged cache
+
+@contextlib.contextmanager
+def _entered(device, stream):
+    if stream is not None and not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    with torch.cuda.device(device):
+        with torch.cuda.stream(stream):  # (None: no change)
+            yield
+
+
+def _on(stream, first, *rest):
+    """Context in which a call on these tensors allocates and launches: their
+    device, and `stream` if one is given, so that what the call allocates is
+    ordered on the stream that uses it."""
+    dev = first.device
+    if not first.is_cuda:
+        raise ValueError("libjlkey works on CUDA tensors only (no CPU fallback)")
+    for t in rest:
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors on different devices: {dev} and {t.device}")
+    if stream is None and dev.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return _entered(dev, stream)
+
+
+def _float_code(t: torch.Tensor, what: str) -> int:
+    if t.dtype == torch.bfloat16:
+        return JL_BF16
+    if t.dtype == torch.float32:
+        return JL_F32
+    raise TypeError(f"{what} must be bf16 or fp32, got {t.dtype}")
+
+
+def _want(t, what, dtype, shape):
+    """A contiguous tensor of one type and shape."""
+    if t.dtype != dtype:
+        raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what} must be {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+
+
+ROPE_SCALINGS = {None: 0, "": 0, "linear": 1, "ntk": 2, "banded": 3}
+
+
+def jl_rotary_frequencies(rot_dim: int, base: float = 10000.0, scaling=None, factor: float = 1.0,
+                          original_len: int = 0, low: float = 1.0, high: float = 4.0,
+                          device=None) -> torch.Tensor:
+    """inv_freq [rot_dim / 2] fp32 for jl_rotary: base^(-2j / rot_dim), plain or
+    scaled for long contexts: ``"linear"`` divides all by ``factor``,
+    ``"ntk"`` raises the base so that the lowest is, ``"banded"`` keeps those
+    that turn more than ``high`` times in ``original_len`` positions, divides
+    those that turn less than ``low`` times and blends between."""
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"unknown frequency scaling {scaling!r}")
+    buf = (ctypes.c_float * max(1, rot_dim // 2))()
+    _check(load().jl_rotary_frequencies(rot_dim, base, ROPE_SCALINGS[scaling], factor,
+                                        original_len, low, high,
+                                        ctypes.cast(buf, ctypes.c_void_p)),
+           "jl_rotary_frequencies")
+    return torch.tensor(list(buf), dtype=torch.float32,
+                        device=device if device is not None else "cuda")
+
+
+def jl_rotary(Q, positions, inv_freq, K=None, interleaved: bool = False, inverse: bool = False,
+              scale: float = 1.0, out_q=None, out_k=None, stream=None):
+    """Rotary positions of Q [n, Hq, d] and, when given, K [n, Hkv, d] (bf16 or
+    fp32; any token and head strides, so views of a joint projection are taken
+    as they are).  positions [n] int32; inv_freq [r / 2] fp32 turns the first r
+    entries of each head, in halves or ``interleaved`` pairs; the others are
+    copied.  ``inverse`` turns back, which is also the gradient.  Outputs are
+    new tensors, or ``out_q`` / ``out_k``, which may be the inputs themselves.
+    Returns out_q, or (out_q, out_k)."""
+    dt = _float_code(Q, "Q")
+    if Q.dim() != 3:
+        raise ValueError("Q must be [n, Hq, d]")
+    n, Hq, d = Q.shape
+    if K is not None and (K.dim() != 3 or K.shape[0] != n or K.shape[2] != d or K.dtype != Q.dtype):
+        raise ValueError(f"K must be [{n}, Hkv, {d}] {Q.dtype}, got {tuple(K.shape)} {K.dtype}")
+    _want(positions, "positions", torch.int32, (n,))
+    if inv_freq.dim() != 1:
+        raise ValueError("inv_freq must be [r / 2]")
+    _want(inv_freq, "inv_freq", torch.float32, inv_freq.shape)
+    for o, x, what in ((out_q, Q, "out_q"), (out_k, K, "out_k")):
+        if o is not None and (x is None or o.shape != x.shape or o.dtype != x.dtype):
+            raise ValueError(f"{what} must have its input's shape and type")
+    for t in (Q, K, out_q, out_k):
+        if t is not None and t.stride(2) != 1:
+            raise ValueError("heads must have unit stride along d")
+    with _on(stream, Q, K, positions, inv_freq, out_q, out_k):
+        if out_q is None:
+            out_q = torch.empty((n, Hq, d), dtype=Q.dtype, device=Q.device)
+        if K is not None and out_k is None:
+            out_k = torch.empty((n, K.shape[1], d), dtype=K.dtype, device=K.device)
+        kk, ko = (K, out_k) if K is not None else (Q, out_q)
+        _check(load().jl_rotary(
+            _ptr(Q), _ptr(K), dt, n, Hq, kk.shape[1], d, 2 * inv_freq.shape[0], Q.stride(0),
+            Q.stride(1), kk.stride(0), kk.stride(1), _ptr(positions), _ptr(inv_freq),
+            1 if interleaved else 0, 1 if inverse else 0, scale, _ptr(out_q), out_q.stride(0),
+            out_q.stride(1), _ptr(out_k), ko.stride(0), ko.stride(1), _stream(Q, stream)),
+            "jl_rotary")
+    return out_q if K is None else (out_q, out_k)
+
+
+def _pools(code_pages, norm_pages, value_pages):
+    """(num_pages, Hkv, page_tokens, words, norms per key, d) of a paged cache
+    of either kind of code."""
+    if code_pages.dim() != 4 or value_pages.dim() != 4:
+        raise ValueError("pools must be [pages, Hkv, page_tokens, ...]")
+    num_pages, Hkv, P, words = code_pages.shape
+    d = value_pages.shape[3]
+    c = 1 if norm_pages.dim() == 3 else 2
+    _want(code_pages, "code pages", torch.int32, code_pages.shape)
+    _want(norm_pages, "norm pages", torch.float16, (num_pages, Hkv, P) + ((2,) if c == 2 else ()))
+    _want(value_pages, "value pages", torch.bfloat16, (num_pages, Hkv, P, d))
+    return num_pages, Hkv, P, words, c, d
+
+
+def jl_store_paged(codes, norms, V, cu_seqlens, code_pages, norm_pages, value_pages, block_table,
+                   seq_lens, stream=None) -> None:
+    """A ragged chunk of coded keys and their values into a paged cache.
+
+    codes int32 [N, Hkv, words] and norms fp16 [N, Hkv] (QJL) or [N, Hkv, 2]
+    (TurboQuant-prod), as the quantizers wrote them for the chunk's keys; V
+    bf16 [N, Hkv, d], any 16-byte token and head strides; cu_seqlens int32
+    [B + 1]: sequence b's rows.  Row i of sequence b becomes key seq_lens[b] +
+    i.  Rows of no sequence are skipped; the caller advances seq_lens."""
+    num_pages, Hkv, P, words, c, d = _pools(code_pages, norm_pages, value_pages)
+    N, B = codes.shape[0], seq_lens.shape[0]
+    _want(codes, "codes", torch.int32, (N, Hkv, words))
+    _want(norms, "norms", torch.float16, (N, Hkv) + ((2,) if c == 2 else ()))
+    if V.dtype != torch.bfloat16:
+        raise TypeError(f"V must be bf16, got {V.dtype}")
+    if tuple(V.shape) != (N, Hkv, d) or V.stride(2) != 1:
+        raise ValueError(f"V must be {(N, Hkv, d)} with unit stride along d")
+    _want(seq_lens, "seq_lens", torch.int32, (B,))
+    _want(cu_seqlens, "cu_seqlens", torch.int32, (B + 1,))
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [B, max_pages]")
+    _want(block_table, "block_table", torch.int32, (B, block_table.shape[1]))
+    with _on(stream, codes, norms, V, cu_seqlens, code_pages, norm_pages, value_pages,
+             block_table, seq_lens):
+        _check(load().jl_store_paged(
+            _ptr(codes), _ptr(norms), _ptr(V), V.stride(0), V.stride(1), N, Hkv, words, c, d,
+            _ptr(cu_seqlens), B, _ptr(code_pages), _ptr(norm_pages), _ptr(value_pages),
+            num_pages, P, _ptr(block_table), block_table.shape[1], _ptr(seq_lens),
+            _stream(codes, stream)), "jl_store_paged")
+
+
+def jl_accumulate_attention(scores, mass, seq_lens, softmax_scale: float, decay: float = 1.0,
+                            out=None, stream=None) -> torch.Tensor:
+    """The attention weight each cached key received, added to a running total:
+    decay * mass + the sum over each KV head's query heads of softmax
+    (softmax_scale * scores).  scores fp32 [B, Hq, max_len] as the decode calls
+    return them, mass fp32 [B, Hkv, max_len], seq_lens int32 [B].  Writes
+    ``out`` (default: ``mass`` itself) up to each length and returns it."""
+    if scores.dim() != 3 or mass.dim() != 3:
+        raise ValueError("scores must be [B, Hq, max_len] and mass [B, Hkv, max_len]")
+    B, Hq, T = scores.shape
+    Hkv = mass.shape[1]
+    _want(scores, "scores", torch.float32, (B, Hq, T))
+    _want(mass, "mass", torch.float32, (B, Hkv, T))
+    _want(seq_lens, "seq_lens", torch.int32, (B,))
+    if out is None:
+        out = mass
+    _want(out, "out", torch.float32, (B, Hkv, T))
+    with _on(stream, scores, mass, seq_lens, out):
+        _check(load().jl_accumulate_attention(_ptr(scores), _ptr(mass), _ptr(seq_lens), B, Hq, Hkv,
+                                              T, softmax_scale, decay, _ptr(out),
+                                              _stream(scores, stream)),
+               "jl_accumulate_attention")
+    return out
+
+
+def jl_evict_paged(mass, seq_lens, keep: int, code_pages, norm_pages, value_pages, src_table,
+                   dst_table, recent: int = 0, sink: int = 0, out_index=None, out_mass=None,
+                   out_lens=None, stream=None):
+    """Shrinks a paged cache to at most ``keep`` keys per sequence: the first
+    ``sink``, the last ``recent``, and of the others those with the largest
+    mass (equal: the lower index), per KV head, in their order, copied from the
+    pages of src_table to those of dst_table (which hold none of the keys).
+    mass fp32 [B, Hkv, max_len].  Returns (index int32 [B, Hkv, keep]: the
+    kept keys' old indices, then -1; their mass fp32 [B, Hkv, keep], then 0;
+    lens int32 [B])."""
+    num_pages, Hkv, P, words, c, d = _pools(code_pages, norm_pages, value_pages)
+    if mass.dim() != 3 or src_table.dim() != 2 or dst_table.dim() != 2:
+        raise ValueError("mass must be [B, Hkv, max_len] and the tables [B, pages]")
+    B, _, T = mass.shape
+    _want(mass, "mass", torch.float32, (B, Hkv, T))
+    _want(seq_lens, "seq_lens", torch.int32, (B,))
+    _want(src_table, "src_table", torch.int32, (B, src_table.shape[1]))
+    _want(dst_table, "dst_table", torch.int32, (B, dst_table.shape[1]))
+    if keep < 1:
+        raise ValueError("keep must be at least 1")
+    for t, what, dt, shape in ((out_index, "out_index", torch.int32, (B, Hkv, keep)),
+                               (out_mass, "out_mass", torch.float32, (B, Hkv, keep)),
+                               (out_lens, "out_lens", torch.int32, (B,))):
+        if t is not None:
+            _want(t, what, dt, shape)
+    with _on(stream, mass, seq_lens, code_pages, norm_pages, value_pages, src_table, dst_table,
+             out_index, out_mass, out_lens):
+        if out_index is None:
+            out_index = torch.empty((B, Hkv, keep), dtype=torch.int32, device=mass.device)
+        if out_mass is None:
+            out_mass = torch.empty((B, Hkv, keep), dtype=torch.float32, device=mass.device)
+        if out_lens is None:
+            out_lens = torch.empty((B,), dtype=torch.int32, device=mass.device)
+        _check(load().jl_evict_paged(
+            _ptr(mass), _ptr(seq_lens), B, Hkv, T, keep, recent, sink, words, c, d,
+            _ptr(code_pages), _ptr(norm_pages), _ptr(value_pages), num_pages, P,
+            _ptr(src_table), src_table.shape[1], _ptr(dst_table), dst_table.shape[1],
+            _ptr(out_index), _ptr(out_mass), _ptr(out_lens), _stream(mass, stream)),
+            "jl_evict_paged")
+    return out_index, out_mass, out_lens

@@ -5,6 +5,8 @@
 #include "jl_common.cuh"
 #include "jl_internal.h"
 
+#include <math.h>
+
 #include <atomic>
 #include <mutex>
 
@@ -174,6 +176,29 @@ int validate_quantize(const void *K, jl_dtype kt, int64_t n, int64_t ldk,
   if (!aligned(S, 16) || !aligned(signs, 16) || !aligned(norms, 2))
     return JL_ERR_INVALID_ARG;
   return JL_OK;
+}
+
+// The pools of a paged cache that keys are moved into: JL_OK, or what the
+// entry point returns.
+int validate_pools(const void *codes, const void *norms, const void *values, int num_pages,
+                   int page_tokens, int Hkv, int words, int norms_per_key, int d) {
+  if (Hkv < 1 || num_pages < 1 || page_tokens < 32 || page_tokens % 32 != 0)
+    return JL_ERR_INVALID_ARG;
+  if ((d != 64 && d != 128) || words < 1 || words > 64 || norms_per_key < 1 || norms_per_key > 2)
+    return JL_ERR_UNSUPPORTED;
+  if (!codes || !norms || !values) return JL_ERR_INVALID_ARG;
+  if (!aligned(codes, 16) || !aligned(norms, 16) || !aligned(values, 16)) return JL_ERR_INVALID_ARG;
+  return JL_OK;
+}
+
+// Strides of an n x H x d tensor that is read (any stride, entries may be
+// shared) or written (no two entries at one address).
+bool strides_ok(int64_t n, int H, int d, int64_t tok, int64_t head, bool written) {
+  if (tok < 0 || head < 0 || tok >= ((int64_t)1 << 40) || head >= ((int64_t)1 << 40)) return false;
+  if (!written) return true;
+  if (n == 1) return H == 1 || head >= d;
+  if (H == 1) return tok >= d;
+  return (head >= d && tok >= head * (H - 1) + d) || (tok >= d && head >= tok * (n - 1) + d);
 }
 
 }  // namespace
@@ -519,6 +544,150 @@ int jl_turbo_dequantize_keys(const uint32_t *codes, const uint16_t *norms, int64
   if (n_keys >= ((int64_t)1 << 40)) return JL_ERR_UNSUPPORTED;
   return from_cuda(jlk::launch_turbo_dequantize(codes, norms, n_keys, basis, m, d, mse_bits, out,
                                                 (cudaStream_t)stream));
+}
+
+int jl_rotary_frequencies(int rot_dim, double base, jl_rope_scaling scaling, double factor,
+                          int64_t original_len, double low, double high, float *inv_freq) {
+  if (!inv_freq || rot_dim < 2 || rot_dim > 1024 || rot_dim % 2 != 0) return JL_ERR_INVALID_ARG;
+  if (!(base > 1.0) || isinf(base)) return JL_ERR_INVALID_ARG;
+  if (scaling != JL_ROPE_PLAIN && scaling != JL_ROPE_LINEAR && scaling != JL_ROPE_NTK &&
+      scaling != JL_ROPE_BANDED)
+    return JL_ERR_INVALID_ARG;
+  if (scaling != JL_ROPE_PLAIN && (!(factor > 0.0) || isinf(factor))) return JL_ERR_INVALID_ARG;
+  if (scaling == JL_ROPE_BANDED && (original_len < 1 || !(high > low) || isinf(high) || isinf(low)))
+    return JL_ERR_INVALID_ARG;
+  if (scaling == JL_ROPE_NTK && rot_dim > 2)
+    base *= pow(factor, rot_dim / (rot_dim - 2.0));
+  for (int j = 0; j < rot_dim / 2; ++j) {
+    double f = pow(base, -2.0 * j / rot_dim);
+    if (scaling == JL_ROPE_LINEAR) f /= factor;
+    if (scaling == JL_ROPE_BANDED) {
+      const double turns = (double)original_len * f / 6.283185307179586476925;
+      const double x = (turns - low) / (high - low);
+      const double left = x < 0.0 ? 0.0 : x > 1.0 ? 1.0 : x;  // share that stays unscaled
+      f *= left + (1.0 - left) / factor;
+    }
+    inv_freq[j] = (float)f;
+  }
+  return JL_OK;
+}
+
+int jl_rotary(const void *Q, const void *K, jl_dtype dtype, int64_t n, int Hq, int Hkv, int d,
+              int rot_dim, int64_t q_tok_stride, int64_t q_head_stride, int64_t k_tok_stride,
+              int64_t k_head_stride, const int32_t *positions, const float *inv_freq,
+              int interleaved, int inverse, float scale, void *out_q, int64_t out_q_tok_stride,
+              int64_t out_q_head_stride, void *out_k, int64_t out_k_tok_stride,
+              int64_t out_k_head_stride, jl_stream_t stream) {
+  if (dtype != JL_BF16 && dtype != JL_F32) return JL_ERR_INVALID_ARG;
+  if (n < 0 || Hq < 1 || (K && Hkv < 1) || d < 2 || rot_dim < 2 || rot_dim % 2 != 0 ||
+      rot_dim > d || !isfinite(scale))
+    return JL_ERR_INVALID_ARG;
+  if ((interleaved != 0 && interleaved != 1) || (inverse != 0 && inverse != 1))
+    return JL_ERR_INVALID_ARG;
+  if (d % 2 != 0 || d > 1024 || n >= ((int64_t)1 << 31) || Hq > 65536 || (K && Hkv > 65536))
+    return JL_ERR_UNSUPPORTED;
+  if (n == 0) return JL_OK;
+  if (!Q || !out_q || !positions || !inv_freq || (K && !out_k)) return JL_ERR_INVALID_ARG;
+  const size_t es = dtype == JL_F32 ? 4 : 2;
+  if (!aligned(Q, es) || !aligned(out_q, es) || !aligned(positions, 4) || !aligned(inv_freq, 4) ||
+      (K && (!aligned(K, es) || !aligned(out_k, es))))
+    return JL_ERR_INVALID_ARG;
+  if (!strides_ok(n, Hq, d, q_tok_stride, q_head_stride, false) ||
+      !strides_ok(n, Hq, d, out_q_tok_stride, out_q_head_stride, true))
+    return JL_ERR_INVALID_ARG;
+  if (K && (!strides_ok(n, Hkv, d, k_tok_stride, k_head_stride, false) ||
+            !strides_ok(n, Hkv, d, out_k_tok_stride, out_k_head_stride, true)))
+    return JL_ERR_INVALID_ARG;
+  jlk::RotaryArgs a{};
+  a.q = Q; a.k = K; a.out_q = out_q; a.out_k = K ? out_k : nullptr;
+  a.q_tok = q_tok_stride; a.q_head = q_head_stride;
+  a.out_q_tok = out_q_tok_stride; a.out_q_head = out_q_head_stride;
+  a.k_tok = k_tok_stride; a.k_head = k_head_stride;
+  a.out_k_tok = out_k_tok_stride; a.out_k_head = out_k_head_stride;
+  a.f32 = dtype == JL_F32; a.interleaved = interleaved != 0; a.inverse = inverse != 0;
+  a.n = n; a.Hq = Hq; a.Hkv = Hkv; a.d = d; a.rot = rot_dim;
+  a.positions = positions; a.inv_freq = inv_freq; a.scale = scale;
+  return from_cuda(jlk::launch_rotary(a, (cudaStream_t)stream));
+}
+
+int jl_store_paged(const uint32_t *codes, const uint16_t *norms, const uint16_t *V,
+                   int64_t v_tok_stride, int64_t v_head_stride, int64_t N, int Hkv, int words,
+                   int norms_per_key, int d, const int32_t *cu_seqlens, int B,
+                   uint32_t *code_pages, uint16_t *norm_pages, uint16_t *value_pages,
+                   int num_pages, int page_tokens, const int32_t *block_table, int max_pages,
+                   const int32_t *seq_lens, jl_stream_t stream) {
+  if (N < 0 || B < 0 || max_pages < 1) return JL_ERR_INVALID_ARG;
+  const int st = validate_pools(code_pages, norm_pages, value_pages, num_pages, page_tokens, Hkv,
+                                words, norms_per_key, d);
+  if (st != JL_OK) return st;
+  if (Hkv > 65535 || N >= ((int64_t)1 << 31)) return JL_ERR_UNSUPPORTED;
+  if (N == 0 || B == 0) return JL_OK;
+  if (!codes || !norms || !V || !cu_seqlens || !block_table || !seq_lens)
+    return JL_ERR_INVALID_ARG;
+  if (!aligned(codes, 4) || !aligned(norms, 2) || !aligned(V, 16) || !aligned(cu_seqlens, 4) ||
+      !aligned(block_table, 4) || !aligned(seq_lens, 4) || v_tok_stride % 8 != 0 ||
+      v_head_stride % 8 != 0 || !strides_ok(N, Hkv, d, v_tok_stride, v_head_stride, false))
+    return JL_ERR_INVALID_ARG;
+  jlk::StoreArgs a{};
+  a.codes = codes; a.norms = norms; a.V = V; a.v_tok = v_tok_stride; a.v_head = v_head_stride;
+  a.N = N; a.Hkv = Hkv; a.words = words; a.norms_per_key = norms_per_key; a.d = d; a.B = B;
+  a.cu_seqlens = cu_seqlens; a.block_table = block_table; a.seq_lens = seq_lens;
+  a.code_pages = code_pages; a.norm_pages = norm_pages; a.value_pages = value_pages;
+  a.num_pages = num_pages; a.page_tokens = page_tokens; a.max_pages = max_pages;
+  return from_cuda(jlk::launch_store_paged(a, (cudaStream_t)stream));
+}
+
+int jl_accumulate_attention(const float *scores, const float *mass, const int32_t *seq_lens,
+                            int B, int Hq, int Hkv, int64_t max_len, float softmax_scale,
+                            float decay, float *out, jl_stream_t stream) {
+  if (B < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || max_len < 1) return JL_ERR_INVALID_ARG;
+  if (!isfinite(softmax_scale) || !isfinite(decay)) return JL_ERR_INVALID_ARG;
+  if (Hq / Hkv > 512 || (int64_t)B * Hkv >= (1 << 24) || max_len >= ((int64_t)1 << 31))
+    return JL_ERR_UNSUPPORTED;
+  if (B == 0) return JL_OK;
+  if (!scores || !seq_lens || !out || (decay != 0.f && !mass)) return JL_ERR_INVALID_ARG;
+  if (!aligned(scores, 4) || !aligned(mass, 4) || !aligned(seq_lens, 4) || !aligned(out, 4))
+    return JL_ERR_INVALID_ARG;
+  jlk::AccumulateArgs a{scores, mass, seq_lens, B, Hq, Hkv, max_len, softmax_scale, decay, out};
+  return from_cuda(jlk::launch_accumulate(a, (cudaStream_t)stream));
+}
+
+int jl_evict_paged(const float *mass, const int32_t *seq_lens, int B, int Hkv, int64_t max_len,
+                   int keep, int recent, int sink, int words, int norms_per_key, int d,
+                   uint32_t *code_pages, uint16_t *norm_pages, uint16_t *value_pages,
+                   int num_pages, int page_tokens, const int32_t *src_table, int src_max_pages,
+                   const int32_t *dst_table, int dst_max_pages, int32_t *out_index,
+                   float *out_mass, int32_t *out_lens, jl_stream_t stream) {
+  if (B < 0 || max_len < 1 || keep < 1 || recent < 0 || sink < 0 || src_max_pages < 1 ||
+      dst_max_pages < 1 || (int64_t)recent + sink > keep)
+    return JL_ERR_INVALID_ARG;
+  const int st = validate_pools(code_pages, norm_pages, value_pages, num_pages, page_tokens, Hkv,
+                                words, norms_per_key, d);
+  if (st != JL_OK) return st;
+  if ((int64_t)dst_max_pages * page_tokens < keep ||
+      (int64_t)src_max_pages * page_tokens < max_len)
+    return JL_ERR_INVALID_ARG;
+  // the moved keys are one flat grid of blocks of at least 16 keys
+  if (max_len >= ((int64_t)1 << 31) || (int64_t)B * Hkv >= (1 << 24) ||
+      (int64_t)B * Hkv * ((int64_t)keep / 16 + 1) >= ((int64_t)1 << 31))
+    return JL_ERR_UNSUPPORTED;
+  if (B == 0) return JL_OK;
+  if (!mass || !seq_lens || !src_table || !dst_table || !out_index || !out_mass || !out_lens ||
+      out_mass == mass)
+    return JL_ERR_INVALID_ARG;
+  if (!aligned(mass, 4) || !aligned(seq_lens, 4) || !aligned(src_table, 4) ||
+      !aligned(dst_table, 4) || !aligned(out_index, 4) || !aligned(out_mass, 4) ||
+      !aligned(out_lens, 4))
+    return JL_ERR_INVALID_ARG;
+  jlk::EvictArgs a{};
+  a.mass = mass; a.seq_lens = seq_lens; a.src_table = src_table; a.dst_table = dst_table;
+  a.B = B; a.Hkv = Hkv; a.keep = keep; a.recent = recent; a.sink = sink; a.words = words;
+  a.norms_per_key = norms_per_key; a.d = d; a.max_len = max_len;
+  a.code_pages = code_pages; a.norm_pages = norm_pages; a.value_pages = value_pages;
+  a.num_pages = num_pages; a.page_tokens = page_tokens;
+  a.src_max_pages = src_max_pages; a.dst_max_pages = dst_max_pages;
+  a.out_index = out_index; a.out_lens = out_lens; a.out_mass = out_mass;
+  return from_cuda(jlk::launch_evict_paged(a, (cudaStream_t)stream));
 }
 
 int jl_test_drop_copies(int enable, uint64_t wait_limit_ns) {

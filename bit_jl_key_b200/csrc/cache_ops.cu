@@ -1,0 +1,553 @@
+// cache_ops.cu -- what a serving loop does to a paged compressed cache between
+// attention calls: store a chunk of coded keys, accumulate the attention
+// weight each key received, and evict the keys that received the least.
+//
+//   store   key i of sequence b goes to position seq_lens[b] + i, that is to
+//           page block_table[b][pos / P], slot pos % P.  A copy.
+//   weight  mass'[b][kv][t] = decay mass[b][kv][t]
+//                             + sum over the KV head's query heads of softmax_t(scale s[t]).
+//   evict   of the L keys of a (sequence, KV head), the first `sink`, the last
+//           `recent`, and of the others the ones with the largest mass (equal
+//           masses: the lower index) up to `keep` in all, in their order.
+//
+// All three are bound by memory; the selection of the eviction is a radix
+// select whose histograms and prefix sums are shared by a cluster of blocks.
+#include "jl_common.cuh"
+#include "jl_internal.h"
+
+#include <cooperative_groups.h>
+
+namespace jlk {
+
+namespace cg = cooperative_groups;
+
+namespace {
+
+// The pools of a paged cache, as bytes are moved: a key's code is W words, its
+// norms c binary16s, its value d bf16s.
+struct Pools {
+  uint32_t *codes;
+  uint16_t *norms, *values;
+  int num_pages, P, Hkv, W, c, d;
+  int *err;
+};
+
+__device__ __forceinline__ int64_t pool_row(const Pools &p, int page, int head, int slot) {
+  return ((int64_t)page * p.Hkv + head) * p.P + slot;
+}
+
+// Page of position pos, or -1 (recorded) where the table has no such column
+// or names a page outside the pool.
+__device__ __forceinline__ int table_page(const int32_t *table, int max_pages, int b, int64_t pos,
+                                          const Pools &p) {
+  const int64_t col = pos / p.P;
+  int page = -1;
+  if (pos >= 0 && col < max_pages) page = __ldg(table + (int64_t)b * max_pages + col);
+  if (page < 0 || page >= p.num_pages) {
+    record_device_error(p.err, DERR_PAGE);
+    return -1;
+  }
+  return page;
+}
+
+// Code words and norms of one key, by the `lanes` lanes of its group.
+__device__ __forceinline__ void copy_code(const Pools &p, int64_t dst, const uint32_t *code,
+                                          const uint16_t *norm, int lane, int lanes) {
+  for (int w = lane; w < p.W; w += lanes) p.codes[dst * p.W + w] = code[w];
+  if (lane < p.c) p.norms[dst * p.c + lane] = norm[lane];
+}
+
+}  // namespace
+
+// ---------------------------------------------------------------------------
+// store
+
+namespace store {
+
+constexpr int THREADS = 256;
+
+struct Params {
+  Pools pool;
+  const uint32_t *codes;  // [N][Hkv][W]
+  const uint16_t *norms;  // [N][Hkv][c]
+  const uint16_t *V;      // strided [N][Hkv][d]
+  int64_t v_tok, v_head;
+  const int32_t *cu, *table, *lens;
+  int B, max_pages;
+  int64_t N;
+};
+
+// d / 8 lanes move one key: 16 bytes of the value each, then the code words.
+// Consecutive groups take consecutive tokens of one KV head, whose rows are
+// neighbours in a page.
+__global__ void __launch_bounds__(THREADS) store_kernel(const Params p) {
+  const int lanes = p.pool.d / 8;
+  const int per_block = THREADS / lanes;
+  const int g = threadIdx.x / lanes, lane = threadIdx.x - g * lanes;
+  const int h = blockIdx.y;
+  const int64_t r = (int64_t)blockIdx.x * per_block + g;
+  if (r >= p.N) return;
+  // the sequence of row r: the last b with cu[b] <= r
+  if (r < __ldg(p.cu) || r >= __ldg(p.cu + p.B)) return;  // a row of no sequence
+  int lo = 0, hi = p.B;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (__ldg(p.cu + mid) <= r) lo = mid; else hi = mid;
+  }
+  const int64_t pos = (int64_t)__ldg(p.lens + lo) + (r - __ldg(p.cu + lo));
+  const int page = table_page(p.table, p.max_pages, lo, pos, p.pool);
+  if (page < 0) return;
+  const int64_t dst = pool_row(p.pool, page, h, (int)(pos % p.pool.P));
+  const int64_t src = r * p.pool.Hkv + h;
+  const uint4 v = *reinterpret_cast<const uint4 *>(p.V + r * p.v_tok + h * p.v_head + 8 * lane);
+  copy_code(p.pool, dst, p.codes + src * p.pool.W, p.norms + src * p.pool.c, lane, lanes);
+  *reinterpret_cast<uint4 *>(p.pool.values + dst * p.pool.d + 8 * lane) = v;
+}
+
+}  // namespace store
+
+cudaError_t launch_store_paged(const StoreArgs &a, cudaStream_t stream) {
+  store::Params p{};
+  p.pool = {a.code_pages, a.norm_pages, a.value_pages, a.num_pages, a.page_tokens,
+            a.Hkv, a.words, a.norms_per_key, a.d, device_error_ptr()};
+  if (!p.pool.err) return cudaErrorInvalidSymbol;
+  p.codes = a.codes; p.norms = a.norms; p.V = a.V;
+  p.v_tok = a.v_tok; p.v_head = a.v_head;
+  p.cu = a.cu_seqlens; p.table = a.block_table; p.lens = a.seq_lens;
+  p.B = a.B; p.max_pages = a.max_pages; p.N = a.N;
+  const int per_block = store::THREADS / (a.d / 8);
+  const dim3 grid((unsigned)((a.N + per_block - 1) / per_block), a.Hkv);
+  store::store_kernel<<<grid, store::THREADS, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
+// ---------------------------------------------------------------------------
+// accumulated attention weight
+
+namespace mass {
+
+constexpr int THREADS = 256, WARPS = THREADS / 32;
+
+struct Params {
+  const float *scores;  // [B][Hq][T]
+  const float *mass;    // [B][Hkv][T] (not read when decay is 0)
+  float *out;
+  const int32_t *lens;
+  int Hq, Hkv, G;
+  int64_t T;
+  float k, decay;  // k: softmax_scale * log2(e)
+  int *err;
+};
+
+struct MS {
+  float m, l;
+};
+// joins two softmax states; a state without keys is (-inf, 0)
+__device__ __forceinline__ MS join(MS a, MS b) {
+  const float m = fmaxf(a.m, b.m);
+  if (m == -INFINITY) return {m, 0.f};
+  return {m, a.l * exp2f(a.m - m) + b.l * exp2f(b.m - m)};
+}
+
+// One cluster per (sequence, KV head); its blocks split the keys.  Pass one
+// reads the scores of the group's heads for their softmax states, which the
+// blocks exchange through distributed shared memory; pass two reads the
+// scores again (from L2: a block's share is a few tens of KB) and writes the
+// weights.
+template <int VEC>
+__global__ void __launch_bounds__(THREADS) mass_kernel(const Params p) {
+  extern __shared__ MS ms_smem[];            // [G][WARPS], then [G] of the block
+  MS *part = ms_smem, *mine = ms_smem + p.G * WARPS, *all = mine + p.G;
+  cg::cluster_group cl = cg::this_cluster();
+  const int nb = (int)cl.num_blocks(), rank = (int)cl.block_rank();
+  const int unit = blockIdx.x / nb, b = unit / p.Hkv, h = unit - b * p.Hkv;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int64_t L = __ldg(p.lens + b);
+  if (L < 0 || L > p.T) {
+    if (threadIdx.x == 0) record_device_error(p.err, DERR_DECODE_PLAN);
+    L = L < 0 ? 0 : p.T;
+  }
+  int64_t share = (L + nb - 1) / nb;
+  share = (share + VEC - 1) / VEC * VEC;
+  const int64_t t0 = rank * share < L ? rank * share : L;
+  const int64_t t1 = t0 + share < L ? t0 + share : L;
+  const float *s0 = p.scores + ((int64_t)b * p.Hq + (int64_t)h * p.G) * p.T;
+
+  for (int g = 0; g < p.G; ++g) {
+    const float *s = s0 + (int64_t)g * p.T;
+    MS a{-INFINITY, 0.f};
+    for (int64_t t = t0 + (int64_t)threadIdx.x * VEC; t < t1; t += THREADS * VEC) {
+      float x[VEC];
+      if constexpr (VEC == 4) {
+        const float4 v = *reinterpret_cast<const float4 *>(s + t);
+        x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+      } else {
+        x[0] = s[t];
+      }
+      float m = a.m;
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        x[e] = t + e < t1 ? x[e] * p.k : -INFINITY;
+        m = fmaxf(m, x[e]);
+      }
+      if (m > -INFINITY) {
+        float l = a.l * exp2f(a.m - m);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) l += exp2f(x[e] - m);
+        a = {m, l};
+      }
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+      a = join(a, {__shfl_xor_sync(~0u, a.m, o), __shfl_xor_sync(~0u, a.l, o)});
+    if (lane == 0) part[g * WARPS + warp] = a;
+  }
+  __syncthreads();
+  for (int g = threadIdx.x; g < p.G; g += THREADS) {
+    MS a = part[g * WARPS];
+    for (int w = 1; w < WARPS; ++w) a = join(a, part[g * WARPS + w]);
+    mine[g] = a;
+  }
+  cl.sync();
+  for (int g = threadIdx.x; g < p.G; g += THREADS) {
+    MS a{-INFINITY, 0.f};
+    for (int r = 0; r < nb; ++r) a = join(a, cl.map_shared_rank(mine, r)[g]);
+    // weight = 2^(x - m) / l; a head whose keys are all -inf adds nothing
+    all[g] = a.m == -INFINITY ? MS{0.f, 0.f} : MS{a.m, 1.f / a.l};
+  }
+  cl.sync();  // also: no block leaves while another reads its states
+  const int64_t row = ((int64_t)b * p.Hkv + h) * p.T;
+  for (int64_t t = t0 + (int64_t)threadIdx.x * VEC; t < t1; t += THREADS * VEC) {
+    float w[VEC] = {};
+    for (int g = 0; g < p.G; ++g) {
+      const float *s = s0 + (int64_t)g * p.T + t;
+      const MS a = all[g];
+      if constexpr (VEC == 4) {
+        const float4 v = *reinterpret_cast<const float4 *>(s);
+        w[0] += a.l == 0.f ? 0.f : exp2f(fmaf(v.x, p.k, -a.m)) * a.l;
+        w[1] += a.l == 0.f ? 0.f : exp2f(fmaf(v.y, p.k, -a.m)) * a.l;
+        w[2] += a.l == 0.f ? 0.f : exp2f(fmaf(v.z, p.k, -a.m)) * a.l;
+        w[3] += a.l == 0.f ? 0.f : exp2f(fmaf(v.w, p.k, -a.m)) * a.l;
+      } else {
+        w[0] += a.l == 0.f ? 0.f : exp2f(fmaf(s[0], p.k, -a.m)) * a.l;
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < VEC; ++e)
+      if (t + e < t1)
+        p.out[row + t + e] = p.decay == 0.f ? w[e] : fmaf(p.decay, p.mass[row + t + e], w[e]);
+  }
+}
+
+}  // namespace mass
+
+namespace {
+template <typename K, typename P>
+cudaError_t launch_cluster(K kernel, int64_t blocks, int cluster, int threads, size_t smem,
+                           cudaStream_t stream, const P &p) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)blocks);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cluster;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+}  // namespace
+
+cudaError_t launch_accumulate(const AccumulateArgs &a, cudaStream_t stream) {
+  mass::Params p{};
+  p.scores = a.scores; p.mass = a.mass; p.out = a.out; p.lens = a.seq_lens;
+  p.Hq = a.Hq; p.Hkv = a.Hkv; p.G = a.Hq / a.Hkv; p.T = a.max_len;
+  p.k = a.softmax_scale * 1.44269504088896340736f;
+  p.decay = a.decay;
+  p.err = device_error_ptr();
+  if (!p.err) return cudaErrorInvalidSymbol;
+  const int64_t units = (int64_t)a.B * a.Hkv;
+  // blocks per (sequence, KV head): as many as keep 1024 keys each, up to the
+  // portable cluster size
+  int cluster = 1;
+  while (cluster < 8 && a.max_len / (2 * cluster) >= 1024) cluster *= 2;
+  const size_t smem = (size_t)p.G * (mass::WARPS + 2) * sizeof(mass::MS);  // <= 40 KB: G <= 512
+  auto al = [](const void *q) { return (reinterpret_cast<uintptr_t>(q) & 15) == 0; };
+  const bool vec = a.max_len % 4 == 0 && al(a.scores);
+  return vec ? launch_cluster(mass::mass_kernel<4>, units * cluster, cluster, mass::THREADS, smem,
+                              stream, p)
+             : launch_cluster(mass::mass_kernel<1>, units * cluster, cluster, mass::THREADS, smem,
+                              stream, p);
+}
+
+// ---------------------------------------------------------------------------
+// eviction
+
+namespace evict {
+
+constexpr int THREADS = 1024, WARPS = THREADS / 32;
+constexpr int BINS = 256;
+constexpr int COPY_THREADS = 256;
+
+struct Params {
+  Pools pool;
+  const float *mass;  // [B][Hkv][T]
+  const int32_t *lens, *src_table, *dst_table;
+  int src_pages, dst_pages, B;
+  int64_t T;
+  int keep, recent, sink, cached;  // cached: the block's sort keys fit in shared memory
+  int32_t *out_index, *out_lens;
+  float *out_mass;
+};
+
+// Sort key: larger mass, larger key.  -0 equals +0; a NaN ranks below all.
+__device__ __forceinline__ uint32_t sort_key(float x) {
+  if (isnan(x)) return 0u;
+  const uint32_t u = __float_as_uint(x + 0.f);
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+
+__device__ __forceinline__ int64_t sequence_length(const Params &p, int b) {
+  int64_t L = __ldg(p.lens + b);
+  if (L < 0 || L > p.T) {
+    if (threadIdx.x == 0) record_device_error(p.pool.err, DERR_DECODE_PLAN);
+    L = L < 0 ? 0 : p.T;
+  }
+  return L;
+}
+
+// Exclusive prefix of a pair of counts over the block; totals in (ta, tb).
+__device__ __forceinline__ void block_scan(int &a, int &b, int &ta, int &tb, int2 *sh) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int ia = a, ib = b;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int xa = __shfl_up_sync(~0u, ia, o), xb = __shfl_up_sync(~0u, ib, o);
+    if (lane >= o) { ia += xa; ib += xb; }
+  }
+  if (lane == 31) sh[warp] = make_int2(ia, ib);
+  __syncthreads();
+  if (warp == 0) {
+    int2 v = sh[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int xa = __shfl_up_sync(~0u, v.x, o), xb = __shfl_up_sync(~0u, v.y, o);
+      if (lane >= o) { v.x += xa; v.y += xb; }
+    }
+    sh[lane] = v;
+  }
+  __syncthreads();
+  const int2 before = warp ? sh[warp - 1] : make_int2(0, 0), tot = sh[WARPS - 1];
+  a = before.x + ia - a;
+  b = before.y + ib - b;
+  ta = tot.x;
+  tb = tot.y;
+  __syncthreads();
+}
+
+// Which keys stay.  A cluster per (sequence, KV head), whose blocks own
+// neighbouring ranges of keys.  The `need` largest masses of the candidates
+// (all but the first `sink` and the last `recent`) are those above the
+// threshold key found 8 bits at a time from histograms summed over the
+// cluster, and the first ones of those equal to it; a prefix sum over the
+// blocks then numbers the kept keys in order.
+__global__ void __launch_bounds__(THREADS) select_kernel(const Params p) {
+  extern __shared__ uint32_t cache[];  // the block's sort keys, if they fit
+  __shared__ uint32_t hist[BINS], sum[BINS];
+  __shared__ int2 scan[WARPS];
+  __shared__ int2 counts;              // of this block: kept for sure, equal to the threshold
+  __shared__ uint32_t s_digit;
+  __shared__ int s_above;
+  cg::cluster_group cl = cg::this_cluster();
+  const int nb = (int)cl.num_blocks(), rank = (int)cl.block_rank();
+  const int unit = blockIdx.x / nb, b = unit / p.pool.Hkv, h = unit - b * p.pool.Hkv;
+  const int64_t L = sequence_length(p, b);
+  const int64_t keep = L < p.keep ? L : p.keep;
+  const float *m = p.mass + (int64_t)unit * p.T;
+  int32_t *idx = p.out_index + (int64_t)unit * p.keep;
+  float *om = p.out_mass + (int64_t)unit * p.keep;
+  if (rank == 0 && h == 0 && threadIdx.x == 0) p.out_lens[b] = (int32_t)keep;
+  const int64_t stride = (int64_t)nb * THREADS, me = (int64_t)rank * THREADS + threadIdx.x;
+  for (int64_t j = keep + me; j < p.keep; j += stride) {
+    idx[j] = -1;
+    om[j] = 0.f;
+  }
+  if (L <= p.keep) {  // every key stays (the same for the whole cluster)
+    for (int64_t j = me; j < L; j += stride) {
+      idx[j] = (int32_t)j;
+      om[j] = m[j];
+    }
+    return;
+  }
+  const int64_t share = (L + nb - 1) / nb;
+  const int64_t t0 = rank * share < L ? rank * share : L;
+  const int64_t t1 = t0 + share < L ? t0 + share : L;
+  const int64_t c0 = p.sink, c1 = L - p.recent;  // candidates [c0, c1)
+  if (p.cached) {
+    for (int64_t t = t0 + threadIdx.x; t < t1; t += THREADS) cache[t - t0] = sort_key(m[t]);
+    __syncthreads();
+  }
+  auto key = [&](int64_t t) { return p.cached ? cache[t - t0] : sort_key(m[t]); };
+
+  int need = (int)(keep - p.sink - p.recent);    // of the candidates; may be 0
+  uint32_t prefix = 0, mask = 0;                 // threshold digits found so far
+  for (int shift = 24; shift >= 0; shift -= 8) {
+    for (int i = threadIdx.x; i < BINS; i += THREADS) hist[i] = 0;
+    __syncthreads();
+    const int64_t a = t0 > c0 ? t0 : c0, z = t1 < c1 ? t1 : c1;
+    for (int64_t t = a + threadIdx.x; t < z; t += THREADS) {
+      const uint32_t k = key(t);
+      if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & 255u], 1u);
+    }
+    cl.sync();
+    for (int i = threadIdx.x; i < BINS; i += THREADS) {
+      uint32_t v = 0;
+      for (int r = 0; r < nb; ++r) v += cl.map_shared_rank(hist, r)[i];
+      sum[i] = v;
+    }
+    cl.sync();  // every block has read the histograms; sum is complete
+    if (threadIdx.x < 32) {
+      // the digit where the count from above first reaches need: lane i
+      // holds bins 255 - 8 i downwards
+      uint32_t v[8], tot = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) tot += v[e] = sum[255 - (8 * threadIdx.x + e)];
+      uint32_t inc = tot;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t x = __shfl_up_sync(~0u, inc, o);
+        if ((int)threadIdx.x >= o) inc += x;
+      }
+      uint32_t above = inc - tot;
+      const bool here = above < (uint32_t)need && inc >= (uint32_t)need;
+      if (here) {
+        int e = 0;
+        while (above + v[e] < (uint32_t)need) above += v[e++];
+        s_digit = 255 - (8 * threadIdx.x + e);
+        s_above = (int)above;
+      }
+      if (need == 0 && threadIdx.x == 0) {
+        s_digit = 255;  // nothing is above the threshold, none of the equal is taken
+        s_above = 0;
+      }
+    }
+    __syncthreads();
+    need -= s_above;
+    prefix |= s_digit << shift;
+    mask |= 255u << shift;
+    __syncthreads();
+  }
+  const uint32_t tau = prefix;  // keys above it stay, and the first `need` equal to it
+
+  // how many of the block's keys stay for sure, and how many equal tau
+  auto classify = [&](int64_t t, int &sure, int &tie) {
+    sure = tie = 0;
+    if (t >= t1) return;
+    if (t < c0 || t >= c1) {
+      sure = 1;
+    } else {
+      const uint32_t k = key(t);
+      sure = k > tau;
+      tie = k == tau;
+    }
+  };
+  int na = 0, nt = 0, ta, tb;
+  for (int64_t t = t0 + threadIdx.x; t < t1; t += THREADS) {
+    int s, e;
+    classify(t, s, e);
+    na += s;
+    nt += e;
+  }
+  block_scan(na, nt, ta, tb, scan);
+  if (threadIdx.x == 0) counts = make_int2(ta, tb);
+  cl.sync();
+  int sure0 = 0, tie0 = 0;
+  for (int r = 0; r < rank; ++r) {
+    const int2 v = *cl.map_shared_rank(&counts, r);
+    sure0 += v.x;
+    tie0 += v.y;
+  }
+  cl.sync();  // no block leaves while another reads its counts
+  for (int64_t base = t0; base < t1; base += THREADS) {
+    const int64_t t = base + threadIdx.x;
+    int s, e;
+    classify(t, s, e);
+    int ps = s, pe = e;
+    block_scan(ps, pe, ta, tb, scan);
+    const int ties = tie0 + pe;  // equal keys before this one
+    if (s || (e && ties < need)) {
+      const int64_t j = (int64_t)sure0 + ps + (ties < need ? ties : need);
+      idx[j] = (int32_t)t;
+      om[j] = m[t];
+    }
+    sure0 += ta;
+    tie0 += tb;
+  }
+}
+
+// Moves the kept keys: d / 8 lanes per key, neighbouring groups to
+// neighbouring slots of the new pages.
+__global__ void __launch_bounds__(COPY_THREADS) move_kernel(const Params p) {
+  griddep_wait();
+  const int lanes = p.pool.d / 8, per_block = COPY_THREADS / lanes;
+  const int g = threadIdx.x / lanes, lane = threadIdx.x - g * lanes;
+  const int tiles = (p.keep + per_block - 1) / per_block;
+  const int unit = blockIdx.x / tiles, b = unit / p.pool.Hkv, h = unit - b * p.pool.Hkv;
+  const int64_t j = (int64_t)(blockIdx.x - unit * tiles) * per_block + g;
+  if (j >= p.keep) return;
+  const int t = p.out_index[(int64_t)unit * p.keep + j];
+  if (t < 0) return;
+  const int sp = table_page(p.src_table, p.src_pages, b, t, p.pool);
+  const int dp = table_page(p.dst_table, p.dst_pages, b, j, p.pool);
+  if (sp < 0 || dp < 0) return;
+  const int64_t src = pool_row(p.pool, sp, h, t % p.pool.P);
+  const int64_t dst = pool_row(p.pool, dp, h, (int)(j % p.pool.P));
+  const uint4 v =
+      *reinterpret_cast<const uint4 *>(p.pool.values + src * p.pool.d + 8 * lane);
+  copy_code(p.pool, dst, p.pool.codes + src * p.pool.W, p.pool.norms + src * p.pool.c, lane,
+            lanes);
+  *reinterpret_cast<uint4 *>(p.pool.values + dst * p.pool.d + 8 * lane) = v;
+}
+
+}  // namespace evict
+
+cudaError_t launch_evict_paged(const EvictArgs &a, cudaStream_t stream) {
+  evict::Params p{};
+  p.pool = {a.code_pages, a.norm_pages, a.value_pages, a.num_pages, a.page_tokens,
+            a.Hkv, a.words, a.norms_per_key, a.d, device_error_ptr()};
+  if (!p.pool.err) return cudaErrorInvalidSymbol;
+  p.mass = a.mass; p.lens = a.seq_lens; p.src_table = a.src_table; p.dst_table = a.dst_table;
+  p.src_pages = a.src_max_pages; p.dst_pages = a.dst_max_pages; p.B = a.B; p.T = a.max_len;
+  p.keep = a.keep; p.recent = a.recent; p.sink = a.sink;
+  p.out_index = a.out_index; p.out_mass = a.out_mass; p.out_lens = a.out_lens;
+  int cluster = 1;
+  while (cluster < 8 && a.max_len / (2 * cluster) >= evict::THREADS) cluster *= 2;
+  const int64_t share = (a.max_len + cluster - 1) / cluster;
+  // 192 KB of sort keys at most: with the block's static shared memory that
+  // stays inside the 227 KB a block may have
+  p.cached = share * 4 <= 192 * 1024;
+  const size_t smem = p.cached ? (size_t)share * 4 : 0;
+  cudaError_t e = cudaSuccess;
+  if (smem > 40 * 1024)  // beyond what a block gets without asking
+    e = cudaFuncSetAttribute(evict::select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             192 * 1024);
+  if (e != cudaSuccess) return e;
+  e = launch_cluster(evict::select_kernel, (int64_t)a.B * a.Hkv * cluster, cluster,
+                     evict::THREADS, smem, stream, p);
+  if (e != cudaSuccess) return e;
+  const int per_block = evict::COPY_THREADS / (a.d / 8);
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)((a.keep + per_block - 1) / per_block * a.B * a.Hkv));
+  cfg.blockDim = dim3(evict::COPY_THREADS);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, evict::move_kernel, p);
+}
+
+}  // namespace jlk

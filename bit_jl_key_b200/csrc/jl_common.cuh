@@ -30,6 +30,7 @@ enum DeviceErr : int {
   DERR_TC_TMEM_ALLOC = 2,                          // tensor-core kernel: TMEM allocation failed
   DERR_DECODE_PLAN = JL_DERR_DECODE_PLAN,          // decode: inconsistent work split
   DERR_DECODE_WAIT_TIMEOUT = JL_DERR_DECODE_WAIT_TIMEOUT,  // decode: a copy wait ran out
+  DERR_PAGE = JL_DERR_PAGE,     // a block-table entry outside the pool or the table
   DERR_INDEX = JL_DERR_INDEX,   // debug builds: an index left its buffer's extent
 };
 

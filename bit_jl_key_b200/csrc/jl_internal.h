@@ -158,4 +158,54 @@ cudaError_t launch_turbo_decode_paged(const DecodePlan &p, int bits, const Paged
 // The codebook's centroid magnitudes and positive boundaries (float).
 bool turbo_magnitudes(int d, int bits, float *mag, float *pos_thr);
 
+// Rotary positions (rotary.cu); strides in elements, k null for queries alone.
+struct RotaryArgs {
+  const void *q, *k;
+  void *out_q, *out_k;
+  int64_t q_tok, q_head, k_tok, k_head, out_q_tok, out_q_head, out_k_tok, out_k_head;
+  bool f32, interleaved, inverse;
+  int64_t n;
+  int Hq, Hkv, d, rot;
+  const int32_t *positions;
+  const float *inv_freq;
+  float scale;
+};
+cudaError_t launch_rotary(const RotaryArgs &a, cudaStream_t stream);
+
+// Cache operators of the serving loop (cache_ops.cu).
+struct StoreArgs {
+  const uint32_t *codes;
+  const uint16_t *norms, *V;
+  int64_t v_tok, v_head, N;
+  int Hkv, words, norms_per_key, d, B;
+  const int32_t *cu_seqlens, *block_table, *seq_lens;
+  uint32_t *code_pages;
+  uint16_t *norm_pages, *value_pages;
+  int num_pages, page_tokens, max_pages;
+};
+cudaError_t launch_store_paged(const StoreArgs &a, cudaStream_t stream);
+
+struct AccumulateArgs {
+  const float *scores, *mass;
+  const int32_t *seq_lens;
+  int B, Hq, Hkv;
+  int64_t max_len;
+  float softmax_scale, decay;
+  float *out;
+};
+cudaError_t launch_accumulate(const AccumulateArgs &a, cudaStream_t stream);
+
+struct EvictArgs {
+  const float *mass;
+  const int32_t *seq_lens, *src_table, *dst_table;
+  int B, Hkv, keep, recent, sink, words, norms_per_key, d;
+  int64_t max_len;
+  uint32_t *code_pages;
+  uint16_t *norm_pages, *value_pages;
+  int num_pages, page_tokens, src_max_pages, dst_max_pages;
+  int32_t *out_index, *out_lens;
+  float *out_mass;
+};
+cudaError_t launch_evict_paged(const EvictArgs &a, cudaStream_t stream);
+
 }  // namespace jlk

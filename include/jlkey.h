@@ -563,6 +563,158 @@ JL_API int jl_turbo_dequantize_keys(const uint32_t *codes, const uint16_t *norms
                                     int64_t n_keys, const uint16_t *basis, int m, int d,
                                     int mse_bits, uint16_t *out, jl_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * The serving loop around a paged compressed cache: rotary positions ahead of
+ * the quantizer, a chunk of coded keys into the pages, attention of a chunk
+ * over them, the attention weight each key received, and eviction of the keys
+ * that received the least.  The pages treat none of these; they are the
+ * operators of a decoder that feeds and reads such a cache.
+ * -------------------------------------------------------------------------*/
+
+/* How jl_rotary_frequencies stretches the frequencies for long contexts. */
+typedef enum {
+    JL_ROPE_PLAIN = 0,
+    JL_ROPE_LINEAR = 1, /* all divided by `factor` */
+    JL_ROPE_NTK = 2,    /* base raised to base * factor^(r / (r - 2)), which divides the
+                           lowest frequency by `factor` and leaves the highest */
+    JL_ROPE_BANDED = 3  /* by their turns in `original_len` positions: more than `high`,
+                           left; fewer than `low`, divided; blended linearly between */
+} jl_rope_scaling;
+
+/*
+ * jl_rotary_frequencies -- inv_freq[j] = base^(-2j / rot_dim), j < rot_dim / 2,
+ * scaled as `scaling` says; computed in float64 and rounded to float.
+ *   inv_freq : out, HOST memory, rot_dim / 2 floats.
+ *   factor   : > 0 (read unless JL_ROPE_PLAIN); original_len > 0 and
+ *              high > low (read for JL_ROPE_BANDED alone).
+ * Errors: JL_ERR_INVALID_ARG (null, rot_dim odd or outside [2, 1024], base not
+ * above 1, a parameter out of its range).
+ */
+JL_API int jl_rotary_frequencies(int rot_dim, double base, jl_rope_scaling scaling,
+                                 double factor, int64_t original_len, double low,
+                                 double high, float *inv_freq);
+
+/*
+ * jl_rotary -- rotary positions of n tokens' queries and keys: pair j of each
+ * head turns by the angle a = positions[token] * inv_freq[j],
+ *     (x, y) -> scale * (x cos a - y sin a, x sin a + y cos a),
+ * and the entries from rot_dim on are copied.  With `inverse` the angle is
+ * -a, which undoes the rotation and is its gradient (both times scale).
+ *   Q, K      : in, device, n x Hq x d and n x Hkv x d of `dtype`, token t and
+ *               head h at element t * tok_stride + h * head_stride, d entries
+ *               contiguous; K may be NULL (then Hkv, its strides and out_k are
+ *               not read).  Aligned to their element.
+ *   rot_dim   : even, 2 .. d; d even, at most 1024.
+ *   positions : in, device, n int32 (any value; a shared position is no error).
+ *   inv_freq  : in, device, rot_dim / 2 floats.
+ *   interleaved : 0: pair j is entries (j, j + rot_dim/2); 1: (2j, 2j + 1).
+ *   scale     : finite factor of the rotated entries (1 for a pure rotation).
+ *   out_q, out_k : out, same shapes, each its own strides; no two of their
+ *               entries may share an address.  out may be the input itself with
+ *               the same strides (in place); any other overlap is an error of
+ *               the caller.
+ * Angles are formed and reduced in float64; the rotation is fp32, rounded to
+ * nearest.  n == 0 is a no-op.  Errors: JL_ERR_INVALID_ARG (null or misaligned
+ * pointer, bad size or stride, scale not finite), JL_ERR_UNSUPPORTED (d, n
+ * above 2^31 - 1), JL_ERR_CUDA.
+ */
+JL_API int jl_rotary(const void *Q, const void *K, jl_dtype dtype, int64_t n, int Hq, int Hkv,
+                     int d, int rot_dim, int64_t q_tok_stride, int64_t q_head_stride,
+                     int64_t k_tok_stride, int64_t k_head_stride, const int32_t *positions,
+                     const float *inv_freq, int interleaved, int inverse, float scale,
+                     void *out_q, int64_t out_q_tok_stride, int64_t out_q_head_stride,
+                     void *out_k, int64_t out_k_tok_stride, int64_t out_k_head_stride,
+                     jl_stream_t stream);
+
+/*
+ * jl_store_paged -- a ragged chunk of coded keys and their values into a paged
+ * cache: row i of sequence b (row cu_seqlens[b] + i of the chunk) becomes key
+ * seq_lens[b] + i, in page block_table[b][t / page_tokens], slot
+ * t % page_tokens.  Serves QJL and TurboQuant-prod codes alike: what
+ * jl_quantize_keys or jl_turbo_quantize_keys wrote for the chunk's keys is
+ * moved bit for bit.
+ *   codes      : in, N x Hkv x words uint32, 4-byte aligned.
+ *   norms      : in, N x Hkv x norms_per_key binary16 (1: QJL, 2: TurboQuant).
+ *   V          : in, N x Hkv x d bf16, token and head strides in elements,
+ *                16-byte aligned base and strides.
+ *   cu_seqlens : in, device, B + 1 int32, nondecreasing: sequence b's rows are
+ *                [cu_seqlens[b], cu_seqlens[b + 1]).  Rows outside
+ *                [cu_seqlens[0], cu_seqlens[B]) are a batch's padding: skipped.
+ *   code_pages, norm_pages, value_pages, num_pages, page_tokens, block_table,
+ *   max_pages : the cache, as in jl_decode_attention_paged.
+ *   seq_lens   : in, device, B int32: keys cached before the call.  Not
+ *                modified (the caller advances it).
+ * A key whose page the table does not give (a column past max_pages, an id
+ * outside [0, num_pages)) is skipped and JL_DERR_PAGE recorded.  N == 0 or
+ * B == 0 is a no-op.  Errors: JL_ERR_INVALID_ARG, JL_ERR_UNSUPPORTED (d not 64
+ * or 128, words outside [1, 64], norms_per_key not 1 or 2), JL_ERR_CUDA.
+ */
+JL_API int jl_store_paged(const uint32_t *codes, const uint16_t *norms, const uint16_t *V,
+                          int64_t v_tok_stride, int64_t v_head_stride, int64_t N, int Hkv,
+                          int words, int norms_per_key, int d, const int32_t *cu_seqlens, int B,
+                          uint32_t *code_pages, uint16_t *norm_pages, uint16_t *value_pages,
+                          int num_pages, int page_tokens, const int32_t *block_table,
+                          int max_pages, const int32_t *seq_lens, jl_stream_t stream);
+
+/*
+ * jl_accumulate_attention -- adds the attention weight that each cached key
+ * received in a step to a running total, the measure by which
+ * jl_evict_paged chooses:
+ *     out[b][kv][t] = decay * mass[b][kv][t]
+ *                     + sum over the KV head's query heads h of
+ *                       softmax over t < seq_lens[b] of (softmax_scale * scores[b][h][t]).
+ *   scores   : in, B x Hq x max_len fp32, the `scores` that the decode entry
+ *              points return; query head h reads KV head h / (Hq / Hkv).
+ *   mass     : in, B x Hkv x max_len fp32 (not read when decay is 0, and may
+ *              then be NULL).
+ *   out      : out, B x Hkv x max_len fp32; may be `mass` itself.  Entries from
+ *              seq_lens[b] on are left as they were.
+ *   seq_lens : in, device, B int32; a length outside [0, max_len] records
+ *              JL_DERR_DECODE_PLAN and is clipped.
+ * A head whose scores are all -inf adds nothing.  Statistics and sums are
+ * fp32.  B == 0 is a no-op.  Errors: JL_ERR_INVALID_ARG, JL_ERR_UNSUPPORTED
+ * (more than 512 query heads per KV head, B * Hkv >= 2^24), JL_ERR_CUDA.
+ */
+JL_API int jl_accumulate_attention(const float *scores, const float *mass,
+                                   const int32_t *seq_lens, int B, int Hq, int Hkv,
+                                   int64_t max_len, float softmax_scale, float decay, float *out,
+                                   jl_stream_t stream);
+
+/*
+ * jl_evict_paged -- shrinks a paged cache to at most `keep` keys per sequence.
+ * Of the L = seq_lens[b] keys of each (sequence, KV head) it keeps, when
+ * L > keep, the first `sink`, the last `recent`, and of the others the
+ * keep - sink - recent with the largest mass (equal masses: the lower index;
+ * a NaN counts below everything); when L <= keep, all.  They are copied, in
+ * their order, to the pages that dst_table names, as keys 0 .. L' - 1 with
+ * L' = min(L, keep).  Each KV head keeps keys of its own, so index t of
+ * different heads may stand for different tokens afterwards; keys carry their
+ * positions in their codes (rotary positions are applied before coding).
+ *   mass       : in, B x Hkv x max_len fp32.
+ *   seq_lens   : in, device, B int32; a length outside [0, max_len] records
+ *                JL_DERR_DECODE_PLAN and is clipped.
+ *   keep       : >= 1; recent, sink >= 0 with recent + sink <= keep.
+ *   pools, words, norms_per_key : as in jl_store_paged.
+ *   src_table  : in, B x src_max_pages: the pages that hold the keys.
+ *   dst_table  : in, B x dst_max_pages, dst_max_pages * page_tokens >= keep:
+ *                pages of the same pools that hold none of the call's keys.
+ *   out_index  : out, B x Hkv x keep int32: the old index of each kept key,
+ *                ascending, then -1.
+ *   out_mass   : out, B x Hkv x keep fp32: the kept keys' mass, then 0.  Not
+ *                `mass` itself.
+ *   out_lens   : out, B int32: L'.
+ * A key with a page outside the pool, at either end, is not moved and
+ * JL_DERR_PAGE recorded.  B == 0 is a no-op.  Errors: JL_ERR_INVALID_ARG,
+ * JL_ERR_UNSUPPORTED (as jl_store_paged; max_len >= 2^31), JL_ERR_CUDA.
+ */
+JL_API int jl_evict_paged(const float *mass, const int32_t *seq_lens, int B, int Hkv,
+                          int64_t max_len, int keep, int recent, int sink, int words,
+                          int norms_per_key, int d, uint32_t *code_pages, uint16_t *norm_pages,
+                          uint16_t *value_pages, int num_pages, int page_tokens,
+                          const int32_t *src_table, int src_max_pages, const int32_t *dst_table,
+                          int dst_max_pages, int32_t *out_index, float *out_mass,
+                          int32_t *out_lens, jl_stream_t stream);
+
 /*
  * jl_device_error -- synchronise `stream`, then read and clear the device
  * error word of the current device (0 = no fault reported).  *code receives
@@ -570,12 +722,15 @@ JL_API int jl_turbo_dequantize_keys(const uint32_t *codes, const uint16_t *norms
  * JL_ERR_CUDA.  Codes: JL_DERR_TC_WAIT_TIMEOUT (a tensor-core kernel's
  * pipeline wait ran out), JL_DERR_DECODE_PLAN (a decode work split or a
  * paged length did not fit), JL_DERR_DECODE_WAIT_TIMEOUT (a decode copy wait
- * ran out), JL_DERR_INDEX (see below).
+ * ran out), JL_DERR_INDEX (see below), JL_DERR_PAGE (a block-table entry
+ * that a call needed lies outside the pool or past the table's last column;
+ * the keys of that page were skipped).
  */
 enum {
     JL_DERR_TC_WAIT_TIMEOUT = 1,
     JL_DERR_DECODE_PLAN = 3,
     JL_DERR_DECODE_WAIT_TIMEOUT = 4,
+    JL_DERR_PAGE = 6,
     JL_DERR_INDEX = 5 /* index-checking debug build only: a kernel computed an
                          index outside the extent the call's shapes give a
                          buffer, and skipped that access */
