@@ -21,6 +21,8 @@ Functions (same names as the C entry points):
   jl_rotary_frequencies(rot_dim, base, scaling, ...) -> inv_freq (fp32 [rot_dim/2])
   jl_rotary(Q, positions, inv_freq, K=None, ...) -> out_q, or (out_q, out_k)
   jl_store_paged(codes, norms, V, cu_seqlens, pools, block_table, seq_lens)
+  jl_chunk_attention_paged(Q, S, pools, block_table, seq_lens, cu_seqlens, max_len)
+      -> out bf16 [N, Hq, d]
   jl_accumulate_attention(scores, mass, seq_lens, softmax_scale, decay) -> mass
   jl_evict_paged(mass, seq_lens, keep, pools, src_table, dst_table, ...)
       -> (index, mass, lens)
@@ -66,7 +68,7 @@ EXPORTED = ("jl_status_string", "jl_sketch_init", "jl_quantize_keys",
             "jl_turbo_dequantize_keys", "jl_test_drop_copies", "jl_build_flags",
             "jl_decode_attention_state", "jl_merge_attention_states",
             "jl_rotary_frequencies", "jl_rotary", "jl_store_paged", "jl_accumulate_attention",
-            "jl_evict_paged")
+            "jl_evict_paged", "jl_chunk_attention_workspace_bytes", "jl_chunk_attention_paged")
 
 # device error codes (jl_device_error)
 JL_DERR_TC_WAIT_TIMEOUT = 1
@@ -163,6 +165,12 @@ def load():
     L.jl_store_paged.restype = i32
     L.jl_store_paged.argtypes = [vp, vp, vp, i64, i64, i64, i32, i32, i32, i32, vp, i32, vp, vp,
                                  vp, i32, i32, vp, i32, vp, vp]
+    L.jl_chunk_attention_workspace_bytes.restype = sz
+    L.jl_chunk_attention_workspace_bytes.argtypes = [i64, i32, i32, i32, i64, i32, i32]
+    L.jl_chunk_attention_paged.restype = i32
+    L.jl_chunk_attention_paged.argtypes = [vp, i32, i64, i64, i64, vp, vp, vp, vp, i32, i32, vp,
+                                           i32, vp, vp, i32, i32, i32, i64, i32, i32, f32, vp,
+                                           vp, sz, vp]
     L.jl_accumulate_attention.restype = i32
     L.jl_accumulate_attention.argtypes = [vp, vp, vp, i32, i32, i32, i64, f32, f32, vp, vp]
     L.jl_evict_paged.restype = i32
@@ -916,6 +924,59 @@ def jl_store_paged(codes, norms, V, cu_seqlens, code_pages, norm_pages, value_pa
             _ptr(cu_seqlens), B, _ptr(code_pages), _ptr(norm_pages), _ptr(value_pages),
             num_pages, P, _ptr(block_table), block_table.shape[1], _ptr(seq_lens),
             _stream(codes, stream)), "jl_store_paged")
+
+
+def jl_chunk_attention_workspace_bytes(N, B, Hq, Hkv, max_len, m, d) -> int:
+    return int(load().jl_chunk_attention_workspace_bytes(N, B, Hq, Hkv, max_len, m, d))
+
+
+def jl_chunk_attention_paged(Q, S, sign_pages, norm_pages, value_pages, block_table, seq_lens,
+                             cu_seqlens, max_len, softmax_scale=None, out=None, workspace=None,
+                             stream=None) -> torch.Tensor:
+    """Attention of a ragged chunk of new tokens over a paged compressed cache.
+
+    Q [N, Hq, d] (bf16/fp32, any token and head strides); pools and block_table
+    as in jl_decode_attention_paged; seq_lens int32 [B]: keys cached, the
+    chunk's own included (jl_store_paged them first); cu_seqlens int32 [B + 1]:
+    sequence b's rows.  Row i of its n sees the keys t < seq_lens[b] - n + i +
+    1.  Returns out [N, Hq, d] bf16, in which rows of no sequence stay as they
+    were (undefined in a tensor made here)."""
+    if Q.dim() != 3 or S.dim() != 2 or block_table.dim() != 2:
+        raise ValueError("Q must be [N, Hq, d], S [m, d] and block_table [B, max_pages]")
+    qt = _float_code(Q, "Q")
+    N, Hq, d = Q.shape
+    m = S.shape[0]
+    num_pages, Hkv, P, words, c, dv = _pools(sign_pages, norm_pages, value_pages)
+    if c != 1 or words * 32 != m or dv != d:
+        raise ValueError(f"the pools do not hold QJL codes of S {tuple(S.shape)} and values of "
+                         f"{d}")
+    if Q.stride(2) != 1:
+        raise ValueError("queries must have unit stride along d")
+    B = seq_lens.shape[0]
+    _want(S, "S", torch.bfloat16, (m, d))
+    _want(seq_lens, "seq_lens", torch.int32, (B,))
+    _want(cu_seqlens, "cu_seqlens", torch.int32, (B + 1,))
+    _want(block_table, "block_table", torch.int32, (B, block_table.shape[1]))
+    if out is not None:
+        _want(out, "out", torch.bfloat16, (N, Hq, d))
+    if softmax_scale is None:
+        softmax_scale = 1.0 / math.sqrt(d)
+    L = load()
+    with _on(stream, Q, S, sign_pages, norm_pages, value_pages, block_table, seq_lens, cu_seqlens,
+             out, workspace):
+        if out is None:
+            out = torch.empty((N, Hq, d), dtype=torch.bfloat16, device=Q.device)
+        if workspace is None:
+            need = L.jl_chunk_attention_workspace_bytes(N, B, Hq, Hkv, max_len, m, d)
+            workspace = torch.empty((max(need, 1),), dtype=torch.uint8, device=Q.device)
+        _check(L.jl_chunk_attention_paged(
+            _ptr(Q), qt, Q.stride(0), Q.stride(1), N, _ptr(S), _ptr(sign_pages),
+            _ptr(norm_pages), _ptr(value_pages), num_pages, P, _ptr(block_table),
+            block_table.shape[1], _ptr(seq_lens), _ptr(cu_seqlens), B, Hq, Hkv, max_len, m, d,
+            softmax_scale, _ptr(out), _ptr(workspace),
+            workspace.numel() * workspace.element_size(), _stream(Q, stream)),
+            "jl_chunk_attention_paged")
+    return out
 
 
 def jl_accumulate_attention(scores, mass, seq_lens, softmax_scale: float, decay: float = 1.0,

@@ -637,6 +637,54 @@ int jl_store_paged(const uint32_t *codes, const uint16_t *norms, const uint16_t 
   return from_cuda(jlk::launch_store_paged(a, (cudaStream_t)stream));
 }
 
+size_t jl_chunk_attention_workspace_bytes(int64_t N, int B, int Hq, int Hkv, int64_t max_len,
+                                          int m, int d) {
+  if (N < 1 || B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || max_len < 1 || !supported_md(m, d))
+    return 0;
+  if (N >= ((int64_t)1 << 31) / Hq || max_len >= ((int64_t)1 << 31)) return 0;
+  return jlk::chunk_workspace_bytes(N, B, Hq, Hkv, max_len, m, d);
+}
+
+int jl_chunk_attention_paged(const void *Q, jl_dtype q_dtype, int64_t q_tok_stride,
+                             int64_t q_head_stride, int64_t N, const uint16_t *S,
+                             const uint32_t *sign_pages, const uint16_t *norm_pages,
+                             const uint16_t *value_pages, int num_pages, int page_tokens,
+                             const int32_t *block_table, int max_pages, const int32_t *seq_lens,
+                             const int32_t *cu_seqlens, int B, int Hq, int Hkv, int64_t max_len,
+                             int m, int d, float softmax_scale, uint16_t *out, void *workspace,
+                             size_t workspace_bytes, jl_stream_t stream) {
+  if (q_dtype != JL_BF16 && q_dtype != JL_F32) return JL_ERR_INVALID_ARG;
+  if (N < 0 || B < 0 || Hq < 1 || Hkv < 1 || max_len < 1 || Hq % Hkv != 0)
+    return JL_ERR_INVALID_ARG;
+  if (num_pages < 1 || max_pages < 1 || page_tokens < 32 || page_tokens % 32 != 0)
+    return JL_ERR_INVALID_ARG;
+  if ((int64_t)max_pages * page_tokens < max_len || !isfinite(softmax_scale))
+    return JL_ERR_INVALID_ARG;
+  if (!supported_md(m, d) || N >= ((int64_t)1 << 31) / Hq || max_len >= ((int64_t)1 << 31) ||
+      (int64_t)num_pages * Hkv >= ((int64_t)1 << 31) / page_tokens)
+    return JL_ERR_UNSUPPORTED;
+  if (N == 0 || B == 0) return JL_OK;
+  if (!Q || !S || !sign_pages || !norm_pages || !value_pages || !block_table || !seq_lens ||
+      !cu_seqlens || !out)
+    return JL_ERR_INVALID_ARG;
+  if (!aligned(Q, q_dtype == JL_F32 ? 4 : 2) || !aligned(S, 16) || !aligned(sign_pages, 16) ||
+      !aligned(norm_pages, 16) || !aligned(value_pages, 16) || !aligned(out, 16) ||
+      !aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(cu_seqlens, 4) ||
+      !strides_ok(N, Hq, d, q_tok_stride, q_head_stride, false))
+    return JL_ERR_INVALID_ARG;
+  if (!workspace || !aligned(workspace, 256) ||
+      workspace_bytes < jlk::chunk_workspace_bytes(N, B, Hq, Hkv, max_len, m, d))
+    return JL_ERR_WORKSPACE;
+  jlk::ChunkArgs a{};
+  a.Q = Q; a.q_f32 = q_dtype == JL_F32; a.q_tok = q_tok_stride; a.q_head = q_head_stride;
+  a.N = N; a.S = S; a.sign_pages = sign_pages; a.norm_pages = norm_pages;
+  a.value_pages = value_pages; a.num_pages = num_pages; a.page_tokens = page_tokens;
+  a.max_pages = max_pages; a.block_table = block_table; a.seq_lens = seq_lens;
+  a.cu_seqlens = cu_seqlens; a.B = B; a.Hq = Hq; a.Hkv = Hkv; a.m = m; a.d = d;
+  a.max_len = max_len; a.softmax_scale = softmax_scale; a.out = out; a.workspace = workspace;
+  return from_cuda(jlk::launch_chunk(a, (cudaStream_t)stream));
+}
+
 int jl_accumulate_attention(const float *scores, const float *mass, const int32_t *seq_lens,
                             int B, int Hq, int Hkv, int64_t max_len, float softmax_scale,
                             float decay, float *out, jl_stream_t stream) {

@@ -208,4 +208,23 @@ struct EvictArgs {
 };
 cudaError_t launch_evict_paged(const EvictArgs &a, cudaStream_t stream);
 
+// Attention of a ragged chunk over a paged cache of QJL codes (chunk_tc.cu).
+struct ChunkArgs {
+  const void *Q;
+  bool q_f32;
+  int64_t q_tok, q_head, N;
+  const uint16_t *S;
+  const uint32_t *sign_pages;
+  const uint16_t *norm_pages, *value_pages;
+  int num_pages, page_tokens, max_pages;
+  const int32_t *block_table, *seq_lens, *cu_seqlens;
+  int B, Hq, Hkv, m, d;
+  int64_t max_len;
+  float softmax_scale;
+  uint16_t *out;
+  void *workspace;
+};
+size_t chunk_workspace_bytes(int64_t N, int B, int Hq, int Hkv, int64_t max_len, int m, int d);
+cudaError_t launch_chunk(const ChunkArgs &a, cudaStream_t stream);
+
 }  // namespace jlk

@@ -657,6 +657,52 @@ JL_API int jl_store_paged(const uint32_t *codes, const uint16_t *norms, const ui
                           int max_pages, const int32_t *seq_lens, jl_stream_t stream);
 
 /*
+ * jl_chunk_attention_workspace_bytes -- device scratch that
+ * jl_chunk_attention_paged needs for these shapes (the projected queries, the
+ * work split and the states of split rows).  Depends on the shapes only;
+ * 0 for unsupported shapes and for N == 0 or B == 0.
+ */
+JL_API size_t jl_chunk_attention_workspace_bytes(int64_t N, int B, int Hq, int Hkv,
+                                                 int64_t max_len, int m, int d);
+
+/*
+ * jl_chunk_attention_paged -- attention of a ragged chunk of new tokens over a
+ * paged compressed cache: a prompt taken in pieces, or the verification of
+ * several drafted tokens.  The chunk's own keys are in the cache already
+ * (jl_store_paged); with n = cu_seqlens[b + 1] - cu_seqlens[b] rows and
+ * L = seq_lens[b] keys, row i of sequence b attends over the keys
+ * t < L - n + i + 1, with the logit of jl_decode_attention_paged, so that the
+ * call equals n decode steps.  A row that sees no key (n > L) gets zeros.
+ *   Q          : in, N x Hq x d of q_dtype, token and head strides in elements,
+ *                d entries contiguous; aligned to its element.
+ *   S, sign_pages, norm_pages, value_pages, num_pages, page_tokens,
+ *   block_table, max_pages : as in jl_decode_attention_paged (read only).
+ *   seq_lens   : in, device, B int32: keys cached, the chunk's included.
+ *   cu_seqlens : in, device, B + 1 int32, nondecreasing: sequence b's rows are
+ *                [cu_seqlens[b], cu_seqlens[b + 1]).  Rows of no sequence
+ *                (a batch's padding) leave `out` as it was.
+ *   max_len    : bound on seq_lens[b].
+ *   out        : out, N x Hq x d bf16, 16-byte aligned.
+ *   workspace  : >= jl_chunk_attention_workspace_bytes(...), 256-byte aligned.
+ * Values past a sequence's last key are never read into the result, whatever
+ * they hold; a value that some rows of the call see must be finite.  A length
+ * outside [0, max_len] is clipped and rows outside [0, N) are dropped, and
+ * JL_DERR_DECODE_PLAN recorded; where the table gives no page inside the pool
+ * JL_DERR_PAGE is recorded and the sequence's rows are undefined.  The queries'
+ * projections are rounded to binary16 under a power-of-two scale per row and
+ * the weights to bf16; sums are fp32.  N == 0 or B == 0 is a no-op.
+ * Errors: JL_ERR_INVALID_ARG, JL_ERR_UNSUPPORTED (m, d; N * Hq, the pools'
+ * rows or max_len at or above 2^31), JL_ERR_WORKSPACE, JL_ERR_CUDA.
+ */
+JL_API int jl_chunk_attention_paged(
+    const void *Q, jl_dtype q_dtype, int64_t q_tok_stride, int64_t q_head_stride, int64_t N,
+    const uint16_t *S, const uint32_t *sign_pages, const uint16_t *norm_pages,
+    const uint16_t *value_pages, int num_pages, int page_tokens, const int32_t *block_table,
+    int max_pages, const int32_t *seq_lens, const int32_t *cu_seqlens, int B, int Hq, int Hkv,
+    int64_t max_len, int m, int d, float softmax_scale, uint16_t *out, void *workspace,
+    size_t workspace_bytes, jl_stream_t stream);
+
+/*
  * jl_accumulate_attention -- adds the attention weight that each cached key
  * received in a step to a running total, the measure by which
  * jl_evict_paged chooses:
