@@ -1,0 +1,326 @@
+// chunk.cuh -- what the two chunk attention kernels share: the plan of the
+// work, the walk through a block's share of it, and the joining of split rows.
+//
+// Rows.  The query heads of a KV head share its keys, so row i * G + g of a
+// (sequence, KV head) is token i, head g.  `rows` consecutive rows make a row
+// tile, BN keys a key tile; a (row tile, key tile) pair that the row tile's
+// last token sees is a unit.  Units are counted in the order (sequence, KV
+// head, row tile, key tile) and every block takes an equal run of them, so a
+// long context with few rows is split and many rows are balanced, the causal
+// triangle included.  A row tile that lies in one block is written out by it;
+// of a split one each block leaves the softmax states (acc, max, sum), which
+// combine_kernel joins.
+#pragma once
+
+#include "jl_common.cuh"
+#include "jl_internal.h"
+
+namespace jlk {
+namespace chunk {
+
+constexpr int BN = 128;            // keys of a tile
+constexpr int GRAN = 32;           // keys that surely share a page
+constexpr float RENEW = 8.f;       // log2 growth of a row's maximum that renews it
+constexpr int PREP_THREADS = 256;
+constexpr int SM_COUNT = 148;      // bounds the workspace per shape
+
+struct Plan {
+  int64_t total;      // units (key tiles, at least one per row tile)
+  int64_t quota;      // units per block
+};
+struct Work {         // workspace
+  Plan *plan;
+  int64_t *b_unit;    // [B + 1] first unit of each sequence
+  int32_t *b_tile;    // [B] first entry of its row tiles in mt_pre
+  int32_t *start, *count, *len;  // [B] first row, tokens, keys, made safe
+  int32_t *mt_pre;    // per sequence: units before each row tile of a head, and their sum
+  uint16_t *U;        // [Hkv][N G][K] binary16 queries, scaled row by row
+  float *rs;          // [Hkv][N G] row scale: log2 units per unit of score
+  float *part;        // [2 blocks][rows][d + 2] softmax states
+  uint16_t *keys;     // [B][Hkv][tiles of max_len][BN][d] binary16 keys (many rows)
+};
+
+struct Params {
+  Work w;
+  const uint32_t *codes;
+  const uint16_t *norms;
+  const int32_t *table, *cu, *lens;
+  const void *Q;
+  int64_t q_tok, q_head;
+  const uint16_t *S;
+  uint16_t *out;
+  int B, Hq, Hkv, G, P, max_pages, num_pages, blocks, min_units, rows;
+  int key_tiles;      // of max_len
+  int64_t N, max_len;
+  float scale;        // softmax_scale
+  int *err;
+};
+
+// Units of row tile mt: key tiles that its last token sees, at least one.
+__device__ __forceinline__ int tile_units(int mt, int n, int L, int G, int rows) {
+  const int last = min(n - 1, (rows * mt + rows - 1) / G);
+  const int seen = max(0, L - n + last + 1);
+  return max(1, (seen + BN - 1) / BN);
+}
+
+__device__ __noinline__ void make_plan(const Params &p) {
+  __shared__ int64_t units[PREP_THREADS];  // of a head, then before the sequence
+  __shared__ int tiles[PREP_THREADS];
+  __shared__ int first[PREP_THREADS], tokens[PREP_THREADS];
+  __shared__ int64_t u_done;
+  __shared__ int t_done, rows_done;
+  if (threadIdx.x == 0) {
+    u_done = 0;
+    t_done = rows_done = 0;
+  }
+  for (int b0 = 0; b0 < p.B; b0 += PREP_THREADS) {
+    const int b = b0 + threadIdx.x;
+    int n = 0, L = 0, nt = 0;
+    int64_t c0 = 0, tot = 0;
+    if (b < p.B) {
+      c0 = p.cu[b];
+      const int64_t c1 = p.cu[b + 1], l = p.lens[b];
+      if (c0 < 0 || c1 < c0 || c1 > p.N) {
+        record_device_error(p.err, DERR_DECODE_PLAN);
+        c0 = 0;
+      } else {
+        n = (int)(c1 - c0);
+      }
+      if (l < 0 || l > p.max_len) record_device_error(p.err, DERR_DECODE_PLAN);
+      L = (int)(l < 0 ? 0 : l > p.max_len ? p.max_len : l);
+      nt = (int)(((int64_t)n * p.G + p.rows - 1) / p.rows);
+      for (int mt = 0; mt < nt; ++mt) tot += tile_units(mt, n, L, p.G, p.rows);
+    }
+    units[threadIdx.x] = tot;
+    tiles[threadIdx.x] = nt ? nt + 1 : 0;
+    first[threadIdx.x] = (int)c0;
+    tokens[threadIdx.x] = n;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      int64_t u = u_done;
+      int t = t_done, rows = rows_done;
+      for (int i = 0; i < PREP_THREADS && b0 + i < p.B; ++i) {
+        if (tokens[i] && first[i] < rows) {  // rows that an earlier sequence has
+          record_device_error(p.err, DERR_DECODE_PLAN);
+          tokens[i] = tiles[i] = 0;
+          units[i] = 0;
+        }
+        if (tokens[i]) rows = first[i] + tokens[i];
+        const int64_t x = units[i];
+        const int y = tiles[i];
+        units[i] = u;
+        tiles[i] = t;
+        u += x * p.Hkv;
+        t += y;
+      }
+      u_done = u;
+      t_done = t;
+      rows_done = rows;
+    }
+    __syncthreads();
+    if (b < p.B) {
+      n = tokens[threadIdx.x];
+      if (n == 0) nt = 0;
+      p.w.b_unit[b] = units[threadIdx.x];
+      p.w.b_tile[b] = tiles[threadIdx.x];
+      p.w.start[b] = (int32_t)c0;
+      p.w.count[b] = n;
+      p.w.len[b] = L;
+      int32_t *pre = p.w.mt_pre + tiles[threadIdx.x];
+      int u = 0;
+      for (int mt = 0; mt < nt; ++mt) {
+        pre[mt] = u;
+        u += tile_units(mt, n, L, p.G, p.rows);
+      }
+      if (nt) pre[nt] = u;
+    }
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) {
+    p.w.b_unit[p.B] = u_done;
+    int64_t q = (u_done + p.blocks - 1) / p.blocks;
+    if (q < p.min_units) q = p.min_units;
+    p.w.plan->total = u_done;
+    p.w.plan->quota = q;
+  }
+}
+
+// The power of two that brings a row whose largest entry is `top` into
+// [2^13, 2^14), as (2^e, 2^-e); 1 for a row of zeros, infinities or NaN.
+__device__ __forceinline__ float2 row_power(float top) {
+  if (!(top > 0.f) || isinf(top)) return make_float2(1.f, 1.f);
+  int e;
+  frexpf(top, &e);  // top = f 2^e, f in [1/2, 1)
+  e = 14 - e;
+  e = max(-120, min(120, e));
+  return make_float2(ldexpf(1.f, e), ldexpf(1.f, -e));
+}
+
+__device__ __forceinline__ float load_q(const void *Q, bool f32, int64_t i) {
+  return f32 ? __ldg(static_cast<const float *>(Q) + i)
+             : bf16_bits_to_f32(__ldg(static_cast<const uint16_t *>(Q) + i));
+}
+
+// A block's run of units, one row tile after another.
+struct Seg {
+  int b, h, mt, nt;   // sequence, KV head, row tile, row tiles of the sequence
+  int k0, k1, units;  // its units [k0, k1) of `units`
+  int n, L, start;    // the sequence's tokens, keys, first row
+  int nk;             // key tiles to do: 0 where the row tile sees no key
+  int64_t u, end;     // next unit, end of the run
+};
+
+__device__ __forceinline__ void seg_fill(Seg &s, const Params &p) {
+  const int32_t *pre = p.w.mt_pre + __ldg(p.w.b_tile + s.b);
+  const int a = __ldg(pre + s.mt), z = __ldg(pre + s.mt + 1);
+  s.units = z - a;
+  const int64_t left = s.end - s.u;
+  s.k1 = (int)(left < s.units - s.k0 ? s.k0 + left : s.units);
+  const int last = min(s.n - 1, (p.rows * s.mt + p.rows - 1) / p.G);
+  s.nk = s.L - s.n + last + 1 > 0 ? s.k1 - s.k0 : 0;
+}
+__device__ __forceinline__ void seg_seq(Seg &s, const Params &p) {
+  s.n = __ldg(p.w.count + s.b);
+  s.L = __ldg(p.w.len + s.b);
+  s.start = __ldg(p.w.start + s.b);
+  s.nt = (int)(((int64_t)s.n * p.G + p.rows - 1) / p.rows);
+}
+// First segment of the block; false when it has none.
+__device__ __forceinline__ bool seg_first(Seg &s, const Params &p) {
+  const int64_t total = __ldg(&p.w.plan->total), quota = __ldg(&p.w.plan->quota);
+  s.u = (int64_t)blockIdx.x * quota;
+  s.end = s.u + quota < total ? s.u + quota : total;
+  if (s.u >= total) return false;
+  int lo = 0, hi = p.B;  // the last b whose first unit is not above u
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (__ldg(p.w.b_unit + mid) <= s.u) lo = mid; else hi = mid;
+  }
+  s.b = lo;
+  seg_seq(s, p);
+  const int64_t u0 = __ldg(p.w.b_unit + lo);
+  const int64_t per_head = (__ldg(p.w.b_unit + lo + 1) - u0) / p.Hkv;
+  s.h = (int)((s.u - u0) / per_head);
+  const int rem = (int)(s.u - u0 - s.h * per_head);
+  const int32_t *pre = p.w.mt_pre + __ldg(p.w.b_tile + lo);
+  int a = 0, z = s.nt;
+  while (z - a > 1) {
+    const int mid = (a + z) >> 1;
+    if (__ldg(pre + mid) <= rem) a = mid; else z = mid;
+  }
+  s.mt = a;
+  s.k0 = rem - __ldg(pre + a);
+  seg_fill(s, p);
+  return true;
+}
+__device__ __forceinline__ bool seg_next(Seg &s, const Params &p) {
+  s.u += s.k1 - s.k0;
+  if (s.u >= s.end) return false;
+  s.k0 = 0;
+  if (++s.mt == s.nt) {
+    s.mt = 0;
+    if (++s.h == p.Hkv) {
+      s.h = 0;
+      do {
+        ++s.b;
+        seg_seq(s, p);
+      } while (s.n == 0);
+    }
+  }
+  seg_fill(s, p);
+  return true;
+}
+
+// Page of the granule that holds key t; a page outside the pool is recorded
+// and replaced by page 0.
+__device__ __forceinline__ int page_of(const Params &p, int b, int t) {
+  const int col = t / p.P;
+  int page = col < p.max_pages ? __ldg(p.table + (int64_t)b * p.max_pages + col) : -1;
+  if (page < 0 || page >= p.num_pages) {
+    record_device_error(p.err, DERR_PAGE);
+    page = 0;
+  }
+  return page;
+}
+
+// ---------------------------------------------------------------------------
+// combine: one warp per (row, query head) of a split row tile
+
+constexpr int CMB_WARPS = 8;
+
+template <int D>
+static __global__ void __launch_bounds__(CMB_WARPS * 32) combine_kernel(const Params p) {
+  griddep_wait();
+  const int lane = threadIdx.x & 31;
+  const int64_t id = (int64_t)blockIdx.x * CMB_WARPS + (threadIdx.x >> 5);
+  const int64_t tok = id / p.Hq;
+  const int hq = (int)(id - tok * p.Hq);
+  if (tok >= p.N) return;
+  // the sequence of the row: the last b whose first row is not above it (cu,
+  // not the checked starts, which are not in order where cu is not)
+  if (tok < __ldg(p.cu) || tok >= __ldg(p.cu + p.B)) return;
+  int lo = 0, hi = p.B;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (__ldg(p.cu + mid) <= tok) lo = mid; else hi = mid;
+  }
+  const int b = lo, n = __ldg(p.w.count + b);
+  const int64_t i = tok - __ldg(p.w.start + b);
+  if (i < 0 || i >= n) return;
+  const int h = hq / p.G;
+  const int64_t row = i * p.G + (hq - h * p.G);
+  const int mt = (int)(row / p.rows), r = (int)(row - (int64_t)mt * p.rows);
+  const int32_t *pre = p.w.mt_pre + __ldg(p.w.b_tile + b);
+  const int64_t u0 = __ldg(p.w.b_unit + b);
+  const int64_t per_head = (__ldg(p.w.b_unit + b + 1) - u0) / p.Hkv;
+  const int64_t a = u0 + h * per_head + __ldg(pre + mt);
+  const int64_t z = u0 + h * per_head + __ldg(pre + mt + 1);
+  const int64_t quota = __ldg(&p.w.plan->quota);
+  const int64_t c0 = a / quota, c1 = (z - 1) / quota;
+  if (c0 == c1) return;  // one block wrote the row
+  constexpr int E = D / 32;
+  float m = -INFINITY, l = 0.f, o[E] = {};
+  for (int64_t c = c0; c <= c1; ++c) {
+    const float *part = p.w.part + ((2 * c + (c * quota <= a ? 1 : 0)) * p.rows + r) * (D + 2);
+    const float2 ml = *reinterpret_cast<const float2 *>(part + D);
+    if (ml.y == 0.f) continue;
+    const float mn = fmaxf(m, ml.x);
+    const float f = m == mn ? 1.f : fast_exp2(m - mn), w = fast_exp2(ml.x - mn);
+    l = l * f + ml.y * w;
+#pragma unroll
+    for (int e = 0; e < E; e += 2) {
+      const float2 x = *reinterpret_cast<const float2 *>(part + lane * E + e);
+      o[e] = o[e] * f + x.x * w;
+      o[e + 1] = o[e + 1] * f + x.y * w;
+    }
+    m = mn;
+  }
+  const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+  uint32_t *out = reinterpret_cast<uint32_t *>(p.out + (tok * p.Hq + hq) * D + lane * E);
+#pragma unroll
+  for (int e = 0; e < E; e += 2)
+    out[e / 2] = inv == 0.f ? 0u : pack_bf16x2(o[e] * inv, o[e + 1] * inv);
+}
+
+// ---------------------------------------------------------------------------
+// host
+
+template <typename... Args>
+inline cudaError_t launch_after(void (*kernel)(Args...), int64_t grid, int threads, size_t smem,
+                                cudaStream_t stream, Args... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+
+}  // namespace chunk
+}  // namespace jlk

@@ -55,6 +55,10 @@
 //   warp 12    owns the TMEM allocation; one elected lane issues the MMAs of a tile
 //              into one of two accumulators and commits them to the barriers
 //              that free the A chunks and publish the accumulator.
+// The PAGED instances expand a paged cache for the attention of long chunks:
+// tile (b, kv head, j) is keys 128 j .. of that sequence, gathered through the
+// block table, tiles past the sequence's length are skipped, and the rows are
+// binary16 (2^-11 of rounding: they are multiplied again) times KEY_FACTOR.
 // Every mbarrier wait is bounded (about 2 s of GPU time); a wait that runs
 // out records DERR_TC_WAIT_TIMEOUT, raises a shared abort flag, and the CTA
 // still frees its TMEM.
@@ -131,7 +135,45 @@ struct Params {
   uint32_t mag[4];        // TurboQuant: centroid magnitudes a_0 < .. (binary16 pairs)
   uint32_t dmag01, dmag23;  // a_0 ^ a_1, a_2 ^ a_3 (binary16 bits)
   int *err;
+  // PAGED: codes and norms are pools, n their rows
+  const int32_t *table, *lens;
+  int Hkv, P, max_pages, num_pages, key_tiles;  // key_tiles: of max_len
+  int64_t max_len;
 };
+
+// Keys of sequence b, inside the call's bound.
+__device__ __forceinline__ int64_t paged_len(const Params &p, int b) {
+  const int64_t l = __ldg(p.lens + b);
+  return l < 0 ? 0 : l > p.max_len ? p.max_len : l;
+}
+// The first tile from `tile` on, in steps of `step`, that holds a key.
+template <bool PAGED>
+__device__ __forceinline__ int64_t live_tile(const Params &p, int64_t tile, int64_t step) {
+  if constexpr (PAGED) {
+    while (tile < p.num_tiles) {
+      const int64_t unit = tile / p.key_tiles;  // (sequence, KV head)
+      if ((tile - unit * p.key_tiles) * BM < paged_len(p, (int)(unit / p.Hkv))) break;
+      tile += step;
+    }
+  }
+  return tile;
+}
+// Pool row of key r of a tile; -1 for keys past the last one and for pages
+// outside the pool (recorded).
+__device__ __forceinline__ int64_t paged_row(const Params &p, int64_t tile, int r) {
+  if (tile >= p.num_tiles) return -1;
+  const int64_t unit = tile / p.key_tiles;
+  const int b = (int)(unit / p.Hkv), h = (int)(unit - (int64_t)b * p.Hkv);
+  const int64_t t = (tile - unit * p.key_tiles) * BM + r;
+  if (t >= paged_len(p, b)) return -1;
+  const int col = (int)(t / p.P);
+  const int page = col < p.max_pages ? __ldg(p.table + (int64_t)b * p.max_pages + col) : -1;
+  if (page < 0 || page >= p.num_pages) {
+    record_device_error(p.err, DERR_PAGE);
+    return -1;
+  }
+  return ((int64_t)page * p.Hkv + h) * p.P + t % p.P;
+}
 
 
 // 4-byte async copy global -> shared; src_bytes < 4 zero-fills.
@@ -213,7 +255,7 @@ __device__ __forceinline__ void centroid_pairs(const uint32_t (&w)[TB], const Pa
   }
 }
 
-template <int M, int D, int TB>
+template <int M, int D, int TB, bool PAGED>
 __global__ void __launch_bounds__(THREADS, 1)
     dequant_tc_kernel(const __grid_constant__ CUtensorMap tmap_out, const Params p) {
   using C = Cfg<M, D, TB>;
@@ -315,9 +357,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t crow =
         base + C::OFF_C + r * C::CODE_ROW + pt * (C::TURBO ? C::PART_BYTES : KP * 8);
     auto code_slot = [&](int slot) { return crow + (uint32_t)(slot * BM * C::CODE_ROW); };
-    auto copy_part = [&](uint32_t dst, int64_t row) {
+    auto copy_part = [&](uint32_t dst, int64_t row) {  // row -1 or past the end: zeros
       if constexpr (!C::TURBO) {
-        const bool live = row < p.n && JL_IN_RANGE(p.err, row * (M / 8) + pt * KP * 8, KP * 8,
+        const bool live = (!PAGED || row >= 0) && row < p.n && JL_IN_RANGE(p.err, row * (M / 8) + pt * KP * 8, KP * 8,
                                                    p.n * (M / 8));
         const uint8_t *src =
             reinterpret_cast<const uint8_t *>(p.codes + (live ? row : 0) * (M / 32)) + pt * KP * 8;
@@ -330,7 +372,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       } else {
         // 8 bytes (the 64 coordinates of the part's chunk index kc0 / 2) of
         // each cell plane and of the sign words, then the norm pair
-        const bool live = row < p.n &&
+        const bool live = (!PAGED || row >= 0) && row < p.n &&
                           JL_IN_RANGE(p.err, row * C::CODE_BYTES_G, C::CODE_BYTES_G,
                                       p.n * C::CODE_BYTES_G) &&
                           JL_IN_RANGE(p.err, 2 * row, 2, 2 * p.n);
@@ -343,18 +385,26 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
       cp_async_commit();
     };
-    if (ok)
-      for (int k = 0; k < CODE_SLOTS - 1; ++k)
-        copy_part(code_slot(k), ((int64_t)blockIdx.x + (int64_t)k * gridDim.x) * BM + r);
+    auto row_of = [&](int64_t tile) {
+      if constexpr (PAGED) return paged_row(p, tile, r);
+      return tile * BM + r;
+    };
+    // the tile two ahead of the current one, whose codes are copied next
+    int64_t ahead = live_tile<PAGED>(p, blockIdx.x, gridDim.x);
+    for (int k = 0; ok && k < CODE_SLOTS - 1; ++k) {
+      copy_part(code_slot(k), row_of(ahead));
+      ahead = live_tile<PAGED>(p, ahead + gridDim.x, gridDim.x);
+    }
     int cs = 0;                    // code slot of this tile's words
     // ring slot and phase of this part's first chunk of the tile: global
     // chunk it * KCH + kc0, advanced by KCH per tile without a division
     int rs0 = kc0 % C::RING;
     uint32_t rph0 = (uint32_t)((kc0 / C::RING) & 1);
     constexpr int NW = C::TURBO ? 2 * TB + 3 : 2 * KP;  // words of a part's slot
-    for (int64_t tile = blockIdx.x; ok && tile < ntiles; tile += gridDim.x) {
-      copy_part(code_slot(cs == 0 ? CODE_SLOTS - 1 : cs - 1),
-                (tile + (int64_t)(CODE_SLOTS - 1) * gridDim.x) * BM + r);
+    for (int64_t tile = live_tile<PAGED>(p, blockIdx.x, gridDim.x); ok && tile < ntiles;
+         tile = live_tile<PAGED>(p, tile + gridDim.x, gridDim.x)) {
+      copy_part(code_slot(cs == 0 ? CODE_SLOTS - 1 : cs - 1), row_of(ahead));
+      ahead = live_tile<PAGED>(p, ahead + gridDim.x, gridDim.x);
       cp_async_wait<CODE_SLOTS - 1>();  // this tile's words have landed
       uint32_t cur[NW];
       {
@@ -437,20 +487,23 @@ __global__ void __launch_bounds__(THREADS, 1)
     // the warp once the accumulator is ready
     constexpr int NSTRIDE = C::TURBO ? 2 : 1;  // binary16s per key
     auto load_norm = [&](int64_t tl) -> uint16_t {
-      const int64_t row = tl * BM + 32 * q + lane;
+      const int64_t row = PAGED ? paged_row(p, tl, 32 * q + lane) : tl * BM + 32 * q + lane;
       uint16_t h = 0;
-      if (tl < ntiles && row < p.n && JL_IN_RANGE(p.err, NSTRIDE * row, 1, NSTRIDE * p.n))
+      if (tl < ntiles && (!PAGED || row >= 0) && row < p.n && JL_IN_RANGE(p.err, NSTRIDE * row, 1, NSTRIDE * p.n))
         h = __ldg(p.norms + NSTRIDE * row);
       return h;
     };
-    uint16_t nrm_next = load_norm(blockIdx.x);
+    int64_t next = live_tile<PAGED>(p, blockIdx.x, gridDim.x);
+    uint16_t nrm_next = load_norm(next);
     int64_t t = 0;
-    for (int64_t tile = blockIdx.x; tile < ntiles; tile += gridDim.x, ++t) {
+    for (int64_t tile = next; tile < ntiles; tile = next, ++t) {
       const int a = (int)(t & 1);
       const uint32_t aph = (uint32_t)((t >> 1) & 1);
       const uint16_t nrm = nrm_next;
-      nrm_next = load_norm(tile + gridDim.x);
-      const float f = (C::TURBO ? 1.f : p.coef) * __half2float(__ushort_as_half(nrm));
+      next = live_tile<PAGED>(p, tile + gridDim.x, gridDim.x);
+      nrm_next = load_norm(next);
+      const float f = (C::TURBO ? 1.f : p.coef) * (PAGED ? KEY_FACTOR : 1.f) *
+                      __half2float(__ushort_as_half(nrm));
       const int ob = (int)(t % C::OBUF);
       uint8_t *stage = gbase + C::OFF_O + (ew * C::OBUF + ob) * C::OWARP;
       // the staging buffer's previous stores must have read it
@@ -465,8 +518,15 @@ __global__ void __launch_bounds__(THREADS, 1)
       auto emit = [&](const uint32_t (&v)[32], int c0) {
         uint32_t o[16];
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-          o[e] = pack_bf16x2(__uint_as_float(v[2 * e]) * f, __uint_as_float(v[2 * e + 1]) * f);
+        for (int e = 0; e < 16; ++e) {
+          const float a = __uint_as_float(v[2 * e]) * f, b = __uint_as_float(v[2 * e + 1]) * f;
+          if constexpr (PAGED) {
+            const __half2 x = __floats2half2_rn(a, b);
+            o[e] = *reinterpret_cast<const uint32_t *>(&x);
+          } else {
+            o[e] = pack_bf16x2(a, b);
+          }
+        }
         uint8_t *box = stage + (c0 >> 6) * C::OBOX + lane * 128;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -513,7 +573,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       uint32_t rph = 0;
       uint32_t t = 0;
       bool ok = true;
-      for (int64_t tile = blockIdx.x; ok && tile < ntiles; tile += gridDim.x, ++t) {
+      for (int64_t tile = live_tile<PAGED>(p, blockIdx.x, gridDim.x); ok && tile < ntiles;
+           tile = live_tile<PAGED>(p, tile + gridDim.x, gridDim.x), ++t) {
         const int a = (int)(t & 1u);
         const uint32_t aph = (t >> 1) & 1u;
         if (!__all_sync(0xffffffffu, wait_phase(accempty_bar(a), aph ^ 1u, abort_flag, p.err)))
@@ -582,21 +643,21 @@ static bool make_out_map(CUtensorMap *map, uint16_t *out, int64_t n, int d) {
             CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int M, int D, int TB>
+template <int M, int D, int TB, bool PAGED = false>
 cudaError_t launch_t(Params p, uint16_t *out, cudaStream_t stream) {
   using C = Cfg<M, D, TB>;
   p.err = device_error_ptr();
   if (!p.err) return cudaErrorInvalidSymbol;
+  if (!PAGED) p.num_tiles = (p.n + BM - 1) / BM;
   CUtensorMap tmap;
-  if (!make_out_map(&tmap, out, p.n, D)) return cudaErrorInvalidValue;
-  p.num_tiles = (p.n + BM - 1) / BM;
+  if (!make_out_map(&tmap, out, PAGED ? p.num_tiles * BM : p.n, D)) return cudaErrorInvalidValue;
   p.coef = (float)(1.2533141373155002512 / (double)M);
-  cudaError_t e = cudaFuncSetAttribute(dequant_tc_kernel<M, D, TB>,
+  cudaError_t e = cudaFuncSetAttribute(dequant_tc_kernel<M, D, TB, PAGED>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
   const int64_t sms = device_sm_count();
   const int64_t grid = p.num_tiles < sms ? p.num_tiles : sms;
-  dequant_tc_kernel<M, D, TB><<<(int)grid, THREADS, C::SMEM, stream>>>(tmap, p);
+  dequant_tc_kernel<M, D, TB, PAGED><<<(int)grid, THREADS, C::SMEM, stream>>>(tmap, p);
   return cudaGetLastError();
 }
 
@@ -633,6 +694,33 @@ cudaError_t launch_dequantize_tc(const uint32_t *signs, const uint16_t *norms, i
   p.n = n;
 #define JL_CASE(MM, DD) \
   if (m == MM && d == DD) return dq::launch_t<MM, DD, 0>(p, out, stream);
+  JL_CASE(64, 64) JL_CASE(128, 64) JL_CASE(256, 64) JL_CASE(512, 64)
+  JL_CASE(64, 128) JL_CASE(128, 128) JL_CASE(256, 128) JL_CASE(512, 128)
+#undef JL_CASE
+  return cudaErrorNotSupported;
+}
+
+cudaError_t launch_expand_paged(const uint32_t *sign_pages, const uint16_t *norm_pages,
+                                int num_pages, int page_tokens, const int32_t *block_table,
+                                int max_pages, const int32_t *seq_lens, int B, int Hkv,
+                                int64_t max_len, const uint16_t *S, int m, int d, uint16_t *out,
+                                cudaStream_t stream) {
+  dq::Params p{};
+  p.codes = sign_pages;
+  p.norms = norm_pages;
+  p.B = S;
+  p.n = (int64_t)num_pages * Hkv * page_tokens;
+  p.table = block_table;
+  p.lens = seq_lens;
+  p.Hkv = Hkv;
+  p.P = page_tokens;
+  p.max_pages = max_pages;
+  p.num_pages = num_pages;
+  p.max_len = max_len;
+  p.key_tiles = (int)((max_len + dq::BM - 1) / dq::BM);
+  p.num_tiles = (int64_t)B * Hkv * p.key_tiles;
+#define JL_CASE(MM, DD) \
+  if (m == MM && d == DD) return dq::launch_t<MM, DD, 0, true>(p, out, stream);
   JL_CASE(64, 64) JL_CASE(128, 64) JL_CASE(256, 64) JL_CASE(512, 64)
   JL_CASE(64, 128) JL_CASE(128, 128) JL_CASE(256, 128) JL_CASE(512, 128)
 #undef JL_CASE

@@ -33,6 +33,17 @@ cudaError_t launch_dequantize_tc(const uint32_t *signs, const uint16_t *norms, i
                                  const uint16_t *S, int m, int d, uint16_t *out,
                                  cudaStream_t stream);
 
+// The keys of a paged cache expanded for attention: binary16 rows
+// KEY_FACTOR * khat, [B][Hkv][ceil(max_len / 128) * 128][d], of the tiles of
+// 128 keys that hold one (keys past the last one of such a tile are zero).
+// The factor keeps the largest binary16 norm's rows inside binary16.
+constexpr float KEY_FACTOR = 0.25f;
+cudaError_t launch_expand_paged(const uint32_t *sign_pages, const uint16_t *norm_pages,
+                                int num_pages, int page_tokens, const int32_t *block_table,
+                                int max_pages, const int32_t *seq_lens, int B, int Hkv,
+                                int64_t max_len, const uint16_t *S, int m, int d, uint16_t *out,
+                                cudaStream_t stream);
+
 // TurboQuant-prod dequantizer (dequant_tc.cu): the reconstruction matrix
 // R = [Pinv | Pinv S^T] in binary16 (d x (d + m)), and khat = ||k|| R a on
 // the tensor cores (d = m = 128).
