@@ -8,8 +8,8 @@
 // head, row tile, key tile) and every block takes an equal run of them, so a
 // long context with few rows is split and many rows are balanced, the causal
 // triangle included.  A row tile that lies in one block is written out by it;
-// of a split one each block leaves the softmax states (acc, max, sum), which
-// combine_kernel joins.
+// of a split one each block leaves the softmax states (acc, max, sum), and the
+// last block to do so joins them, in the order of the keys.
 #pragma once
 
 #include "jl_common.cuh"
@@ -21,6 +21,7 @@ namespace chunk {
 constexpr int BN = 128;            // keys of a tile
 constexpr int GRAN = 32;           // keys that surely share a page
 constexpr float RENEW = 8.f;       // log2 growth of a row's maximum that renews it
+constexpr float MIN_SCALE = 1.17549435e-38f;  // of a row: -inf times it stays -inf
 constexpr int PREP_THREADS = 256;
 constexpr int SM_COUNT = 148;      // bounds the workspace per shape
 
@@ -36,7 +37,8 @@ struct Work {         // workspace
   int32_t *mt_pre;    // per sequence: units before each row tile of a head, and their sum
   uint16_t *U;        // [Hkv][N G][K] binary16 queries, scaled row by row
   float *rs;          // [Hkv][N G] row scale: log2 units per unit of score
-  float *part;        // [2 blocks][rows][d + 2] softmax states
+  float *part;        // [2 blocks] softmax states: a block's first and last row tile
+  int32_t *arrived;   // [2 blocks] states left of the split row tile that begins in a block
   uint16_t *keys;     // [B][Hkv][tiles of max_len][BN][d] binary16 keys (many rows)
 };
 
@@ -63,7 +65,7 @@ __device__ __forceinline__ int tile_units(int mt, int n, int L, int G, int rows)
   return max(1, (seen + BN - 1) / BN);
 }
 
-__device__ __noinline__ void make_plan(const Params &p) {
+static __device__ __noinline__ void make_plan(const Params &p) {
   __shared__ int64_t units[PREP_THREADS];  // of a head, then before the sequence
   __shared__ int tiles[PREP_THREADS];
   __shared__ int first[PREP_THREADS], tokens[PREP_THREADS];
@@ -136,6 +138,7 @@ __device__ __noinline__ void make_plan(const Params &p) {
     }
     __syncthreads();
   }
+  for (int i = threadIdx.x; i < 2 * p.blocks; i += PREP_THREADS) p.w.arrived[i] = 0;
   if (threadIdx.x == 0) {
     p.w.b_unit[p.B] = u_done;
     int64_t q = (u_done + p.blocks - 1) / p.blocks;
@@ -244,62 +247,37 @@ __device__ __forceinline__ int page_of(const Params &p, int b, int t) {
 }
 
 // ---------------------------------------------------------------------------
-// combine: one warp per (row, query head) of a split row tile
+// split row tiles
 
-constexpr int CMB_WARPS = 8;
+// The blocks whose runs the segment's row tile touches, and where each of them
+// leaves its states: record 2 c + 1 where block c has the row tile's first
+// unit, 2 c otherwise (then the row tile is the first of its run).
+struct Split {
+  int64_t c0, c1, first, quota;
+  __device__ __forceinline__ Split(const Seg &s, const Params &p) {
+    quota = __ldg(&p.w.plan->quota);
+    first = s.u - s.k0;
+    c0 = first / quota;
+    c1 = (first + s.units - 1) / quota;
+  }
+  __device__ __forceinline__ int64_t record(int64_t c) const {
+    return 2 * c + (c * quota <= first ? 1 : 0);
+  }
+};
 
-template <int D>
-static __global__ void __launch_bounds__(CMB_WARPS * 32) combine_kernel(const Params p) {
-  griddep_wait();
-  const int lane = threadIdx.x & 31;
-  const int64_t id = (int64_t)blockIdx.x * CMB_WARPS + (threadIdx.x >> 5);
-  const int64_t tok = id / p.Hq;
-  const int hq = (int)(id - tok * p.Hq);
-  if (tok >= p.N) return;
-  // the sequence of the row: the last b whose first row is not above it (cu,
-  // not the checked starts, which are not in order where cu is not)
-  if (tok < __ldg(p.cu) || tok >= __ldg(p.cu + p.B)) return;
-  int lo = 0, hi = p.B;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (__ldg(p.cu + mid) <= tok) lo = mid; else hi = mid;
-  }
-  const int b = lo, n = __ldg(p.w.count + b);
-  const int64_t i = tok - __ldg(p.w.start + b);
-  if (i < 0 || i >= n) return;
-  const int h = hq / p.G;
-  const int64_t row = i * p.G + (hq - h * p.G);
-  const int mt = (int)(row / p.rows), r = (int)(row - (int64_t)mt * p.rows);
-  const int32_t *pre = p.w.mt_pre + __ldg(p.w.b_tile + b);
-  const int64_t u0 = __ldg(p.w.b_unit + b);
-  const int64_t per_head = (__ldg(p.w.b_unit + b + 1) - u0) / p.Hkv;
-  const int64_t a = u0 + h * per_head + __ldg(pre + mt);
-  const int64_t z = u0 + h * per_head + __ldg(pre + mt + 1);
-  const int64_t quota = __ldg(&p.w.plan->quota);
-  const int64_t c0 = a / quota, c1 = (z - 1) / quota;
-  if (c0 == c1) return;  // one block wrote the row
-  constexpr int E = D / 32;
-  float m = -INFINITY, l = 0.f, o[E] = {};
-  for (int64_t c = c0; c <= c1; ++c) {
-    const float *part = p.w.part + ((2 * c + (c * quota <= a ? 1 : 0)) * p.rows + r) * (D + 2);
-    const float2 ml = *reinterpret_cast<const float2 *>(part + D);
-    if (ml.y == 0.f) continue;
-    const float mn = fmaxf(m, ml.x);
-    const float f = m == mn ? 1.f : fast_exp2(m - mn), w = fast_exp2(ml.x - mn);
-    l = l * f + ml.y * w;
-#pragma unroll
-    for (int e = 0; e < E; e += 2) {
-      const float2 x = *reinterpret_cast<const float2 *>(part + lane * E + e);
-      o[e] = o[e] * f + x.x * w;
-      o[e + 1] = o[e + 1] * f + x.y * w;
-    }
-    m = mn;
-  }
-  const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-  uint32_t *out = reinterpret_cast<uint32_t *>(p.out + (tok * p.Hq + hq) * D + lane * E);
-#pragma unroll
-  for (int e = 0; e < E; e += 2)
-    out[e / 2] = inv == 0.f ? 0u : pack_bf16x2(o[e] * inv, o[e + 1] * inv);
+// Called by `threads` threads that share the row tile (or half `a` of it),
+// after each has written its part of the states: true, for all of them, in the
+// last block to arrive. `flag` is a word of shared memory of theirs.
+__device__ __forceinline__ bool last_to_arrive(const Split &t, const Params &p, int a, int bar,
+                                               int threads, bool leader, volatile int *flag) {
+  __threadfence();
+  asm volatile("bar.sync %0, %1;\n" ::"r"(bar), "r"(threads) : "memory");
+  if (leader)
+    *flag = atomicAdd(p.w.arrived + 2 * t.c0 + a, 1) == (int)(t.c1 - t.c0);
+  asm volatile("bar.sync %0, %1;\n" ::"r"(bar), "r"(threads) : "memory");
+  const bool last = *flag != 0;
+  if (last) __threadfence();
+  return last;
 }
 
 // ---------------------------------------------------------------------------
@@ -321,6 +299,43 @@ inline cudaError_t launch_after(void (*kernel)(Args...), int64_t grid, int threa
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+
+// The workspace: `rows` per row tile, K entries of a converted query, `part`
+// floats of states per record, `keys` bytes of expanded keys.
+inline size_t lay_out(Work *w, void *base, int64_t N, int B, int Hq, int Hkv, int rows, int K,
+                      size_t part, size_t keys) {
+  size_t off = 0;
+  auto take = [&](size_t n) {
+    uint8_t *x = static_cast<uint8_t *>(base) + off;
+    off += (n + 255) & ~(size_t)255;
+    return x;
+  };
+  Work t;
+  t.plan = reinterpret_cast<Plan *>(take(sizeof(Plan)));
+  t.b_unit = reinterpret_cast<int64_t *>(take((size_t)(B + 1) * 8));
+  t.b_tile = reinterpret_cast<int32_t *>(take((size_t)B * 4));
+  t.start = reinterpret_cast<int32_t *>(take((size_t)B * 4));
+  t.count = reinterpret_cast<int32_t *>(take((size_t)B * 4));
+  t.len = reinterpret_cast<int32_t *>(take((size_t)B * 4));
+  t.mt_pre = reinterpret_cast<int32_t *>(
+      take(((size_t)N * (Hq / Hkv) / rows + 2 * (size_t)B + 1) * 4));
+  t.arrived = reinterpret_cast<int32_t *>(take((size_t)2 * SM_COUNT * 4));
+  t.U = reinterpret_cast<uint16_t *>(take((size_t)N * Hq * K * 2));
+  t.rs = reinterpret_cast<float *>(take((size_t)N * Hq * 4));
+  t.part = reinterpret_cast<float *>(take((size_t)2 * SM_COUNT * part * 4));
+  t.keys = reinterpret_cast<uint16_t *>(take(keys));
+  if (w) *w = t;
+  return off;
+}
+
+// The kernels for few and for many rows (chunk_few.cu, chunk_tc.cu): the
+// workspace they need, and their launches.
+size_t few_workspace(int64_t N, int B, int Hq, int Hkv, int m, int d, Work *w, void *base);
+size_t many_workspace(int64_t N, int B, int Hq, int Hkv, int64_t max_len, int d, Work *w,
+                      void *base);
+cudaError_t launch_few(Params p, const ChunkArgs &a, cudaStream_t stream);
+cudaError_t launch_many(Params p, const ChunkArgs &a, cudaStream_t stream);
+int few_rows(int64_t N, int B, int G);  // rows of a row tile of the kernel for few rows
 
 }  // namespace chunk
 }  // namespace jlk

@@ -17,7 +17,6 @@
 //               down to 2^-27 of the row's largest), and the plan.
 //   2. expand   khat as binary16, from the pages (dequant_tc.cu).
 //   3. attend   the products, below.
-//   4. combine  joins the states of split row tiles (chunk.cuh).
 //
 // attend takes 256 rows at a time as two halves of 128, and per key tile and
 // half (all products fp32-accumulated in tensor memory):
@@ -50,11 +49,8 @@ namespace {
 constexpr int BM = 128, HALVES = 2, ROWS = BM * HALVES;
 constexpr int SM_WARPS = 4;                       // of a half
 constexpr int MMA_WARP = SM_WARPS * HALVES, LOAD_WARP = MMA_WARP + 1;
-constexpr int THREADS = 12 * 32;                  // three warpgroups; two warps idle
-// Registers: a softmax thread holds its row of scores, so the two softmax
-// warpgroups take over what the third gives up.
-constexpr int REGS = 168, SM_REGS = 208, REST_REGS = 88;
-static_assert(2 * SM_REGS + REST_REGS <= 3 * REGS, "register split");
+constexpr int THREADS = (LOAD_WARP + 1) * 32;
+constexpr int POLY_EVERY = 4;                     // one pair of weights in so many on the FMA pipe
 constexpr int BOX = BM * 128;                     // 128 rows of 64 16-bit elements
 
 __device__ __forceinline__ float load_q(const void *Q, bool f32, int64_t i) {
@@ -91,7 +87,8 @@ __global__ void __launch_bounds__(PREP_THREADS) prep_kernel(const Params p) {
   for (int e = 0; e < E; ++e)
     p.w.U[r * D + lane + 32 * e] = __half_as_ushort(__float2half_rn(sgn * q[e] * f.x));
   if (lane == 0)
-    p.w.rs[r] = (float)(1.4426950408889634074 / KEY_FACTOR) * fabsf(p.scale) * f.y;
+    p.w.rs[r] = fmaxf((float)(1.4426950408889634074 / KEY_FACTOR) * fabsf(p.scale) * f.y,
+                      MIN_SCALE);
 }
 
 template <int D>
@@ -123,25 +120,115 @@ __device__ __forceinline__ uint64_t desc_v(uint32_t addr) {
   return d;
 }
 
-// (a, b) * (m, m) + (c, c), and the sum of two pairs: one instruction each
-__device__ __forceinline__ float2 fma2(float a, float b, float m, float c) {
-  uint64_t x, mm, cc, y;
-  asm("mov.b64 %0, {%1, %2};\n" : "=l"(x) : "f"(a), "f"(b));
-  asm("mov.b64 %0, {%1, %1};\n" : "=l"(mm) : "f"(m));
-  asm("mov.b64 %0, {%1, %1};\n" : "=l"(cc) : "f"(c));
-  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(y) : "l"(x), "l"(mm), "l"(cc));
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;\n" : "=f"(r.x), "=f"(r.y) : "l"(y));
+// Pairs of fp32 in one register pair, one instruction for both.
+using f32x2 = uint64_t;
+__device__ __forceinline__ f32x2 pair(float a, float b) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "f"(a), "f"(b));
   return r;
 }
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  uint64_t x, z, y;
-  asm("mov.b64 %0, {%1, %2};\n" : "=l"(x) : "f"(a.x), "f"(a.y));
-  asm("mov.b64 %0, {%1, %2};\n" : "=l"(z) : "f"(b.x), "f"(b.y));
-  asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(y) : "l"(x), "l"(z));
+__device__ __forceinline__ float2 halves_of(f32x2 x) {
   float2 r;
-  asm("mov.b64 {%0, %1}, %2;\n" : "=f"(r.x), "=f"(r.y) : "l"(y));
+  asm("mov.b64 {%0, %1}, %2;\n" : "=f"(r.x), "=f"(r.y) : "l"(x));
   return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;\n" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// 2^x of a pair on the multiply-add pipe, for the share of the weights that
+// the exponential unit has no time for.  x = n + f with n the nearest whole
+// number, 2^f by the cubic with the least largest relative error on
+// [-1/2, 1/2] (Remez exchange; 7.5e-5 = 2^-13.7, a twentieth of the rounding to
+// bf16 that follows), n added to the exponent.  x below -126 gives 2^-126.
+__device__ __forceinline__ float2 exp2_poly(f32x2 x) {
+  constexpr float BIG = 12582912.f;  // 1.5 * 2^23: adding it rounds to a whole number
+  const float2 c = halves_of(x);
+  x = pair(fmaxf(c.x, -126.f), fmaxf(c.y, -126.f));
+  const f32x2 t = add2(x, pair(BIG, BIG));
+  const f32x2 n = add2(t, pair(-BIG, -BIG));
+  const f32x2 f = fma2(n, pair(-1.f, -1.f), x);
+  f32x2 y = fma2(f, pair(0.0551716685f, 0.0551716685f), pair(0.2426111251f, 0.2426111251f));
+  y = fma2(y, f, pair(0.6932609677f, 0.6932609677f));
+  y = fma2(y, f, pair(0.9999280572f, 0.9999280572f));
+  const float2 k = halves_of(t), v = halves_of(y);
+  return make_float2(__uint_as_float(__float_as_uint(k.x) * 0x800000u + __float_as_uint(v.x)),
+                     __uint_as_float(__float_as_uint(k.y) * 0x800000u + __float_as_uint(v.y)));
+}
+
+// Largest of the 128 scores of a row; those from column lim on do not count.
+// A NaN among the others is the result.
+template <bool MASK>
+__device__ __forceinline__ float row_max(uint32_t tS, int lim) {
+  uint32_t v[4][32];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) ld32(tS + 32 * c, v[c]);
+#pragma unroll
+  for (int c = 0; c < 4; ++c) ld_wait(v[c]);
+  float t[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) t[q] = -INFINITY;
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+#pragma unroll
+    for (int j = 0; j < 32; j += 8)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        float x = __uint_as_float(v[c][j + q]), y = __uint_as_float(v[c][j + 4 + q]);
+        if (MASK && 32 * c + j + q >= lim) x = -INFINITY;
+        if (MASK && 32 * c + j + 4 + q >= lim) y = -INFINITY;
+        t[q] = max_nan(t[q], max_nan(x, y));
+      }
+  return max_nan(max_nan(t[0], t[1]), max_nan(t[2], t[3]));
+}
+
+// Weights 2^(x rs + mm) of 64 scores from column 64 * half on, as bf16 over the
+// scores' columns 32 * half ..; their sums added to `sum`.
+template <bool MASK>
+__device__ __forceinline__ void row_weights(uint32_t tS, int half, int lim, float rs, float mm,
+                                            f32x2 &sum) {
+  uint32_t v[2][32];
+#pragma unroll
+  for (int c = 0; c < 2; ++c) ld32(tS + 64 * half + 32 * c, v[c]);
+#pragma unroll
+  for (int c = 0; c < 2; ++c) ld_wait(v[c]);
+  const f32x2 rs2 = pair(rs, rs), mm2 = pair(mm, mm);
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    uint32_t w[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      float a = __uint_as_float(v[c][2 * e]), b = __uint_as_float(v[c][2 * e + 1]);
+      const int col = 64 * half + 32 * c + 2 * e;
+      if (MASK && col >= lim) a = -INFINITY;
+      if (MASK && col + 1 >= lim) b = -INFINITY;
+      const f32x2 x = fma2(pair(a, b), rs2, mm2);
+      float2 y;
+      if (!MASK && e % POLY_EVERY == POLY_EVERY - 1) {
+        y = exp2_poly(x);
+      } else {
+        y = halves_of(x);
+        y.x = fast_exp2(y.x);
+        y.y = fast_exp2(y.y);
+      }
+      sum = add2(sum, pair(y.x, y.y));
+      w[e] = pack_bf16x2(y.x, y.y);
+    }
+    st16(tS + 32 * half + 16 * c, w);
+  }
+  st_wait();
 }
 
 template <int D>
@@ -162,7 +249,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     return a;
   };
   const uint32_t kfull = bars(C::SK), kempty = bars(C::SK), vfull = bars(C::SV),
-                 vempty = bars(C::SV), sfull = bars(HALVES), pready = bars(HALVES),
+                 vempty = bars(C::SV), sfull = bars(HALVES), pready = bars(2 * HALVES),
                  ofree = bars(HALVES), pvdone = bars(2 * HALVES), ufull = bars(1),
                  uempty = bars(1), fin = bars(1);
   // two barriers a half for the value products in turn: whoever waits for a
@@ -171,6 +258,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   auto pv_phase = [](uint32_t t) { return (t >> 1) & 1u; };
   uint32_t *holder = reinterpret_cast<uint32_t *>(g + C::OFF_BAR + 496);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(g + C::OFF_BAR + 500);
+  volatile int *join_flag = reinterpret_cast<volatile int *>(g + C::OFF_BAR + 504);  // per half
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -184,7 +272,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     for (int a = 0; a < HALVES; ++a) {
       mbar_init(sfull + 8 * a, 1);
-      mbar_init(pready + 8 * a, SM_WARPS);
+      mbar_init(pready + 16 * a, SM_WARPS);
+      mbar_init(pready + 16 * a + 8, SM_WARPS);
       mbar_init(ofree + 8 * a, SM_WARPS);
       mbar_init(pvdone + 16 * a, 1);
       mbar_init(pvdone + 16 * a + 8, 1);
@@ -215,7 +304,6 @@ __global__ void __launch_bounds__(THREADS, 1)
 
   if (warp < MMA_WARP) {
     // ---------------- softmax: thread = row of half a
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(SM_REGS));
     const int a = warp / SM_WARPS;
     const int r = threadIdx.x & (BM - 1);                   // row of the half
     const uint32_t trow = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
@@ -243,80 +331,6 @@ __global__ void __launch_bounds__(THREADS, 1)
         __syncwarp();
         fence_after();
         const int t0 = (s.k0 + k) * BN;
-        if (any_live) {
-          uint32_t v[4][32];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) ld32(tS + 32 * c, v[c]);
-          const int lim = seen - t0;  // columns the row sees
-          float top = -INFINITY;
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            ld_wait(v[c]);
-            if (lim < 32 * c + 32) {  // keys the row does not see
-#pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (32 * c + j >= lim) v[c][j] = 0xff800000u;
-            }
-            float t[4];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) t[q] = __uint_as_float(v[c][q]);
-#pragma unroll
-            for (int j = 4; j < 32; j += 8)
-#pragma unroll
-              for (int q = 0; q < 4; ++q)
-                t[q] = j + 4 + q < 32
-                           ? fmaxf(t[q], fmaxf(__uint_as_float(v[c][j + q]),
-                                               __uint_as_float(v[c][j + 4 + q])))
-                           : fmaxf(t[q], __uint_as_float(v[c][j + q]));
-            top = fmaxf(top, fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])));
-          }
-          const float cand = top == -INFINITY ? -INFINITY : top * rs;
-          if (k == 0) {
-            m = cand;
-          } else {
-            const bool grow = cand > m + RENEW || (m == -INFINITY && cand > m);
-            if (__any_sync(~0u, grow)) {
-              // earlier products must have landed before the accumulator is scaled
-              if (!wait_phase(pv_bar(a, it - 1), pv_phase(it - 1), abort_flag, p.err)) ok = false;
-              __syncwarp();
-              fence_after();
-              const float mn = grow ? cand : m;
-              const float f = m == mn ? 1.f : fast_exp2(m - mn);
-              m = mn;
-              l *= f;
-#pragma unroll 1
-              for (int c = 0; c < D; c += 16) {
-                uint32_t o[16];
-                ld16(tO + c, o);
-#pragma unroll
-                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                st16(tO + c, o);
-              }
-            }
-          }
-          const float mm = m == -INFINITY ? 0.f : -m;
-          float2 sum = make_float2(0.f, 0.f);
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t w[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              float2 x = fma2(__uint_as_float(v[c][2 * e]), __uint_as_float(v[c][2 * e + 1]), rs,
-                              mm);
-              x.x = fast_exp2(x.x);
-              x.y = fast_exp2(x.y);
-              sum = add2(sum, x);
-              w[e] = pack_bf16x2(x.x, x.y);
-            }
-            st16(tS + 16 * c, w);
-          }
-          l += sum.x + sum.y;
-          st_wait();
-        }
-        if (!__all_sync(~0u, ok)) {
-          ok = false;
-          break;
-        }
         // values of keys past the last one, whatever their page holds there,
         // must not meet a weight of zero
         const int left = s.L - t0;
@@ -335,9 +349,58 @@ __global__ void __launch_bounds__(THREADS, 1)
                     make_uint4(0, 0, 0, 0);
           fence_async_smem();
         }
-        fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(pready + 8 * a);
+        const int lim = seen - t0;  // columns the row sees
+        const bool all = __all_sync(~0u, lim >= BN);
+        float mm = 0.f;
+        f32x2 sum = 0;
+        if (any_live) {
+          const float top = all ? row_max<false>(tS, BN) : row_max<true>(tS, lim);
+          const float cand = top == -INFINITY ? -INFINITY : top * rs;
+          if (k == 0) {
+            m = cand;
+          } else {
+            const bool grow = !(cand <= m + RENEW);  // also the first NaN of a row
+            if (__any_sync(~0u, grow)) {
+              // earlier products must have landed before the accumulator is scaled
+              if (!wait_phase(pv_bar(a, it - 1), pv_phase(it - 1), abort_flag, p.err)) ok = false;
+              __syncwarp();
+              fence_after();
+              const float mn = grow ? cand : m;
+              const float f = m == mn ? 1.f : fast_exp2(m - mn);
+              m = mn;
+              l *= f;
+#pragma unroll 1
+              for (int c = 0; c < D; c += 16) {
+                uint32_t o[16];
+                ld16(tO + c, o);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                st16(tO + c, o);
+              }
+              if (!__all_sync(~0u, ok)) {
+                ok = false;
+                break;
+              }
+            }
+          }
+          mm = m == -INFINITY ? 0.f : -m;
+        }
+        // the weights of 64 keys at a time, so that the first ones' product
+        // starts while the others are computed
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          if (any_live) {
+            if (all)
+              row_weights<false>(tS, half, BN, rs, mm, sum);
+            else
+              row_weights<true>(tS, half, lim, rs, mm, sum);
+          }
+          fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(pready + 16 * a + 8 * half);
+        }
+        const float2 ss = halves_of(sum);
+        l += ss.x + ss.y;
       }
       if (!ok) break;
       // output: the row itself, or its state where the row tile is split
@@ -353,8 +416,24 @@ __global__ void __launch_bounds__(THREADS, 1)
       const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
       uint16_t *out = p.out + ((int64_t)(s.start + tok) * p.Hq + s.h * p.G +
                                (row - (int64_t)tok * p.G)) * D;
-      float *part = p.w.part +
-                    ((int64_t)(2 * blockIdx.x + (s.k0 == 0 ? 1 : 0)) * ROWS + a * BM + r) * (D + 2);
+      auto write_out = [&](int c, const uint32_t (&o)[32], float inv) {  // 32 dims from c on
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          uint4 q;
+          uint32_t *qq = reinterpret_cast<uint32_t *>(&q);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const float y = __uint_as_float(o[8 * e + 2 * x]),
+                        z = __uint_as_float(o[8 * e + 2 * x + 1]);
+            qq[x] = inv == 0.f ? 0u : pack_bf16x2(y * inv, z * inv);
+          }
+          *reinterpret_cast<uint4 *>(out + c + 8 * e) = q;
+        }
+      };
+      // states of a split row tile: [half][d + 2][128 rows], a row per lane
+      const Split split(s, p);
+      constexpr int HALF = (D + 2) * BM;
+      const int64_t mine = (split.record(blockIdx.x) * HALVES + a) * HALF + r;
 #pragma unroll 1
       for (int c = 0; c < D; c += 32) {
         uint32_t o[32];
@@ -365,36 +444,52 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = 0;
         }
-        if (live && whole) {
+        if (whole) {
+          if (live) write_out(c, o, inv);
+        } else {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            uint4 q;
-            uint32_t *qq = reinterpret_cast<uint32_t *>(&q);
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const float y = __uint_as_float(o[8 * e + 2 * x]),
-                          z = __uint_as_float(o[8 * e + 2 * x + 1]);
-              qq[x] = inv == 0.f ? 0u : pack_bf16x2(y * inv, z * inv);
-            }
-            *reinterpret_cast<uint4 *>(out + c + 8 * e) = q;
-          }
-        } else if (live) {
-#pragma unroll
-          for (int e = 0; e < 32; e += 2)
-            *reinterpret_cast<float2 *>(part + c + e) =
-                make_float2(__uint_as_float(o[e]), __uint_as_float(o[e + 1]));
+          for (int e = 0; e < 32; ++e) p.w.part[mine + (c + e) * BM] = __uint_as_float(o[e]);
         }
       }
-      if (live && !whole) *reinterpret_cast<float2 *>(part + D) = make_float2(m, l);
+      if (!whole) {
+        p.w.part[mine + D * BM] = m;
+        p.w.part[mine + (D + 1) * BM] = l;
+        if (last_to_arrive(split, p, a, 1 + a, BM, r == 0, join_flag + a)) {
+          float mj = -INFINITY, lj = 0.f;
+          for (int64_t c = split.c0; c <= split.c1; ++c) {
+            const float *q = p.w.part + (split.record(c) * HALVES + a) * HALF + r;
+            const float mc = __ldcg(q + D * BM), lc = __ldcg(q + (D + 1) * BM);
+            if (lc == 0.f) continue;
+            const float mn = fmaxf(mj, mc);
+            lj = lj * (mj == mn ? 1.f : fast_exp2(mj - mn)) + lc * fast_exp2(mc - mn);
+            mj = mn;
+          }
+          const float ij = lj > 0.f || lj != lj ? 1.f / lj : 0.f;
+#pragma unroll 1
+          for (int d0 = 0; d0 < D; d0 += 32) {
+            float o[32] = {};
+            for (int64_t c = split.c0; c <= split.c1; ++c) {
+              const float *q = p.w.part + (split.record(c) * HALVES + a) * HALF + r;
+              const float lc = __ldcg(q + (D + 1) * BM);
+              if (lc == 0.f) continue;
+              const float w = fast_exp2(__ldcg(q + D * BM) - mj);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = fmaf(w, __ldcg(q + (d0 + e) * BM), o[e]);
+            }
+            uint32_t ob[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) ob[e] = __float_as_uint(o[e]);
+            if (live) write_out(d0, ob, ij);
+          }
+        }
+      }
       if (s.nk > 0) {
         fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(ofree + 8 * a);
       }
     }
-  } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(REST_REGS));
-  if (warp == MMA_WARP) {
+  } else if (warp == MMA_WARP) {
     // ---------------- MMA issue: the halves in turn, values of a tile and then
     // the scores of the next
     constexpr uint32_t id_s = idesc_f16(BM, BN, 0);
@@ -436,17 +531,24 @@ __global__ void __launch_bounds__(THREADS, 1)
           const uint32_t it = a ? it1 : it0, sa = a ? sg1 : sg;
           if (a == 0 && !(ok = wait(vfull + 8 * vs, (kt / C::SV) & 1u))) break;
           if (k == 0 && sa > 0 && !(ok = wait(ofree + 8 * a, (sa - 1) & 1u))) break;
-          if (!(ok = wait(pready + 8 * a, it & 1u))) break;
-          if (elect_one()) {
-            const uint64_t dv = dv0 + (uint64_t)((vs * C::TILE) >> 4);
+          const uint64_t dv = dv0 + (uint64_t)((vs * C::TILE) >> 4);
+          for (int half = 0; half < 2; ++half) {  // of the tile's keys
+            if (!(ok = wait(pready + 16 * a + 8 * half, it & 1u))) break;
+            if (elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < BN / 16; ++kk)
-              mma_ts(tmem + C::COL_O + a * D, tmem + a * BN + 8 * kk,
-                     dv + (uint64_t)((kk * 2048) >> 4), id_o, (k > 0 || kk > 0) ? 1u : 0u);
-            commit(pv_bar(a, it));
-            if (a == na - 1) commit(vempty + 8 * vs);
+              for (int i = 0; i < BN / 32; ++i) {
+                const int kk = half * (BN / 32) + i;
+                mma_ts(tmem + C::COL_O + a * D, tmem + a * BN + 8 * kk,
+                       dv + (uint64_t)((kk * 2048) >> 4), id_o, (k > 0 || kk > 0) ? 1u : 0u);
+              }
+              if (half) {
+                commit(pv_bar(a, it));
+                if (a == na - 1) commit(vempty + 8 * vs);
+              }
+            }
+            __syncwarp();
           }
-          __syncwarp();
+          if (!ok) break;
           if (k + 1 < s.nk) {
             if (a == 0 && !(ok = wait(kfull + 8 * nx, ((kt + 1) / C::SK) & 1u))) break;
             scores(a, kt + 1);
@@ -467,7 +569,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (elect_one()) commit(fin);
     __syncwarp();
     drain_wait(fin, 0);
-  } else if (warp == LOAD_WARP) {
+  } else {
     // ---------------- copies: queries of a segment, K and V of each key tile
     bool ok = true;
     uint32_t kt = 0, sg = 0;
@@ -530,7 +632,6 @@ __global__ void __launch_bounds__(THREADS, 1)
         drain_wait(vfull + 8 * (i % C::SV), (i / C::SV) & 1u);
     }
   }
-  }
   fence_before();
   __syncthreads();
   if (warp == MMA_WARP) {
@@ -542,9 +643,8 @@ __global__ void __launch_bounds__(THREADS, 1)
 }
 
 template <int D>
-cudaError_t launch_many_t(Params p, bool f32, const ChunkArgs &a, cudaStream_t stream) {
+cudaError_t launch_many_t(const Params &p, const ChunkArgs &a, cudaStream_t stream) {
   using C = Cfg<D>;
-  p.rows = ROWS;
   CUtensorMap map_u, map_k, map_v;
   const int64_t rows = p.N * p.Hq;
   if (!tc::make_map(&map_u, p.w.U, rows, D, D, BM) ||
@@ -552,7 +652,7 @@ cudaError_t launch_many_t(Params p, bool f32, const ChunkArgs &a, cudaStream_t s
       !tc::make_map(&map_v, a.value_pages, (uint64_t)p.num_pages * p.Hkv * p.P, D, D, GRAN))
     return cudaErrorInvalidValue;
   const int64_t prep = 1 + (rows + PREP_THREADS / 32 - 1) / (PREP_THREADS / 32);
-  if (f32)
+  if (a.q_f32)
     prep_kernel<D, true><<<(unsigned)prep, PREP_THREADS, 0, stream>>>(p);
   else
     prep_kernel<D, false><<<(unsigned)prep, PREP_THREADS, 0, stream>>>(p);
@@ -561,80 +661,24 @@ cudaError_t launch_many_t(Params p, bool f32, const ChunkArgs &a, cudaStream_t s
   e = launch_expand_paged(p.codes, p.norms, p.num_pages, p.P, p.table, p.max_pages, p.lens, p.B,
                           p.Hkv, p.max_len, p.S, a.m, D, p.w.keys, stream);
   if (e != cudaSuccess) return e;
-  // the register split is drawn from what the block is launched with
-  cudaFuncAttributes fa;
-  e = cudaFuncGetAttributes(&fa, attend_kernel<D>);
-  if (e != cudaSuccess) return e;
-  if (fa.numRegs != REGS) return cudaErrorInvalidConfiguration;
   e = cudaFuncSetAttribute(attend_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
-  e = launch_after(attend_kernel<D>, p.blocks, THREADS, C::SMEM, stream, map_u, map_k, map_v, p);
-  if (e != cudaSuccess) return e;
-  return launch_after(combine_kernel<D>, (rows + CMB_WARPS - 1) / CMB_WARPS, CMB_WARPS * 32, 0,
-                      stream, p);
-}
-
-struct Sizes {
-  size_t plan, b_unit, b_tile, seq, mt_pre, U, rs, part, keys, total;
-};
-Sizes sizes(int64_t N, int B, int Hq, int Hkv, int64_t max_len, int m, int d) {
-  auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
-  const int G = Hq / Hkv;
-  Sizes z{};
-  z.plan = up(sizeof(Plan));
-  z.b_unit = up((size_t)(B + 1) * 8);
-  z.b_tile = up((size_t)B * 4);
-  z.seq = up((size_t)B * 4);
-  z.mt_pre = up(((size_t)N * G / ROWS + 2 * (size_t)B + 1) * 4);
-  z.U = up((size_t)N * Hq * d * 2);
-  z.rs = up((size_t)N * Hq * 4);
-  z.part = up((size_t)2 * SM_COUNT * ROWS * (d + 2) * 4);
-  z.keys = (size_t)B * Hkv * ((max_len + BN - 1) / BN) * BN * d * 2;
-  z.total = z.plan + z.b_unit + z.b_tile + 3 * z.seq + z.mt_pre + z.U + z.rs + z.part + z.keys;
-  return z;
+  return launch_after(attend_kernel<D>, p.blocks, THREADS, C::SMEM, stream, map_u, map_k, map_v, p);
 }
 
 }  // namespace
+
+size_t many_workspace(int64_t N, int B, int Hq, int Hkv, int64_t max_len, int d, Work *w,
+                      void *base) {
+  return lay_out(w, base, N, B, Hq, Hkv, ROWS, d, (size_t)ROWS * (d + 2),
+                 (size_t)B * Hkv * ((max_len + BN - 1) / BN) * BN * d * 2);
+}
+
+cudaError_t launch_many(Params p, const ChunkArgs &a, cudaStream_t stream) {
+  p.rows = ROWS;
+  many_workspace(p.N, p.B, p.Hq, p.Hkv, p.max_len, a.d, &p.w, a.workspace);
+  return a.d == 128 ? launch_many_t<128>(p, a, stream) : launch_many_t<64>(p, a, stream);
+}
+
 }  // namespace chunk
-
-size_t chunk_workspace_bytes(int64_t N, int B, int Hq, int Hkv, int64_t max_len, int m, int d) {
-  return chunk::sizes(N, B, Hq, Hkv, max_len, m, d).total;
-}
-
-cudaError_t launch_chunk(const ChunkArgs &a, cudaStream_t stream) {
-  chunk::Params p{};
-  p.err = device_error_ptr();
-  if (!p.err) return cudaErrorInvalidSymbol;
-  const chunk::Sizes z = chunk::sizes(a.N, a.B, a.Hq, a.Hkv, a.max_len, a.m, a.d);
-  uint8_t *w = static_cast<uint8_t *>(a.workspace);
-  auto take = [&](size_t n) {
-    uint8_t *x = w;
-    w += n;
-    return x;
-  };
-  p.w.plan = reinterpret_cast<chunk::Plan *>(take(z.plan));
-  p.w.b_unit = reinterpret_cast<int64_t *>(take(z.b_unit));
-  p.w.b_tile = reinterpret_cast<int32_t *>(take(z.b_tile));
-  p.w.start = reinterpret_cast<int32_t *>(take(z.seq));
-  p.w.count = reinterpret_cast<int32_t *>(take(z.seq));
-  p.w.len = reinterpret_cast<int32_t *>(take(z.seq));
-  p.w.mt_pre = reinterpret_cast<int32_t *>(take(z.mt_pre));
-  p.w.U = reinterpret_cast<uint16_t *>(take(z.U));
-  p.w.rs = reinterpret_cast<float *>(take(z.rs));
-  p.w.part = reinterpret_cast<float *>(take(z.part));
-  p.w.keys = reinterpret_cast<uint16_t *>(take(z.keys));
-  p.codes = a.sign_pages; p.norms = a.norm_pages;
-  p.table = a.block_table; p.cu = a.cu_seqlens; p.lens = a.seq_lens;
-  p.Q = a.Q; p.q_tok = a.q_tok; p.q_head = a.q_head; p.S = a.S; p.out = a.out;
-  p.B = a.B; p.Hq = a.Hq; p.Hkv = a.Hkv; p.G = a.Hq / a.Hkv; p.P = a.page_tokens;
-  p.max_pages = a.max_pages; p.num_pages = a.num_pages; p.N = a.N; p.max_len = a.max_len;
-  p.key_tiles = (int)((a.max_len + chunk::BN - 1) / chunk::BN);
-  p.scale = a.softmax_scale;
-  const int sms = device_sm_count();
-  p.blocks = sms < chunk::SM_COUNT ? sms : chunk::SM_COUNT;
-  p.min_units = 2;
-  return a.d == 128 ? chunk::launch_many_t<128>(p, a.q_f32, a, stream)
-                    : chunk::launch_many_t<64>(p, a.q_f32, a, stream);
-}
-
 }  // namespace jlk

@@ -154,13 +154,15 @@ __device__ __forceinline__ uint32_t sign_word(const uint32_t (&v)[32]) {
 __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity,
                                            volatile int *abort_flag, int *err,
                                            unsigned long long limit_ns = WAIT_LIMIT_NS) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const unsigned long long t0 = globaltimer();
+  unsigned long long t0 = 0;  // read late: the global timer takes hundreds of clocks
   for (uint32_t it = 1;; ++it) {
     if (mbar_try_wait(bar, parity)) return true;
     if ((it & 63u) == 0) {
       if (*abort_flag) return false;
-      if (globaltimer() - t0 > limit_ns) {
+      const unsigned long long now = globaltimer();
+      if (t0 == 0) {
+        t0 = now;
+      } else if (now - t0 > limit_ns) {
         *abort_flag = 1;
         record_device_error(err, DERR_TC_WAIT_TIMEOUT);
         return false;
