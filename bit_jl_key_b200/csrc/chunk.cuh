@@ -15,11 +15,12 @@
 #include "jl_common.cuh"
 #include "jl_internal.h"
 
+#include <cudaTypedefs.h>
+
 namespace jlk {
 namespace chunk {
 
 constexpr int BN = 128;            // keys of a tile
-constexpr int GRAN = 32;           // keys that surely share a page
 constexpr float RENEW = 8.f;       // log2 growth of a row's maximum that renews it
 constexpr float MIN_SCALE = 1.17549435e-38f;  // of a row: -inf times it stays -inf
 constexpr int PREP_THREADS = 256;
@@ -29,8 +30,14 @@ struct Plan {
   int64_t total;      // units (key tiles, at least one per row tile)
   int64_t quota;      // units per block
 };
+struct Start {        // where a block's run begins
+  int64_t u, end;     // units [u, end); none where u >= end
+  int b, h, mt, k0;   // the unit u: sequence, KV head, row tile, unit of it
+  int n, L, row, units;  // the sequence's tokens, keys, first row; units of the row tile
+};
 struct Work {         // workspace
   Plan *plan;
+  Start *begin;       // [blocks]
   int64_t *b_unit;    // [B + 1] first unit of each sequence
   int32_t *b_tile;    // [B] first entry of its row tiles in mt_pre
   int32_t *start, *count, *len;  // [B] first row, tokens, keys, made safe
@@ -53,6 +60,7 @@ struct Params {
   uint16_t *out;
   int B, Hq, Hkv, G, P, max_pages, num_pages, blocks, min_units, rows;
   int key_tiles;      // of max_len
+  int gran, gran_log; // keys of a tile copied at once, all in one page: 32, 64 or 128
   int64_t N, max_len;
   float scale;        // softmax_scale
   int *err;
@@ -138,13 +146,45 @@ static __device__ __noinline__ void make_plan(const Params &p) {
     }
     __syncthreads();
   }
-  for (int i = threadIdx.x; i < 2 * p.blocks; i += PREP_THREADS) p.w.arrived[i] = 0;
+  const int64_t total = u_done;
+  int64_t quota = (total + p.blocks - 1) / p.blocks;
+  if (quota < p.min_units) quota = p.min_units;
   if (threadIdx.x == 0) {
-    p.w.b_unit[p.B] = u_done;
-    int64_t q = (u_done + p.blocks - 1) / p.blocks;
-    if (q < p.min_units) q = p.min_units;
-    p.w.plan->total = u_done;
-    p.w.plan->quota = q;
+    p.w.b_unit[p.B] = total;
+    p.w.plan->total = total;
+    p.w.plan->quota = quota;
+  }
+  __threadfence_block();
+  __syncthreads();
+  for (int i = threadIdx.x; i < p.blocks; i += PREP_THREADS) {
+    p.w.arrived[2 * i] = p.w.arrived[2 * i + 1] = 0;
+    Start s{};
+    s.u = i * quota;
+    s.end = s.u + quota < total ? s.u + quota : total;
+    if (s.u < total) {
+      int lo = 0, hi = p.B;  // the last b whose first unit is not above u
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (p.w.b_unit[mid] <= s.u) lo = mid; else hi = mid;
+      }
+      s.b = lo;
+      s.n = p.w.count[lo];
+      s.L = p.w.len[lo];
+      s.row = p.w.start[lo];
+      const int64_t u0 = p.w.b_unit[lo], per_head = (p.w.b_unit[lo + 1] - u0) / p.Hkv;
+      s.h = (int)((s.u - u0) / per_head);
+      const int rem = (int)(s.u - u0 - s.h * per_head);
+      const int32_t *pre = p.w.mt_pre + p.w.b_tile[lo];
+      int a = 0, z = (int)(((int64_t)s.n * p.G + p.rows - 1) / p.rows);
+      while (z - a > 1) {
+        const int mid = (a + z) >> 1;
+        if (pre[mid] <= rem) a = mid; else z = mid;
+      }
+      s.mt = a;
+      s.k0 = rem - pre[a];
+      s.units = pre[a + 1] - pre[a];
+    }
+    p.w.begin[i] = s;
   }
 }
 
@@ -164,6 +204,10 @@ __device__ __forceinline__ float load_q(const void *Q, bool f32, int64_t i) {
              : bf16_bits_to_f32(__ldg(static_cast<const uint16_t *>(Q) + i));
 }
 
+// Whatever prep writes is read with __ldcg here: attend may start before prep
+// ends and waits for it (griddep_wait), and a load declared read-only (__ldg)
+// may be moved above that wait.
+
 // A block's run of units, one row tile after another.
 struct Seg {
   int b, h, mt, nt;   // sequence, KV head, row tile, row tiles of the sequence
@@ -174,45 +218,27 @@ struct Seg {
 };
 
 __device__ __forceinline__ void seg_fill(Seg &s, const Params &p) {
-  const int32_t *pre = p.w.mt_pre + __ldg(p.w.b_tile + s.b);
-  const int a = __ldg(pre + s.mt), z = __ldg(pre + s.mt + 1);
-  s.units = z - a;
   const int64_t left = s.end - s.u;
   s.k1 = (int)(left < s.units - s.k0 ? s.k0 + left : s.units);
   const int last = min(s.n - 1, (p.rows * s.mt + p.rows - 1) / p.G);
   s.nk = s.L - s.n + last + 1 > 0 ? s.k1 - s.k0 : 0;
 }
 __device__ __forceinline__ void seg_seq(Seg &s, const Params &p) {
-  s.n = __ldg(p.w.count + s.b);
-  s.L = __ldg(p.w.len + s.b);
-  s.start = __ldg(p.w.start + s.b);
+  s.n = __ldcg(p.w.count + s.b);
+  s.L = __ldcg(p.w.len + s.b);
+  s.start = __ldcg(p.w.start + s.b);
   s.nt = (int)(((int64_t)s.n * p.G + p.rows - 1) / p.rows);
 }
 // First segment of the block; false when it has none.
 __device__ __forceinline__ bool seg_first(Seg &s, const Params &p) {
-  const int64_t total = __ldg(&p.w.plan->total), quota = __ldg(&p.w.plan->quota);
-  s.u = (int64_t)blockIdx.x * quota;
-  s.end = s.u + quota < total ? s.u + quota : total;
-  if (s.u >= total) return false;
-  int lo = 0, hi = p.B;  // the last b whose first unit is not above u
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (__ldg(p.w.b_unit + mid) <= s.u) lo = mid; else hi = mid;
-  }
-  s.b = lo;
-  seg_seq(s, p);
-  const int64_t u0 = __ldg(p.w.b_unit + lo);
-  const int64_t per_head = (__ldg(p.w.b_unit + lo + 1) - u0) / p.Hkv;
-  s.h = (int)((s.u - u0) / per_head);
-  const int rem = (int)(s.u - u0 - s.h * per_head);
-  const int32_t *pre = p.w.mt_pre + __ldg(p.w.b_tile + lo);
-  int a = 0, z = s.nt;
-  while (z - a > 1) {
-    const int mid = (a + z) >> 1;
-    if (__ldg(pre + mid) <= rem) a = mid; else z = mid;
-  }
-  s.mt = a;
-  s.k0 = rem - __ldg(pre + a);
+  const int4 *q = reinterpret_cast<const int4 *>(p.w.begin + blockIdx.x);
+  const int4 x = __ldcg(q), y = __ldcg(q + 1), z = __ldcg(q + 2);
+  s.u = (int64_t)(((uint64_t)(uint32_t)x.y << 32) | (uint32_t)x.x);
+  s.end = (int64_t)(((uint64_t)(uint32_t)x.w << 32) | (uint32_t)x.z);
+  s.b = y.x; s.h = y.y; s.mt = y.z; s.k0 = y.w;
+  s.n = z.x; s.L = z.y; s.start = z.z; s.units = z.w;
+  s.nt = (int)(((int64_t)s.n * p.G + p.rows - 1) / p.rows);
+  if (s.u >= s.end) return false;
   seg_fill(s, p);
   return true;
 }
@@ -230,6 +256,8 @@ __device__ __forceinline__ bool seg_next(Seg &s, const Params &p) {
       } while (s.n == 0);
     }
   }
+  const int32_t *pre = p.w.mt_pre + __ldcg(p.w.b_tile + s.b) + s.mt;
+  s.units = __ldcg(pre + 1) - __ldcg(pre);
   seg_fill(s, p);
   return true;
 }
@@ -255,7 +283,7 @@ __device__ __forceinline__ int page_of(const Params &p, int b, int t) {
 struct Split {
   int64_t c0, c1, first, quota;
   __device__ __forceinline__ Split(const Seg &s, const Params &p) {
-    quota = __ldg(&p.w.plan->quota);
+    quota = __ldcg(&p.w.plan->quota);
     first = s.u - s.k0;
     c0 = first / quota;
     c1 = (first + s.units - 1) / quota;
@@ -312,6 +340,7 @@ inline size_t lay_out(Work *w, void *base, int64_t N, int B, int Hq, int Hkv, in
   };
   Work t;
   t.plan = reinterpret_cast<Plan *>(take(sizeof(Plan)));
+  t.begin = reinterpret_cast<Start *>(take((size_t)SM_COUNT * sizeof(Start)));
   t.b_unit = reinterpret_cast<int64_t *>(take((size_t)(B + 1) * 8));
   t.b_tile = reinterpret_cast<int32_t *>(take((size_t)B * 4));
   t.start = reinterpret_cast<int32_t *>(take((size_t)B * 4));
@@ -326,6 +355,32 @@ inline size_t lay_out(Work *w, void *base, int64_t N, int B, int Hq, int Hkv, in
   t.keys = reinterpret_cast<uint16_t *>(take(keys));
   if (w) *w = t;
   return off;
+}
+
+// A tile's values in shared memory: granule after granule, each as D / 64 boxes
+// of gran rows x 128 bytes (64 dims, 128-byte swizzle), brought by one bulk
+// tensor copy from the pool seen as [D / 64][rows][64].
+inline bool make_value_map(CUtensorMap *map, const uint16_t *values, uint64_t rows, int d,
+                           int gran) {
+  auto fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(tensor_map_encoder());
+  if (!fn) return false;
+  cuuint64_t dims[3] = {64, rows, (cuuint64_t)d / 64};
+  cuuint64_t strides[2] = {(cuuint64_t)d * 2, 128};
+  cuuint32_t box[3] = {64, (cuuint32_t)gran, (cuuint32_t)d / 64};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t *>(values), dims,
+            strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// Byte offset of key r of a tile in it (its first 64 dims); the others follow
+// gran * 128 bytes apart.
+__device__ __forceinline__ uint32_t value_offset(int r, const Params &p, int D) {
+  const int g = r >> p.gran_log;
+  return (uint32_t)((g << p.gran_log) * D * 2 + (r & (p.gran - 1)) * 128);
+}
+
+__device__ __forceinline__ void prefetch_map(const CUtensorMap *map) {
+  asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
 
 // The kernels for few and for many rows (chunk_few.cu, chunk_tc.cu): the

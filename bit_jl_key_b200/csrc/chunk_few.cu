@@ -25,8 +25,8 @@
 // Kernels: prep (u and the plan, chunk.cuh), attend.  Warps of attend: 0-3
 // softmax and output; then 8 (4 with 64 rows) that expand, a quarter of the
 // keys each and, when 8, alternate chunks; one for MMA issue and tensor memory;
-// one for copies (V by bulk tensor copies, codes and norms by bulk copies: the
-// 32 keys of a granule lie side by side in one page).  Every wait is bounded;
+// one for copies (V by a bulk tensor copy, codes and norms by a bulk copy per
+// granule, whose keys lie side by side in one page).  Every wait is bounded;
 // one that runs out records DERR_TC_WAIT_TIMEOUT.
 #include "chunk.cuh"
 #include "jl_tc.cuh"
@@ -41,61 +41,66 @@ namespace {
 
 constexpr int SM_WARPS = 4, EXP_WARP0 = SM_WARPS;
 constexpr int BOX = BN * 128;      // 128 keys of 64 16-bit elements
-constexpr int RING = 8;            // Z chunks in tensor memory, 32 columns each
+constexpr int ZRING = 2;           // groups of Z chunks in tensor memory
 
 // Place of coordinate i in the contraction's order (see the file's head).
 __host__ __device__ __forceinline__ int k_slot(int i) {
   return (i & ~31) + 2 * (i & 15) + ((i >> 4) & 1);
 }
 
-__device__ __forceinline__ float load_q(const void *Q, bool f32, int64_t i) {
-  return f32 ? __ldg(static_cast<const float *>(Q) + i)
-             : bf16_bits_to_f32(__ldg(static_cast<const uint16_t *>(Q) + i));
-}
+constexpr int PREP_ROWS = 8;
 
-constexpr int PREP_ROWS = 16;
+// Block 0 makes the plan; the others project PREP_ROWS rows each: the sketch
+// goes through shared memory (rows 16 bytes longer than their entries, so that
+// neighbouring rows lie in different banks), a thread takes one sketch row and
+// meets every query row as a broadcast.
+template <int M, int D>
+constexpr int prep_smem() { return M * (D * 2 + 16); }
 
-// Block 0 makes the plan; the others project PREP_ROWS rows each.  A thread
-// holds one sketch row in registers and meets every query row in shared
-// memory (a broadcast), m threads side by side.
 template <int M, int D, bool F32>
 __global__ void __launch_bounds__(PREP_THREADS) prep_kernel(const Params p) {
+  griddep_launch_dependents();  // attend may set itself up meanwhile
   if (blockIdx.x == 0) {
     make_plan(p);
     return;
   }
+  extern __shared__ __align__(16) uint8_t sketch[];
   __shared__ __align__(16) float q[PREP_ROWS][D];
   __shared__ float top[PREP_ROWS][PREP_THREADS / 32];
-  const int64_t rows = p.N * p.G;                    // of a KV head
-  const int64_t total = rows * p.Hkv;
-  const int64_t r0 = (int64_t)(blockIdx.x - 1) * PREP_ROWS;
+  constexpr int LD = D * 2 + 16;
+  for (int i = threadIdx.x; i < M * (D / 8); i += PREP_THREADS) {
+    const int r = i / (D / 8), c = i % (D / 8);
+    cp_async_16(smem_u32(sketch + r * LD + 16 * c), p.S + (int64_t)r * D + 8 * c, 16);
+  }
+  cp_async_commit();
+  const uint32_t rows = (uint32_t)(p.N * p.G);       // of a KV head
+  const uint32_t total = rows * p.Hkv;
+  const uint32_t r0 = (blockIdx.x - 1) * PREP_ROWS;
   const float sgn = p.scale < 0.f ? -1.f : 1.f;
   for (int i = threadIdx.x; i < PREP_ROWS * D; i += PREP_THREADS) {
-    const int64_t r = r0 + i / D;
+    const uint32_t r = r0 + i / D;
     float v = 0.f;
     if (r < total) {
-      const int h = (int)(r / rows);
-      const int64_t tg = r - h * rows, tok = tg / p.G;
-      const int g = (int)(tg - tok * p.G);
+      const uint32_t h = r / rows, tg = r - h * rows, tok = tg / p.G, g = tg - tok * p.G;
       v = sgn * load_q(p.Q, F32, tok * p.q_tok + (int64_t)(h * p.G + g) * p.q_head + i % D);
     }
     q[i / D][i % D] = v;
   }
+  cp_async_wait<0>();
   __syncthreads();
-  // SPLIT threads groups share the rows when m < 256; m = 512 takes two passes
+  // groups of threads share the rows when m < 256; m = 512 takes two passes
   constexpr int TH = M < PREP_THREADS ? M : PREP_THREADS;
   constexpr int PASS = M / TH, GROUPS = PREP_THREADS / TH, RG = PREP_ROWS / GROUPS;
   const int grp = threadIdx.x / TH;
   float acc[PASS][RG];
 #pragma unroll
   for (int ps = 0; ps < PASS; ++ps) {
-    const int i = threadIdx.x % TH + ps * TH;
+    const uint8_t *s = sketch + (threadIdx.x % TH + ps * TH) * LD;
 #pragma unroll
     for (int r = 0; r < RG; ++r) acc[ps][r] = 0.f;
-    const uint4 *s = reinterpret_cast<const uint4 *>(p.S + (int64_t)i * D);
 #pragma unroll 4
     for (int c = 0; c < D / 8; ++c) {
-      const uint4 w = __ldg(s + c);
+      const uint4 w = *reinterpret_cast<const uint4 *>(s + 16 * c);
       const float x[8] = {__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u),
                           __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u),
                           __uint_as_float(w.z << 16), __uint_as_float(w.z & 0xffff0000u),
@@ -127,14 +132,14 @@ __global__ void __launch_bounds__(PREP_THREADS) prep_kernel(const Params p) {
   __syncthreads();
 #pragma unroll
   for (int r = 0; r < RG; ++r) {
-    const int64_t row = r0 + grp * RG + r;
+    const uint32_t row = r0 + grp * RG + r;
     if (row >= total) break;
     float v = 0.f;
     for (int w = 0; w < RW; ++w) v = fmaxf(v, top[grp * RG + r][w]);
     const float2 f = row_power(v);
 #pragma unroll
     for (int ps = 0; ps < PASS; ++ps)
-      p.w.U[row * M + k_slot(threadIdx.x % TH + ps * TH)] =
+      p.w.U[(int64_t)row * M + k_slot(threadIdx.x % TH + ps * TH)] =
           __half_as_ushort(__float2half_rn(acc[ps][r] * f.x));
     if (threadIdx.x % TH == 0)
       p.w.rs[row] = fmaxf((float)(1.2533141373155002512 / M * 1.4426950408889634074) *
@@ -143,6 +148,9 @@ __global__ void __launch_bounds__(PREP_THREADS) prep_kernel(const Params p) {
   }
 }
 
+// ---------------------------------------------------------------------------
+// attend
+
 template <int K, int D, int NR>
 struct Cfg {
   // warps: with 64 rows a softmax thread holds twice the scores and sums, and
@@ -150,7 +158,9 @@ struct Cfg {
   static constexpr int EXP_PARTS = NR == 64 ? 1 : 2, EXP_WARPS = 4 * EXP_PARTS;
   static constexpr int MMA_WARP = EXP_WARP0 + EXP_WARPS, LOAD_WARP = MMA_WARP + 1;
   static constexpr int THREADS = (LOAD_WARP + 1) * 32;
-  static constexpr int KCH = K / 64;                 // 64-coordinate chunks
+  static constexpr int KCH = K / 64;                 // 64-coordinate chunks of 32 columns,
+  static constexpr int GCH = KCH < 4 ? KCH : 4;      // handed over in groups of up to four
+  static constexpr int NG = KCH / GCH, GCOLS = GCH * 32;
   static constexpr int DB = D / 64;                  // boxes of a V tile
   static constexpr int U_BYTES = KCH * NR * 128;
   static constexpr int P_ROW = NR * 2, P_BYTES = BN * P_ROW;
@@ -168,17 +178,19 @@ struct Cfg {
   // tensor memory columns
   static constexpr int COL_O = 2 * NR, COL_Z = 3 * NR < 128 ? 128 : 256, TMEM = 512;
   static_assert(ST >= 2, "stages");
-  static_assert(COL_Z + RING * 32 <= TMEM && COL_O + NR <= COL_Z, "tensor memory");
+  static_assert(COL_Z + ZRING * GCOLS <= TMEM && COL_O + NR <= COL_Z, "tensor memory");
   static_assert(SMEM <= 227 * 1024 && 2 * P_BYTES >= BOX, "shared memory");
 };
 
 // Operands whose rows lie along K (V^T: dims contiguous within a key; P^T: rows
 // contiguous within a key): 128-byte (64 elements) or 64-byte (32 elements)
-// swizzle, `group` bytes from 8 keys to the next 8, 64-dim boxes BOX apart.
-__device__ __forceinline__ uint64_t desc_mn(uint32_t addr, uint32_t group, uint32_t swizzle) {
+// swizzle, `group` bytes from 8 keys to the next 8, `box` bytes from 64 rows or
+// dims to the next 64.
+__device__ __forceinline__ uint64_t desc_mn(uint32_t addr, uint32_t box, uint32_t group,
+                                            uint32_t swizzle) {
   uint64_t d = 0;
   d |= (uint64_t)((addr >> 4) & 0x3FFFu);
-  d |= (uint64_t)((uint32_t)BOX >> 4) << 16;
+  d |= (uint64_t)(box >> 4) << 16;
   d |= (uint64_t)(group >> 4) << 32;
   d |= (uint64_t)1u << 46;
   d |= (uint64_t)swizzle << 61;
@@ -202,6 +214,7 @@ struct Rows {
   float part[SM_WARPS][NR];   // a maximum or sum of each warp
   float sum[NR];
   int seen[NR];               // keys the row sees
+  int out[NR];                // row of the output
 };
 
 // The 32 values of each lane reduced over the warp: lane j gets value j's.
@@ -239,7 +252,7 @@ __global__ void __launch_bounds__(Cfg<K, D, NR>::THREADS, 1)
     nbar += n;
     return a;
   };
-  const uint32_t full = bars(C::ST), empty = bars(C::ST), zfull = bars(RING), zempty = bars(RING),
+  const uint32_t full = bars(C::ST), empty = bars(C::ST), zfull = bars(ZRING), zempty = bars(ZRING),
                  sfull = bars(2), pready = bars(2), pvdone = bars(2), ufull = bars(1),
                  uempty = bars(1), ofree = bars(1), fin = bars(1);
   uint32_t *holder = reinterpret_cast<uint32_t *>(g + OFF_BAR + 496);
@@ -252,8 +265,8 @@ __global__ void __launch_bounds__(Cfg<K, D, NR>::THREADS, 1)
       mbar_init(full + 8 * i, 1);
       mbar_init(empty + 8 * i, EXP_WARPS + 1);  // codes read by each warp, V by the product
     }
-    for (int i = 0; i < RING; ++i) {
-      mbar_init(zfull + 8 * i, 4);              // a warp per quarter of the keys
+    for (int i = 0; i < ZRING; ++i) {
+      mbar_init(zfull + 8 * i, EXP_WARPS);
       mbar_init(zempty + 8 * i, 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -274,6 +287,10 @@ __global__ void __launch_bounds__(Cfg<K, D, NR>::THREADS, 1)
         "tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::"r"(smem_u32(holder)),
         "n"(C::TMEM)
         : "memory");
+  }
+  if (warp == C::LOAD_WARP && lane == 0) {
+    prefetch_map(&map_u);
+    prefetch_map(&map_v);
   }
   fence_before();
   __syncthreads();
@@ -308,9 +325,11 @@ __global__ void __launch_bounds__(Cfg<K, D, NR>::THREADS, 1)
       auto token = [&](int j) { return (int)((row0 + j) / p.G); };
       if (r < NR) {
         const int64_t urow = ((int64_t)s.h * p.N + s.start) * p.G + row0 + r;
-        rows.scale[r] = r < nrow ? __ldg(p.w.rs + urow) : MIN_SCALE;
+        rows.scale[r] = r < nrow ? __ldcg(p.w.rs + urow) : MIN_SCALE;
         rows.seen[r] = r < nrow ? min(s.L, max(0, s.L - s.n + token(r) + 1)) : 0;
         rows.neg[r] = 0.f;
+        const int tok = token(r);
+        rows.out[r] = (s.start + tok) * p.Hq + s.h * p.G + (int)(row0 + r - (int64_t)tok * p.G);
       }
       sync();
       // the first key that some row does not see
@@ -436,11 +455,11 @@ __global__ void __launch_bounds__(Cfg<K, D, NR>::THREADS, 1)
         // values of keys past the last one, whatever their page holds there,
         // must not meet a weight of zero
         if (t >= s.L) {  // (the tile's copies have landed: its scores are there)
-          uint8_t *V = g + C::OFF_ST + (it % C::ST) * C::STAGE + r * 128;
+          uint8_t *V = g + C::OFF_ST + (it % C::ST) * C::STAGE + value_offset(r, p, D);
           for (int x = 0; x < C::DB; ++x)
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-              *reinterpret_cast<uint4 *>(V + x * BOX + 16 * e) = make_uint4(0, 0, 0, 0);
+              *reinterpret_cast<uint4 *>(V + x * p.gran * 128 + 16 * e) = make_uint4(0, 0, 0, 0);
         }
         fence_async_smem();
         fence_before();
@@ -470,10 +489,10 @@ __global__ void __launch_bounds__(Cfg<K, D, NR>::THREADS, 1)
         rows.sum[r] = (rows.part[0][r] + rows.part[1][r]) + (rows.part[2][r] + rows.part[3][r]);
       sync();
       const bool whole = s.k0 == 0 && s.k1 == s.units;
-      auto out_at = [&](int j) -> uint16_t * {
-        const int tok = token(j);
-        return p.out + ((int64_t)(s.start + tok) * p.Hq + s.h * p.G +
-                        (row0 + j - (int64_t)tok * p.G)) * D + r;
+      auto write = [&](int j, float x) {  // dim r of row j
+        const float sum = rows.sum[j];
+        const float y = sum == 0.f ? 0.f : __fdividef(x, sum);
+        p.out[(int64_t)rows.out[j] * D + r] = __bfloat16_as_ushort(__float2bfloat16_rn(y));
       };
       // states of a split row tile: [NR][d + 2]
       const Split split(s, p);
@@ -488,14 +507,10 @@ __global__ void __launch_bounds__(Cfg<K, D, NR>::THREADS, 1)
           for (int e = 0; e < 16; ++e) {
             const int j = 16 * q + e;
             if (j >= nrow) break;
-            if (whole) {
-              const float sum = rows.sum[j];
-              *out_at(j) = sum == 0.f ? (uint16_t)0
-                                      : __bfloat16_as_ushort(__float2bfloat16_rn(
-                                            __uint_as_float(o[e]) / sum));
-            } else {
+            if (whole)
+              write(j, __uint_as_float(o[e]));
+            else
               mine[j * (D + 2) + r] = __uint_as_float(o[e]);
-            }
           }
         }
       }
@@ -508,54 +523,62 @@ __global__ void __launch_bounds__(Cfg<K, D, NR>::THREADS, 1)
         if (r < nrow) *reinterpret_cast<float2 *>(mine + r * (D + 2) + D) =
             make_float2(-rows.neg[r], rows.sum[r]);
         if (last_to_arrive(split, p, 0, 1, SM_WARPS * 32, r == 0, join_flag)) {
-          // the joined maximum and sum of each row
-          if (r < nrow) {
+          // the joined maximum and sum of each row, then its accumulators,
+          // the loads of a record's rows side by side
+          auto record = [&](int64_t c) {
+            return p.w.part + split.record(c) * (int64_t)(NR * (D + 2));
+          };
+          if (r < NR) {
             float m = -INFINITY, sum = 0.f;
-            for (int64_t c = split.c0; c <= split.c1; ++c) {
-              const float2 ml = __ldcg(reinterpret_cast<const float2 *>(
-                  p.w.part + split.record(c) * (int64_t)(NR * (D + 2)) + r * (D + 2) + D));
-              if (ml.y == 0.f) continue;
-              const float now = fmaxf(m, ml.x);
-              sum = sum * (m == now ? 1.f : fast_exp2(m - now)) + ml.y * fast_exp2(ml.x - now);
-              m = now;
-            }
+            if (r < nrow)
+              for (int64_t c = split.c0; c <= split.c1; ++c) {
+                const float2 ml =
+                    __ldcg(reinterpret_cast<const float2 *>(record(c) + r * (D + 2) + D));
+                if (ml.y == 0.f) continue;
+                const float now = fmaxf(m, ml.x);
+                sum = sum * (m == now ? 1.f : fast_exp2(m - now)) + ml.y * fast_exp2(ml.x - now);
+                m = now;
+              }
             rows.neg[r] = -m;
             rows.sum[r] = sum;
           }
-          sync();
-          if (r < D) {
-            for (int j0 = 0; j0 < nrow; j0 += 8) {
-              float o[8] = {};
-              for (int64_t c = split.c0; c <= split.c1; ++c) {
-                const float *q = p.w.part + split.record(c) * (int64_t)(NR * (D + 2));
+          float o[NR];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                  const int j = min(j0 + e, nrow - 1);
-                  const float2 ml =
-                      __ldcg(reinterpret_cast<const float2 *>(q + j * (D + 2) + D));
-                  const float x = __ldcg(q + j * (D + 2) + r);
-                  if (ml.y != 0.f) o[e] = fmaf(fast_exp2(ml.x + rows.neg[j]), x, o[e]);
-                }
+          for (int j = 0; j < NR; ++j) o[j] = 0.f;
+          for (int64_t c = split.c0; c <= split.c1; ++c) {
+            const float *q = record(c);
+            if (r < NR) {
+              float w = 0.f;
+              if (r < nrow) {
+                const float2 ml = __ldcg(reinterpret_cast<const float2 *>(q + r * (D + 2) + D));
+                if (ml.y != 0.f) w = fast_exp2(ml.x + rows.neg[r]);
               }
-#pragma unroll
-              for (int e = 0; e < 8; ++e)
-                if (j0 + e < nrow) {
-                  const float sum = rows.sum[j0 + e];
-                  *out_at(j0 + e) =
-                      sum == 0.f ? (uint16_t)0
-                                 : __bfloat16_as_ushort(__float2bfloat16_rn(o[e] / sum));
-                }
+              rows.factor[r] = w;
             }
+            sync();
+            if (r < D) {
+#pragma unroll
+              for (int j = 0; j < NR; ++j) {
+                const float x = j < nrow ? __ldcg(q + j * (D + 2) + r) : 0.f;
+                o[j] = fmaf(rows.factor[j], x, o[j]);
+              }
+            }
+            sync();
+          }
+          if (r < D) {
+#pragma unroll
+            for (int j = 0; j < NR; ++j)
+              if (j < nrow) write(j, o[j]);
           }
         }
       }
       sync();  // the row arrays are free for the next row tile
     }
   } else if (warp < MMA_WARP) {
-    // ---------------- expand: quarter q of the keys, chunks pt, pt + 2, ..
+    // ---------------- expand: quarter q of the keys, chunks pt, pt + EXP_PARTS, ..
     const int q = warp & 3, pt = (warp - EXP_WARP0) >> 2;
     const int r = 32 * q + lane;
-    constexpr int KP = (C::KCH + EXP_PARTS - 1) / EXP_PARTS;
+    constexpr int KP = (C::GCH + EXP_PARTS - 1) / EXP_PARTS;  // of a group
     const uint32_t tz = tmem + ((uint32_t)(32 * q) << 16) + C::COL_Z;
     bool ok = true;
     for (; ok && more; more = seg_next(s, p)) {
@@ -566,33 +589,38 @@ __global__ void __launch_bounds__(Cfg<K, D, NR>::THREADS, 1)
           break;
         }
         const uint8_t *stage = g + C::OFF_ST + st * C::STAGE + C::ST_V;
-        uint2 w[KP];
+        uint2 w[C::NG * KP];
 #pragma unroll
-        for (int i = 0; i < KP; ++i)
-          if (pt + EXP_PARTS * i < C::KCH)
-            w[i] = *reinterpret_cast<const uint2 *>(stage + r * C::CODE_ROW +
-                                                    8 * (pt + EXP_PARTS * i));
+        for (int i = 0; i < C::NG * KP; ++i) {
+          const int kc = (i / KP) * C::GCH + pt + EXP_PARTS * (i % KP);
+          if (pt + EXP_PARTS * (i % KP) < C::GCH)
+            w[i] = *reinterpret_cast<const uint2 *>(stage + r * C::CODE_ROW + 8 * kc);
+        }
         const uint32_t n16 = *reinterpret_cast<const uint16_t *>(stage + C::ST_C + 2 * r);
         const uint32_t key = 0x80008000u ^ (n16 << 16 | n16);  // bit set: +norm
         __syncwarp();
         if (lane == 0) mbar_arrive(empty + 8 * st);
 #pragma unroll
-        for (int i = 0; i < KP; ++i) {
-          const int kc = pt + EXP_PARTS * i;
-          if (kc >= C::KCH) break;
-          const uint32_t c = it * C::KCH + kc, slot = c % RING;
-          if (!wait_phase(zempty + 8 * slot, ((c / RING) & 1u) ^ 1u, abort_flag, p.err)) {
+        for (int gr = 0; gr < C::NG; ++gr) {
+          const uint32_t c = it * C::NG + gr, slot = c % ZRING;
+          if (!wait_phase(zempty + 8 * slot, ((c / ZRING) & 1u) ^ 1u, abort_flag, p.err)) {
             ok = false;
             break;
           }
-          uint32_t z[32];
+          fence_after();  // the products that read this slot before
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            z[j] = ((w[i].x << (15 - j)) & 0x80008000u) ^ key;
-            z[16 + j] = ((w[i].y << (15 - j)) & 0x80008000u) ^ key;
+          for (int i = 0; i < KP; ++i) {
+            const int kc = pt + EXP_PARTS * i;
+            if (kc >= C::GCH) break;
+            const uint2 x = w[gr * KP + i];
+            uint32_t z[32];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              z[j] = ((x.x << (15 - j)) & 0x80008000u) ^ key;
+              z[16 + j] = ((x.y << (15 - j)) & 0x80008000u) ^ key;
+            }
+            st32(tz + C::GCOLS * slot + 32 * kc, z);
           }
-          fence_after();  // the product that read this slot before
-          st32(tz + 32 * slot, z);
           st_wait();
           fence_before();
           __syncwarp();
@@ -606,8 +634,13 @@ __global__ void __launch_bounds__(Cfg<K, D, NR>::THREADS, 1)
     constexpr uint32_t id_o = idesc_f16(BN, NR, 1) | (1u << 15) | (1u << 16);
     constexpr uint32_t P_GROUP = 8 * C::P_ROW, P_SWZ = NR == 64 ? 2u : 4u;
     const uint64_t du0 = desc_sw128(base);
-    const uint64_t dv0 = desc_mn(base + C::OFF_ST, 1024, 2);
-    const uint64_t dp0 = desc_mn(base + C::OFF_P, P_GROUP, P_SWZ);
+    // (with 64 dims the upper half of the product reads whatever follows, as
+    // dims that are not there; nothing looks at it)
+    const uint64_t dv0 = desc_mn(base + C::OFF_ST, p.gran * 128, 1024, 2);
+    const uint64_t dp0 = desc_mn(base + C::OFF_P, BOX, P_GROUP, P_SWZ);
+    uint32_t voff[BN / 16];  // of 16 keys each, in descriptor units
+#pragma unroll
+    for (int kk = 0; kk < BN / 16; ++kk) voff[kk] = value_offset(16 * kk, p, D) >> 4;
     bool ok = true;
     uint32_t zc = 0;
     auto wait = [&](uint32_t bar, uint32_t ph) {
@@ -616,20 +649,21 @@ __global__ void __launch_bounds__(Cfg<K, D, NR>::THREADS, 1)
       return w;
     };
     auto scores = [&](uint32_t t) {
-      for (int kc = 0; kc < C::KCH; ++kc, ++zc) {
-        const uint32_t slot = zc % RING;
-        if (!wait(zfull + 8 * slot, (zc / RING) & 1u)) return false;
+      for (int gr = 0; gr < C::NG; ++gr, ++zc) {
+        const uint32_t slot = zc % ZRING;
+        if (!wait(zfull + 8 * slot, (zc / ZRING) & 1u)) return false;
         if (elect_one()) {
+          const uint32_t d = tmem + (t & 1u) * NR, z = tmem + C::COL_Z + C::GCOLS * slot;
+          const uint64_t du = du0 + (uint64_t)((gr * C::GCH * NR * 128) >> 4);
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            mma_ts(tmem + (t & 1u) * NR, tmem + C::COL_Z + 32 * slot + 8 * kk,
-                   du0 + (uint64_t)((kc * NR * 128 + kk * 32) >> 4), id_s, (kc | kk) ? 1u : 0u);
+          for (int kk = 0; kk < 4 * C::GCH; ++kk)
+            mma_ts(d, z + 8 * kk, du + (uint64_t)(((kk >> 2) * NR * 128 + (kk & 3) * 32) >> 4),
+                   id_s, (gr | kk) ? 1u : 0u);
           commit(zempty + 8 * slot);
+          if (gr == C::NG - 1) commit(sfull + 8 * (t & 1u));
         }
         __syncwarp();
       }
-      if (elect_one()) commit(sfull + 8 * (t & 1u));
-      __syncwarp();
       return true;
     };
     for (; ok && more; more = seg_next(s, p)) {
@@ -649,7 +683,8 @@ __global__ void __launch_bounds__(Cfg<K, D, NR>::THREADS, 1)
         if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < BN / 16; ++kk)
-            mma_ss(tmem + C::COL_O, dv0 + (uint64_t)((st * C::STAGE + kk * 2048) >> 4),
+            mma_ss(tmem + C::COL_O,
+                   dv0 + (uint64_t)((st * C::STAGE) >> 4) + voff[kk],
                    dp0 + (uint64_t)(((it & 1u) * C::P_BYTES + kk * 2 * P_GROUP) >> 4), id_o,
                    (k > 0 || kk > 0) ? 1u : 0u);
           commit(empty + 8 * st);
@@ -677,31 +712,36 @@ __global__ void __launch_bounds__(Cfg<K, D, NR>::THREADS, 1)
       }
       __syncwarp();
       ++sg;
+      // lane i copies granule i; the next tile's page is looked up meanwhile
+      auto place = [&](int k, bool &here) -> int64_t {
+        const int t = (s.k0 + k) * BN + p.gran * lane;
+        here = k < s.nk && lane < BN >> p.gran_log && t < s.L;
+        return here ? ((int64_t)page_of(p, s.b, t) * p.Hkv + s.h) * p.P + t % p.P : 0;
+      };
+      bool here;
+      int64_t row = place(0, here);
       for (int k = 0; k < s.nk; ++k) {
         const uint32_t st = it % C::ST;
-        const int t = (s.k0 + k) * BN + GRAN * (lane & 3);
-        const bool here = lane < 4 && t < s.L;
-        const int page = here ? page_of(p, s.b, t) : 0;
         const int grans = __popc(__ballot_sync(~0u, here));
         if (!__all_sync(~0u, wait_phase(empty + 8 * st, ((it / C::ST) & 1u) ^ 1u, abort_flag,
                                         p.err))) {
           ok = false;
           break;
         }
-        constexpr int G_V = GRAN * 128, G_C = GRAN * C::CODE_ROW, G_N = GRAN * 2;
+        const uint32_t bytes_v = p.gran * D * 2, bytes_c = p.gran * C::CODE_ROW,
+                       bytes_n = p.gran * 2;
         const uint32_t bar = full + 8 * st;
-        if (lane == 0) mbar_expect_tx(bar, grans * (G_V * C::DB + G_C + G_N));
+        if (lane == 0) mbar_expect_tx(bar, grans * (bytes_v + bytes_c + bytes_n));
         __syncwarp();
         if (here) {
-          const int64_t row = ((int64_t)page * p.Hkv + s.h) * p.P + t % p.P;
           const uint32_t dst = base + C::OFF_ST + st * C::STAGE;
-          bulk_load(dst + C::ST_V + lane * G_C, p.codes + row * (K / 32), G_C, bar);
-          bulk_load(dst + C::ST_V + C::ST_C + lane * G_N, p.norms + row, G_N, bar);
-          for (int x = 0; x < C::DB; ++x)
-            tma_load_2d(dst + x * BOX + lane * G_V, &map_v, 64 * x, (int)row, bar);
+          bulk_load(dst + C::ST_V + lane * bytes_c, p.codes + row * (K / 32), bytes_c, bar);
+          bulk_load(dst + C::ST_V + C::ST_C + lane * bytes_n, p.norms + row, bytes_n, bar);
+          tma_load_3d(dst + lane * bytes_v, &map_v, 0, (int)row, 0, bar);
         }
         __syncwarp();
         ++it;
+        row = place(k + 1, here);
       }
     }
     if (*abort_flag) {  // let the copies in flight land before the block leaves
@@ -726,14 +766,15 @@ cudaError_t launch_nr(const Params &p, const ChunkArgs &a, cudaStream_t stream) 
   CUtensorMap map_u, map_v;
   const int64_t rows = p.N * p.Hq;
   if (!tc::make_map(&map_u, p.w.U, rows, M, M, NR) ||
-      !tc::make_map(&map_v, a.value_pages, (uint64_t)p.num_pages * p.Hkv * p.P, D, D, GRAN))
+      !make_value_map(&map_v, a.value_pages, (uint64_t)p.num_pages * p.Hkv * p.P, D, p.gran))
     return cudaErrorInvalidValue;
   const int64_t prep = 1 + (rows + PREP_ROWS - 1) / PREP_ROWS;
-  if (a.q_f32)
-    prep_kernel<M, D, true><<<(unsigned)prep, PREP_THREADS, 0, stream>>>(p);
-  else
-    prep_kernel<M, D, false><<<(unsigned)prep, PREP_THREADS, 0, stream>>>(p);
-  cudaError_t e = cudaGetLastError();
+  auto prep_k = a.q_f32 ? prep_kernel<M, D, true> : prep_kernel<M, D, false>;
+  cudaError_t e = cudaFuncSetAttribute(prep_k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       prep_smem<M, D>());
+  if (e != cudaSuccess) return e;
+  prep_k<<<(unsigned)prep, PREP_THREADS, prep_smem<M, D>(), stream>>>(p);
+  e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   e = cudaFuncSetAttribute(attend_kernel<M, D, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            C::SMEM);
@@ -799,6 +840,8 @@ cudaError_t launch_chunk(const ChunkArgs &a, cudaStream_t stream) {
   p.B = a.B; p.Hq = a.Hq; p.Hkv = a.Hkv; p.G = a.Hq / a.Hkv; p.P = a.page_tokens;
   p.max_pages = a.max_pages; p.num_pages = a.num_pages; p.N = a.N; p.max_len = a.max_len;
   p.key_tiles = (int)((a.max_len + chunk::BN - 1) / chunk::BN);
+  p.gran_log = a.page_tokens % 128 == 0 ? 7 : a.page_tokens % 64 == 0 ? 6 : 5;
+  p.gran = 1 << p.gran_log;
   p.scale = a.softmax_scale;
   const int sms = device_sm_count();
   p.blocks = sms < chunk::SM_COUNT ? sms : chunk::SM_COUNT;

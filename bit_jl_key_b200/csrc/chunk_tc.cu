@@ -33,7 +33,7 @@
 // weights up to 2^8 are as exact, and the accumulator need not be rescaled.
 //
 // Warps: 0-3 and 4-7 softmax and output of a half (one row per thread), 8 MMA
-// issue and tensor memory, 9 copies (a 32-key granule of V lies in one page).
+// issue and tensor memory, 9 copies (a granule of V lies in one page).
 // Every wait is bounded; one that runs out records DERR_TC_WAIT_TIMEOUT.
 #include "chunk.cuh"
 #include "jl_tc.cuh"
@@ -52,11 +52,6 @@ constexpr int MMA_WARP = SM_WARPS * HALVES, LOAD_WARP = MMA_WARP + 1;
 constexpr int THREADS = (LOAD_WARP + 1) * 32;
 constexpr int POLY_EVERY = 4;                     // one pair of weights in so many on the FMA pipe
 constexpr int BOX = BM * 128;                     // 128 rows of 64 16-bit elements
-
-__device__ __forceinline__ float load_q(const void *Q, bool f32, int64_t i) {
-  return f32 ? __ldg(static_cast<const float *>(Q) + i)
-             : bf16_bits_to_f32(__ldg(static_cast<const uint16_t *>(Q) + i));
-}
 
 // Block 0 makes the plan; the others convert the queries, one warp per row.
 template <int D, bool F32>
@@ -108,12 +103,12 @@ struct Cfg {
 };
 
 // V operand: keys along K in rows of 128 bytes (64 dims), 8-key groups 1024
-// bytes apart (stride offset), 64-dim boxes BOX bytes apart (leading offset),
+// bytes apart (stride offset), 64-dim boxes `box` bytes apart (leading offset),
 // 128-byte swizzle.
-__device__ __forceinline__ uint64_t desc_v(uint32_t addr) {
+__device__ __forceinline__ uint64_t desc_v(uint32_t addr, uint32_t box) {
   uint64_t d = 0;
   d |= (uint64_t)((addr >> 4) & 0x3FFFu);
-  d |= (uint64_t)((uint32_t)BOX >> 4) << 16;
+  d |= (uint64_t)(box >> 4) << 16;
   d |= (uint64_t)(1024u >> 4) << 32;
   d |= (uint64_t)1u << 46;
   d |= (uint64_t)2u << 61;
@@ -321,7 +316,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int tok = live ? (int)(row / p.G) : 0;
       const int seen = live ? min(s.L, max(0, s.L - s.n + tok + 1)) : 0;
       const int64_t urow = ((int64_t)s.h * p.N + s.start) * p.G + row;
-      const float rs = live ? __ldg(p.w.rs + urow) : 0.f;
+      const float rs = live ? __ldcg(p.w.rs + urow) : 0.f;
       float m = -INFINITY, l = 0.f;
       for (int k = 0; k < s.nk; ++k, ++it, ++vt) {
         if (!wait_phase(sfull + 8 * a, it & 1u, abort_flag, p.err)) {
@@ -340,12 +335,12 @@ __global__ void __launch_bounds__(THREADS, 1)
             ok = false;
             break;
           }
-          uint8_t *V = g + C::OFF_V + vs * C::TILE;
+          uint8_t *V = g + C::OFF_V + vs * C::TILE + value_offset(r, p, D);
           if (r >= left)
             for (int x = 0; x < C::DB; ++x)
 #pragma unroll
               for (int e = 0; e < 8; ++e)
-                *reinterpret_cast<uint4 *>(V + x * BOX + r * 128 + 16 * e) =
+                *reinterpret_cast<uint4 *>(V + x * p.gran * 128 + 16 * e) =
                     make_uint4(0, 0, 0, 0);
           fence_async_smem();
         }
@@ -495,7 +490,10 @@ __global__ void __launch_bounds__(THREADS, 1)
     constexpr uint32_t id_s = idesc_f16(BM, BN, 0);
     constexpr uint32_t id_o = idesc_f16(BM, D, 1) | (1u << 16);  // V along its N side
     const uint64_t du0 = desc_sw128(base), dk0 = desc_sw128(base + C::OFF_K);
-    const uint64_t dv0 = desc_v(base + C::OFF_V);
+    const uint64_t dv0 = desc_v(base + C::OFF_V, p.gran * 128);
+    uint32_t voff[BN / 16];  // of 16 keys each, in descriptor units
+#pragma unroll
+    for (int kk = 0; kk < BN / 16; ++kk) voff[kk] = value_offset(16 * kk, p, D) >> 4;
     bool ok = true;
     uint32_t kt = 0, sg = 0;            // key tiles and segments of the block
     uint32_t it0 = 0, it1 = 0, sg1 = 0; // key tiles of each half, segments of half 1
@@ -539,7 +537,8 @@ __global__ void __launch_bounds__(THREADS, 1)
               for (int i = 0; i < BN / 32; ++i) {
                 const int kk = half * (BN / 32) + i;
                 mma_ts(tmem + C::COL_O + a * D, tmem + a * BN + 8 * kk,
-                       dv + (uint64_t)((kk * 2048) >> 4), id_o, (k > 0 || kk > 0) ? 1u : 0u);
+                       dv + voff[kk], id_o,
+                       (k > 0 || kk > 0) ? 1u : 0u);
               }
               if (half) {
                 commit(pv_bar(a, it));
@@ -579,13 +578,21 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int na = halves();
       if (lane == 0) {
         mbar_expect_tx(ufull, na * C::TILE);
-        const int64_t row = ((int64_t)s.h * p.N + s.start) * p.G + (int64_t)s.mt * ROWS;
+        const int64_t urow = ((int64_t)s.h * p.N + s.start) * p.G + (int64_t)s.mt * ROWS;
         for (int a = 0; a < na; ++a)
           for (int x = 0; x < C::DB; ++x)
-            tma_load_2d(base + a * C::TILE + x * BOX, &map_u, x * 64, (int)row + a * BM, ufull);
+            tma_load_2d(base + a * C::TILE + x * BOX, &map_u, x * 64, (int)urow + a * BM, ufull);
       }
       __syncwarp();
       ++sg;
+      // lane i copies granule i of V; the next tile's page is looked up meanwhile
+      auto place = [&](int k, bool &here) -> int64_t {
+        const int t = (s.k0 + k) * BN + p.gran * lane;
+        here = k < s.nk && lane < BN >> p.gran_log && t < s.L;
+        return here ? ((int64_t)page_of(p, s.b, t) * p.Hkv + s.h) * p.P + t % p.P : 0;
+      };
+      bool here;
+      int64_t row = place(0, here);
       const int64_t krow = ((int64_t)s.b * p.Hkv + s.h) * p.key_tiles;
       for (int k = 0; k < s.nk; ++k) {
         const int ks = kt % C::SK, vs = kt % C::SV;
@@ -601,9 +608,6 @@ __global__ void __launch_bounds__(THREADS, 1)
                         (int)((krow + s.k0 + k) * BN), kfull + 8 * ks);
         }
         __syncwarp();
-        const int t = (s.k0 + k) * BN + GRAN * (lane & 3);
-        const bool here = lane < 4 && t < s.L;
-        const int page = here ? page_of(p, s.b, t) : 0;
         const int grans = __popc(__ballot_sync(~0u, here));
         const bool vok = __all_sync(
             ~0u, wait_phase(vempty + 8 * vs, ((kt / C::SV) & 1u) ^ 1u, abort_flag, p.err));
@@ -612,15 +616,14 @@ __global__ void __launch_bounds__(THREADS, 1)
           ok = false;
           break;
         }
-        if (lane == 0) mbar_expect_tx(vfull + 8 * vs, grans * GRAN * 128 * C::DB);
+        const uint32_t bytes = p.gran * D * 2;
+        if (lane == 0) mbar_expect_tx(vfull + 8 * vs, grans * bytes);
         __syncwarp();
-        if (here) {
-          const int64_t vrow = ((int64_t)page * p.Hkv + s.h) * p.P + t % p.P;
-          for (int x = 0; x < C::DB; ++x)
-            tma_load_2d(base + C::OFF_V + vs * C::TILE + x * BOX + lane * GRAN * 128, &map_v,
-                        64 * x, (int)vrow, vfull + 8 * vs);
-        }
+        if (here)
+          tma_load_3d(base + C::OFF_V + vs * C::TILE + lane * bytes, &map_v, 0, (int)row, 0,
+                      vfull + 8 * vs);
         __syncwarp();
+        row = place(k + 1, here);
       }
     }
     if (*abort_flag) {  // let the copies in flight land before the block leaves
@@ -649,7 +652,7 @@ cudaError_t launch_many_t(const Params &p, const ChunkArgs &a, cudaStream_t stre
   const int64_t rows = p.N * p.Hq;
   if (!tc::make_map(&map_u, p.w.U, rows, D, D, BM) ||
       !tc::make_map(&map_k, p.w.keys, (uint64_t)p.B * p.Hkv * p.key_tiles * BN, D, D, BN) ||
-      !tc::make_map(&map_v, a.value_pages, (uint64_t)p.num_pages * p.Hkv * p.P, D, D, GRAN))
+      !make_value_map(&map_v, a.value_pages, (uint64_t)p.num_pages * p.Hkv * p.P, D, p.gran))
     return cudaErrorInvalidValue;
   const int64_t prep = 1 + (rows + PREP_THREADS / 32 - 1) / (PREP_THREADS / 32);
   if (a.q_f32)
