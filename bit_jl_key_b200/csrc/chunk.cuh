@@ -73,10 +73,10 @@ __device__ __forceinline__ int tile_units(int mt, int n, int L, int G, int rows)
   return max(1, (seen + BN - 1) / BN);
 }
 
-static __device__ __noinline__ void make_plan(const Params &p) {
+__device__ __forceinline__ void make_plan(const Params &p) {
   __shared__ int64_t units[PREP_THREADS];  // of a head, then before the sequence
   __shared__ int tiles[PREP_THREADS];
-  __shared__ int first[PREP_THREADS], tokens[PREP_THREADS];
+  __shared__ int first[PREP_THREADS], tokens[PREP_THREADS], keys[PREP_THREADS];
   __shared__ int64_t u_done;
   __shared__ int t_done, rows_done;
   if (threadIdx.x == 0) {
@@ -105,6 +105,7 @@ static __device__ __noinline__ void make_plan(const Params &p) {
     tiles[threadIdx.x] = nt ? nt + 1 : 0;
     first[threadIdx.x] = (int)c0;
     tokens[threadIdx.x] = n;
+    keys[threadIdx.x] = L;
     __syncthreads();
     if (threadIdx.x == 0) {
       int64_t u = u_done;
@@ -156,33 +157,50 @@ static __device__ __noinline__ void make_plan(const Params &p) {
   }
   __threadfence_block();
   __syncthreads();
+  // where each block begins; up to PREP_THREADS sequences are still at hand in
+  // shared memory, and so is a row tile of the first few of a sequence
+  const bool here = p.B <= PREP_THREADS;
   for (int i = threadIdx.x; i < p.blocks; i += PREP_THREADS) {
     p.w.arrived[2 * i] = p.w.arrived[2 * i + 1] = 0;
     Start s{};
     s.u = i * quota;
     s.end = s.u + quota < total ? s.u + quota : total;
     if (s.u < total) {
+      auto first_unit = [&](int b) {
+        return b == p.B ? total : here ? units[b] : p.w.b_unit[b];
+      };
       int lo = 0, hi = p.B;  // the last b whose first unit is not above u
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (p.w.b_unit[mid] <= s.u) lo = mid; else hi = mid;
+        if (first_unit(mid) <= s.u) lo = mid; else hi = mid;
       }
       s.b = lo;
-      s.n = p.w.count[lo];
-      s.L = p.w.len[lo];
-      s.row = p.w.start[lo];
-      const int64_t u0 = p.w.b_unit[lo], per_head = (p.w.b_unit[lo + 1] - u0) / p.Hkv;
+      s.n = here ? tokens[lo] : p.w.count[lo];
+      s.L = here ? keys[lo] : p.w.len[lo];
+      s.row = here ? first[lo] : p.w.start[lo];
+      const int64_t u0 = first_unit(lo), per_head = (first_unit(lo + 1) - u0) / p.Hkv;
       s.h = (int)((s.u - u0) / per_head);
       const int rem = (int)(s.u - u0 - s.h * per_head);
-      const int32_t *pre = p.w.mt_pre + p.w.b_tile[lo];
-      int a = 0, z = (int)(((int64_t)s.n * p.G + p.rows - 1) / p.rows);
-      while (z - a > 1) {
-        const int mid = (a + z) >> 1;
-        if (pre[mid] <= rem) a = mid; else z = mid;
+      const int nt = (int)(((int64_t)s.n * p.G + p.rows - 1) / p.rows);
+      int a = 0, before = 0;
+      if (nt <= 16) {
+        s.units = tile_units(0, s.n, s.L, p.G, p.rows);
+        while (before + s.units <= rem) {
+          before += s.units;
+          s.units = tile_units(++a, s.n, s.L, p.G, p.rows);
+        }
+      } else {
+        const int32_t *pre = p.w.mt_pre + (here ? tiles[lo] : p.w.b_tile[lo]);
+        int z = nt;
+        while (z - a > 1) {
+          const int mid = (a + z) >> 1;
+          if (pre[mid] <= rem) a = mid; else z = mid;
+        }
+        before = pre[a];
+        s.units = pre[a + 1] - before;
       }
       s.mt = a;
-      s.k0 = rem - pre[a];
-      s.units = pre[a + 1] - pre[a];
+      s.k0 = rem - before;
     }
     p.w.begin[i] = s;
   }

@@ -48,15 +48,13 @@ __host__ __device__ __forceinline__ int k_slot(int i) {
   return (i & ~31) + 2 * (i & 15) + ((i >> 4) & 1);
 }
 
-constexpr int PREP_ROWS = 8;
+constexpr int PREP_ROWS = 16;
 
-// Block 0 makes the plan; the others project PREP_ROWS rows each: the sketch
-// goes through shared memory (rows 16 bytes longer than their entries, so that
-// neighbouring rows lie in different banks), a thread takes one sketch row and
-// meets every query row as a broadcast.
-template <int M, int D>
-constexpr int prep_smem() { return M * (D * 2 + 16); }
-
+// Block 0 makes the plan; the others project PREP_ROWS rows each with
+// mma.sync (a few rows, where the time is one trip to memory: the sketch's
+// operand registers are loaded straight from it before anything else).  A bf16
+// query is one operand; an fp32 one is three bf16 ones that add up to it, so
+// all products are exact and the sums fp32.
 template <int M, int D, bool F32>
 __global__ void __launch_bounds__(PREP_THREADS) prep_kernel(const Params p) {
   griddep_launch_dependents();  // attend may set itself up meanwhile
@@ -64,19 +62,27 @@ __global__ void __launch_bounds__(PREP_THREADS) prep_kernel(const Params p) {
     make_plan(p);
     return;
   }
-  extern __shared__ __align__(16) uint8_t sketch[];
-  __shared__ __align__(16) float q[PREP_ROWS][D];
-  __shared__ float top[PREP_ROWS][PREP_THREADS / 32];
-  constexpr int LD = D * 2 + 16;
-  for (int i = threadIdx.x; i < M * (D / 8); i += PREP_THREADS) {
-    const int r = i / (D / 8), c = i % (D / 8);
-    cp_async_16(smem_u32(sketch + r * LD + 16 * c), p.S + (int64_t)r * D + 8 * c, 16);
-  }
-  cp_async_commit();
+  constexpr int WARPS = PREP_THREADS / 32, NT = M / 8 / WARPS, KT = D / 16;
+  constexpr int TERMS = F32 ? 3 : 1, LD = D + 8;
+  __shared__ __align__(16) uint16_t q[TERMS][PREP_ROWS][LD];
+  __shared__ float top[PREP_ROWS][WARPS];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int n0 = warp * NT * 8;                      // the warp's sketch rows
+  uint32_t b[NT][KT][2];
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int k = 0; k < KT; ++k) {
+      const uint32_t *s = reinterpret_cast<const uint32_t *>(
+          p.S + (int64_t)(n0 + 8 * n + (lane >> 2)) * D + 16 * k + 2 * (lane & 3));
+      b[n][k][0] = __ldg(s);
+      b[n][k][1] = __ldg(s + 4);
+    }
   const uint32_t rows = (uint32_t)(p.N * p.G);       // of a KV head
   const uint32_t total = rows * p.Hkv;
   const uint32_t r0 = (blockIdx.x - 1) * PREP_ROWS;
   const float sgn = p.scale < 0.f ? -1.f : 1.f;
+#pragma unroll
   for (int i = threadIdx.x; i < PREP_ROWS * D; i += PREP_THREADS) {
     const uint32_t r = r0 + i / D;
     float v = 0.f;
@@ -84,64 +90,66 @@ __global__ void __launch_bounds__(PREP_THREADS) prep_kernel(const Params p) {
       const uint32_t h = r / rows, tg = r - h * rows, tok = tg / p.G, g = tg - tok * p.G;
       v = sgn * load_q(p.Q, F32, tok * p.q_tok + (int64_t)(h * p.G + g) * p.q_head + i % D);
     }
-    q[i / D][i % D] = v;
-  }
-  cp_async_wait<0>();
-  __syncthreads();
-  // groups of threads share the rows when m < 256; m = 512 takes two passes
-  constexpr int TH = M < PREP_THREADS ? M : PREP_THREADS;
-  constexpr int PASS = M / TH, GROUPS = PREP_THREADS / TH, RG = PREP_ROWS / GROUPS;
-  const int grp = threadIdx.x / TH;
-  float acc[PASS][RG];
 #pragma unroll
-  for (int ps = 0; ps < PASS; ++ps) {
-    const uint8_t *s = sketch + (threadIdx.x % TH + ps * TH) * LD;
-#pragma unroll
-    for (int r = 0; r < RG; ++r) acc[ps][r] = 0.f;
-#pragma unroll 4
-    for (int c = 0; c < D / 8; ++c) {
-      const uint4 w = *reinterpret_cast<const uint4 *>(s + 16 * c);
-      const float x[8] = {__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u),
-                          __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u),
-                          __uint_as_float(w.z << 16), __uint_as_float(w.z & 0xffff0000u),
-                          __uint_as_float(w.w << 16), __uint_as_float(w.w & 0xffff0000u)};
-#pragma unroll
-      for (int r = 0; r < RG; ++r) {
-        const float4 a = *reinterpret_cast<const float4 *>(&q[grp * RG + r][8 * c]);
-        const float4 b = *reinterpret_cast<const float4 *>(&q[grp * RG + r][8 * c + 4]);
-        float t = acc[ps][r];
-        t = fmaf(a.x, x[0], t); t = fmaf(a.y, x[1], t);
-        t = fmaf(a.z, x[2], t); t = fmaf(a.w, x[3], t);
-        t = fmaf(b.x, x[4], t); t = fmaf(b.y, x[5], t);
-        t = fmaf(b.z, x[6], t); t = fmaf(b.w, x[7], t);
-        acc[ps][r] = t;
-      }
+    for (int t = 0; t < TERMS; ++t) {
+      const uint16_t x = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+      q[t][i / D][i % D] = x;
+      v -= bf16_bits_to_f32(x);
     }
   }
-  // the largest entry of each row: over the row's warps
-  constexpr int RW = TH / 32;  // warps of a row group
+  __syncthreads();
+  float acc[NT][4];
 #pragma unroll
-  for (int r = 0; r < RG; ++r) {
-    float v = 0.f;
+  for (int n = 0; n < NT; ++n)
 #pragma unroll
-    for (int ps = 0; ps < PASS; ++ps) v = fmaxf(v, fabsf(acc[ps][r]));
+    for (int e = 0; e < 4; ++e) acc[n][e] = 0.f;
 #pragma unroll
-    for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(~0u, v, o));
-    if ((threadIdx.x & 31) == 0) top[grp * RG + r][(threadIdx.x % TH) >> 5] = v;
+  for (int t = TERMS - 1; t >= 0; --t)               // the small terms first
+#pragma unroll
+    for (int k = 0; k < KT; ++k) {
+      const uint16_t *x = &q[t][lane >> 2][16 * k + 2 * (lane & 3)];
+      uint32_t a[4];
+      a[0] = *reinterpret_cast<const uint32_t *>(x);
+      a[1] = *reinterpret_cast<const uint32_t *>(x + 8 * LD);
+      a[2] = *reinterpret_cast<const uint32_t *>(x + 8);
+      a[3] = *reinterpret_cast<const uint32_t *>(x + 8 * LD + 8);
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+        mma_bf16_16816(acc[n], a[0], a[1], a[2], a[3], b[n][k][0], b[n][k][1]);
+    }
+  // the largest entry of each row: over the four lanes that hold it, the warps
+  float m0 = 0.f, m1 = 0.f;
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    m0 = fmaxf(m0, fmaxf(fabsf(acc[n][0]), fabsf(acc[n][1])));
+    m1 = fmaxf(m1, fmaxf(fabsf(acc[n][2]), fabsf(acc[n][3])));
+  }
+#pragma unroll
+  for (int o = 2; o; o >>= 1) {
+    m0 = fmaxf(m0, __shfl_xor_sync(~0u, m0, o));
+    m1 = fmaxf(m1, __shfl_xor_sync(~0u, m1, o));
+  }
+  if ((lane & 3) == 0) {
+    top[lane >> 2][warp] = m0;
+    top[(lane >> 2) + 8][warp] = m1;
   }
   __syncthreads();
 #pragma unroll
-  for (int r = 0; r < RG; ++r) {
-    const uint32_t row = r0 + grp * RG + r;
+  for (int half = 0; half < 2; ++half) {
+    const int r = (lane >> 2) + 8 * half;
+    const uint32_t row = r0 + r;
     if (row >= total) break;
     float v = 0.f;
-    for (int w = 0; w < RW; ++w) v = fmaxf(v, top[grp * RG + r][w]);
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) v = fmaxf(v, top[r][w]);
     const float2 f = row_power(v);
 #pragma unroll
-    for (int ps = 0; ps < PASS; ++ps)
-      p.w.U[(int64_t)row * M + k_slot(threadIdx.x % TH + ps * TH)] =
-          __half_as_ushort(__float2half_rn(acc[ps][r] * f.x));
-    if (threadIdx.x % TH == 0)
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        p.w.U[(int64_t)row * M + k_slot(n0 + 8 * n + 2 * (lane & 3) + e)] =
+            __half_as_ushort(__float2half_rn(acc[n][2 * half + e] * f.x));
+    if (warp == 0 && (lane & 3) == 0)
       p.w.rs[row] = fmaxf((float)(1.2533141373155002512 / M * 1.4426950408889634074) *
                               fabsf(p.scale) * f.y,
                           MIN_SCALE);
@@ -212,6 +220,7 @@ struct Rows {
   float scale[NR], neg[NR];   // of a score; minus the maximum weights refer to
   float factor[NR];           // of sums and accumulators when that is renewed
   float part[SM_WARPS][NR];   // a maximum or sum of each warp
+  float weight[SM_WARPS][NR]; // of the records that are joined
   float sum[NR];
   int seen[NR];               // keys the row sees
   int out[NR];                // row of the output
@@ -243,8 +252,8 @@ __global__ void __launch_bounds__(Cfg<K, D, NR>::THREADS, 1)
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t *g = chunk_smem + (base - raw);
   Rows<NR> &rows = *reinterpret_cast<Rows<NR> *>(g + C::OFF_SMALL);
-  constexpr int OFF_BAR = C::OFF_SMALL + 3072;
-  static_assert(sizeof(Rows<NR>) <= 3072, "row arrays");
+  constexpr int OFF_BAR = C::OFF_SMALL + 3584;
+  static_assert(sizeof(Rows<NR>) <= 3584, "row arrays");
   const uint32_t bar0 = base + OFF_BAR;
   int nbar = 0;
   auto bars = [&](int n) {
@@ -523,52 +532,63 @@ __global__ void __launch_bounds__(Cfg<K, D, NR>::THREADS, 1)
         if (r < nrow) *reinterpret_cast<float2 *>(mine + r * (D + 2) + D) =
             make_float2(-rows.neg[r], rows.sum[r]);
         if (last_to_arrive(split, p, 0, 1, SM_WARPS * 32, r == 0, join_flag)) {
-          // the joined maximum and sum of each row, then its accumulators,
-          // the loads of a record's rows side by side
+          // the joined maximum and sum of each row: a quarter of the records
+          // (half with 64 rows) to each group of NR threads
           auto record = [&](int64_t c) {
             return p.w.part + split.record(c) * (int64_t)(NR * (D + 2));
           };
-          if (r < NR) {
-            float m = -INFINITY, sum = 0.f;
-            if (r < nrow)
-              for (int64_t c = split.c0; c <= split.c1; ++c) {
-                const float2 ml =
-                    __ldcg(reinterpret_cast<const float2 *>(record(c) + r * (D + 2) + D));
-                if (ml.y == 0.f) continue;
-                const float now = fmaxf(m, ml.x);
-                sum = sum * (m == now ? 1.f : fast_exp2(m - now)) + ml.y * fast_exp2(ml.x - now);
-                m = now;
-              }
-            rows.neg[r] = -m;
-            rows.sum[r] = sum;
+          constexpr int GR = SM_WARPS * 32 / NR;
+          const int j = r % NR, gr = r / NR;
+          auto state = [&](int64_t c) {
+            return j < nrow && c <= split.c1
+                       ? __ldcg(reinterpret_cast<const float2 *>(record(c) + j * (D + 2) + D))
+                       : make_float2(-INFINITY, 0.f);
+          };
+          auto join = [](float2 a, float2 b) {
+            const float m = fmaxf(a.x, b.x);
+            if (m == -INFINITY) return make_float2(m, a.y + b.y);
+            return make_float2(m, (a.y == 0.f ? 0.f : a.y * fast_exp2(a.x - m)) +
+                                      (b.y == 0.f ? 0.f : b.y * fast_exp2(b.x - m)));
+          };
+          float2 ms = make_float2(-INFINITY, 0.f);
+          for (int64_t c = split.c0 + gr; c <= split.c1; c += GR) {
+            const float2 x = state(c);
+            if (x.y != 0.f) ms = join(ms, x);
           }
+          rows.part[gr][j] = ms.x;
+          rows.weight[gr][j] = ms.y;
+          sync();
+          if (r < NR) {
+            ms = make_float2(rows.part[0][r], rows.weight[0][r]);
+            for (int q = 1; q < GR; ++q)
+              ms = join(ms, make_float2(rows.part[q][r], rows.weight[q][r]));
+            rows.neg[r] = -ms.x;
+            rows.sum[r] = ms.y;
+          }
+          // the accumulators, GR records at a time, a record's loads side by side
           float o[NR];
 #pragma unroll
-          for (int j = 0; j < NR; ++j) o[j] = 0.f;
-          for (int64_t c = split.c0; c <= split.c1; ++c) {
-            const float *q = record(c);
-            if (r < NR) {
-              float w = 0.f;
-              if (r < nrow) {
-                const float2 ml = __ldcg(reinterpret_cast<const float2 *>(q + r * (D + 2) + D));
-                if (ml.y != 0.f) w = fast_exp2(ml.x + rows.neg[r]);
-              }
-              rows.factor[r] = w;
-            }
+          for (int e = 0; e < NR; ++e) o[e] = 0.f;
+          for (int64_t c0 = split.c0; c0 <= split.c1; c0 += GR) {
+            const float2 x = state(c0 + gr);
             sync();
-            if (r < D) {
+            rows.weight[gr][j] = x.y == 0.f ? 0.f : fast_exp2(x.x + rows.neg[j]);
+            sync();
+            for (int q = 0; q < GR && c0 + q <= split.c1; ++q) {
+              const float *acc = record(c0 + q) + r;
+              if (r < D) {
 #pragma unroll
-              for (int j = 0; j < NR; ++j) {
-                const float x = j < nrow ? __ldcg(q + j * (D + 2) + r) : 0.f;
-                o[j] = fmaf(rows.factor[j], x, o[j]);
+                for (int e = 0; e < NR; ++e) {
+                  const float y = e < nrow ? __ldcg(acc + e * (D + 2)) : 0.f;
+                  o[e] = fmaf(rows.weight[q][e], y, o[e]);
+                }
               }
             }
-            sync();
           }
           if (r < D) {
 #pragma unroll
-            for (int j = 0; j < NR; ++j)
-              if (j < nrow) write(j, o[j]);
+            for (int e = 0; e < NR; ++e)
+              if (e < nrow) write(e, o[e]);
           }
         }
       }
@@ -770,11 +790,8 @@ cudaError_t launch_nr(const Params &p, const ChunkArgs &a, cudaStream_t stream) 
     return cudaErrorInvalidValue;
   const int64_t prep = 1 + (rows + PREP_ROWS - 1) / PREP_ROWS;
   auto prep_k = a.q_f32 ? prep_kernel<M, D, true> : prep_kernel<M, D, false>;
-  cudaError_t e = cudaFuncSetAttribute(prep_k, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       prep_smem<M, D>());
-  if (e != cudaSuccess) return e;
-  prep_k<<<(unsigned)prep, PREP_THREADS, prep_smem<M, D>(), stream>>>(p);
-  e = cudaGetLastError();
+  prep_k<<<(unsigned)prep, PREP_THREADS, 0, stream>>>(p);
+  cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   e = cudaFuncSetAttribute(attend_kernel<M, D, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            C::SMEM);
