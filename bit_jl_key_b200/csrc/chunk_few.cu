@@ -831,9 +831,11 @@ cudaError_t launch_few(Params p, const ChunkArgs &a, cudaStream_t stream) {
 
 // Which kernel: expanding the keys costs what one reading and one writing of
 // 2 d bytes per key cost and then makes a row cheap, so it pays from about
-// MANY rows per (sequence, KV head) on, and only while the expanded keys stay
-// inside MAX_KEYS bytes of workspace.
-constexpr int MANY = 256;
+// MANY rows per (sequence, KV head) on (4 sequences of 16384 keys, 32 query and
+// 8 KV heads, d = 128, m = 256: 128 rows 147 us here and 170 us there, 256 rows
+// 233 and 184 us; of 2048 keys: 62 and 54 us, 84 and 60 us), and only while the
+// expanded keys stay inside MAX_KEYS bytes of workspace.
+constexpr int MANY = 160;
 constexpr int64_t MAX_KEYS = (int64_t)8 << 30;
 static bool many(int64_t N, int B, int Hq, int Hkv, int64_t max_len, int d) {
   const int64_t tiles = (max_len + chunk::BN - 1) / chunk::BN * B * Hkv;

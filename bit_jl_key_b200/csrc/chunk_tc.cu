@@ -53,37 +53,62 @@ constexpr int THREADS = (LOAD_WARP + 1) * 32;
 constexpr int POLY_EVERY = 4;                     // one pair of weights in so many on the FMA pipe
 constexpr int BOX = BM * 128;                     // 128 rows of 64 16-bit elements
 
-// Block 0 makes the plan; the others convert the queries, one warp per row.
-template <int D, bool F32>
+// Block 0 makes the plan; the others convert the queries, d / 8 lanes per row
+// (VEC: 16 bytes at a time, where every row starts on 16 bytes).
+template <int D, bool F32, bool VEC>
 __global__ void __launch_bounds__(PREP_THREADS) prep_kernel(const Params p) {
+  griddep_launch_dependents();  // the keys may be expanded meanwhile
   if (blockIdx.x == 0) {
     make_plan(p);
     return;
   }
-  constexpr int E = D / 32;
-  const int64_t rows = p.N * p.G, total = rows * p.Hkv;
-  const int lane = threadIdx.x & 31;
-  const int64_t r = (int64_t)(blockIdx.x - 1) * (PREP_THREADS / 32) + (threadIdx.x >> 5);
-  if (r >= total) return;
-  const int h = (int)(r / rows);
-  const int64_t tg = r - h * rows, tok = tg / p.G;
-  const int64_t q0 = tok * p.q_tok + (int64_t)(h * p.G + (int)(tg - tok * p.G)) * p.q_head;
-  float q[E], top = 0.f;
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    q[e] = load_q(p.Q, F32, q0 + lane + 32 * e);
-    top = fmaxf(top, fabsf(q[e]));
-  }
-#pragma unroll
-  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-  const float2 f = row_power(top);
+  constexpr int LANES = D / 8;
+  const uint32_t rows = (uint32_t)(p.N * p.Hq);
+  const int lane = threadIdx.x % LANES;
   const float sgn = p.scale < 0.f ? -1.f : 1.f;
+  for (uint32_t r = (blockIdx.x - 1) * (PREP_THREADS / LANES) + threadIdx.x / LANES; r < rows;
+       r += (gridDim.x - 1) * (PREP_THREADS / LANES)) {
+    const uint32_t tok = r / p.Hq, hq = r - tok * p.Hq, h = hq / p.G;
+    const int64_t q0 = tok * p.q_tok + (int64_t)hq * p.q_head + 8 * lane;
+    float q[8], top = 0.f;
+    if constexpr (VEC && F32) {
+      const float4 *x = reinterpret_cast<const float4 *>(static_cast<const float *>(p.Q) + q0);
+      const float4 a = __ldg(x), b = __ldg(x + 1);
+      q[0] = a.x; q[1] = a.y; q[2] = a.z; q[3] = a.w;
+      q[4] = b.x; q[5] = b.y; q[6] = b.z; q[7] = b.w;
+    } else if constexpr (VEC) {
+      const uint4 x =
+          __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.Q) + q0));
+      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-  for (int e = 0; e < E; ++e)
-    p.w.U[r * D + lane + 32 * e] = __half_as_ushort(__float2half_rn(sgn * q[e] * f.x));
-  if (lane == 0)
-    p.w.rs[r] = fmaxf((float)(1.4426950408889634074 / KEY_FACTOR) * fabsf(p.scale) * f.y,
-                      MIN_SCALE);
+      for (int e = 0; e < 4; ++e) {
+        q[2 * e] = __uint_as_float(w[e] << 16);
+        q[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) q[e] = load_q(p.Q, F32, q0 + e);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(q[e]));
+    // (the row's lanes leave the loop together)
+    const unsigned mask = LANES == 32 ? ~0u : ((1u << LANES) - 1u) << (threadIdx.x & 31 & -LANES);
+#pragma unroll
+    for (int o = LANES / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(mask, top, o));
+    const float2 f = row_power(top);
+    uint32_t u[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const __half2 y =
+          __floats2half2_rn(sgn * q[2 * e] * f.x, sgn * q[2 * e + 1] * f.x);
+      u[e] = *reinterpret_cast<const uint32_t *>(&y);
+    }
+    const int64_t row = ((int64_t)h * p.N + tok) * p.G + (hq - h * p.G);
+    *reinterpret_cast<uint4 *>(p.w.U + row * D + 8 * lane) = make_uint4(u[0], u[1], u[2], u[3]);
+    if (lane == 0)
+      p.w.rs[row] = fmaxf((float)(1.4426950408889634074 / KEY_FACTOR) * fabsf(p.scale) * f.y,
+                          MIN_SCALE);
+  }
 }
 
 template <int D>
@@ -654,11 +679,14 @@ cudaError_t launch_many_t(const Params &p, const ChunkArgs &a, cudaStream_t stre
       !tc::make_map(&map_k, p.w.keys, (uint64_t)p.B * p.Hkv * p.key_tiles * BN, D, D, BN) ||
       !make_value_map(&map_v, a.value_pages, (uint64_t)p.num_pages * p.Hkv * p.P, D, p.gran))
     return cudaErrorInvalidValue;
-  const int64_t prep = 1 + (rows + PREP_THREADS / 32 - 1) / (PREP_THREADS / 32);
-  if (a.q_f32)
-    prep_kernel<D, true><<<(unsigned)prep, PREP_THREADS, 0, stream>>>(p);
-  else
-    prep_kernel<D, false><<<(unsigned)prep, PREP_THREADS, 0, stream>>>(p);
+  const int64_t blocks = (rows + PREP_THREADS / (D / 8) - 1) / (PREP_THREADS / (D / 8));
+  const int64_t most = (int64_t)p.blocks * 8;
+  const uint64_t al = (uint64_t)reinterpret_cast<uintptr_t>(p.Q) |
+                      (uint64_t)(p.q_tok | p.q_head) * (a.q_f32 ? 4 : 2);
+  const bool vec = (al & 15) == 0;
+  auto prep = a.q_f32 ? (vec ? prep_kernel<D, true, true> : prep_kernel<D, true, false>)
+                      : (vec ? prep_kernel<D, false, true> : prep_kernel<D, false, false>);
+  prep<<<(unsigned)(1 + (blocks < most ? blocks : most)), PREP_THREADS, 0, stream>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   e = launch_expand_paged(p.codes, p.norms, p.num_pages, p.P, p.table, p.max_pages, p.lens, p.B,

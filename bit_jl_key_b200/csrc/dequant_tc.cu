@@ -628,6 +628,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                  "n"(C::TMEM_COLS)
                  : "memory");
   }
+  // PAGED: started beside the kernel before it (of which it needs nothing);
+  // the next one, which needs both, waits for this one
+  if constexpr (PAGED) griddep_wait();
 }
 
 // out [n][d] bf16, boxes of 64 columns (128 B) x 32 rows, 128-byte swizzle
@@ -657,8 +660,17 @@ cudaError_t launch_t(Params p, uint16_t *out, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   const int64_t sms = device_sm_count();
   const int64_t grid = p.num_tiles < sms ? p.num_tiles : sms;
-  dequant_tc_kernel<M, D, TB, PAGED><<<(int)grid, THREADS, C::SMEM, stream>>>(tmap, p);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = PAGED ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, dequant_tc_kernel<M, D, TB, PAGED>, tmap, p);
 }
 
 // R = [Pinv | Pinv S^T] rounded to binary16: one thread per element, the
