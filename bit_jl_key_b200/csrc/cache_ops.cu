@@ -135,18 +135,20 @@ struct Params {
   const int32_t *lens;
   int Hq, Hkv, G;
   int64_t T;
-  float k, decay;  // k: softmax_scale * log2(e)
+  float k, sign, decay;  // k: |softmax_scale| log2(e); sign: of softmax_scale
   int *err;
 };
 
 struct MS {
   float m, l;
 };
-// joins two softmax states; a state without keys is (-inf, 0)
-__device__ __forceinline__ MS join(MS a, MS b) {
+// Joins two softmax states; a state without keys is (-inf, 0).  The maximum is
+// of the scores themselves (times the scale's sign): only differences are
+// scaled, so a row of the type's lowest value is as uniform as any other.
+__device__ __forceinline__ MS join(MS a, MS b, float k) {
   const float m = fmaxf(a.m, b.m);
   if (m == -INFINITY) return {m, 0.f};
-  return {m, a.l * exp2f(a.m - m) + b.l * exp2f(b.m - m)};
+  return {m, a.l * exp2f((a.m - m) * k) + b.l * exp2f((b.m - m) * k)};
 }
 
 // One cluster per (sequence, KV head); its blocks split the keys.  Pass one
@@ -187,32 +189,32 @@ __global__ void __launch_bounds__(THREADS) mass_kernel(const Params p) {
       float m = a.m;
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
-        x[e] = t + e < t1 ? x[e] * p.k : -INFINITY;
+        x[e] = t + e < t1 ? x[e] * p.sign : -INFINITY;
         m = fmaxf(m, x[e]);
       }
       if (m > -INFINITY) {
-        float l = a.l * exp2f(a.m - m);
+        float l = a.l * exp2f((a.m - m) * p.k);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) l += exp2f(x[e] - m);
+        for (int e = 0; e < VEC; ++e) l += exp2f((x[e] - m) * p.k);
         a = {m, l};
       }
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1)
-      a = join(a, {__shfl_xor_sync(~0u, a.m, o), __shfl_xor_sync(~0u, a.l, o)});
+      a = join(a, {__shfl_xor_sync(~0u, a.m, o), __shfl_xor_sync(~0u, a.l, o)}, p.k);
     if (lane == 0) part[g * WARPS + warp] = a;
   }
   __syncthreads();
   for (int g = threadIdx.x; g < p.G; g += THREADS) {
     MS a = part[g * WARPS];
-    for (int w = 1; w < WARPS; ++w) a = join(a, part[g * WARPS + w]);
+    for (int w = 1; w < WARPS; ++w) a = join(a, part[g * WARPS + w], p.k);
     mine[g] = a;
   }
   cl.sync();
   for (int g = threadIdx.x; g < p.G; g += THREADS) {
     MS a{-INFINITY, 0.f};
-    for (int r = 0; r < nb; ++r) a = join(a, cl.map_shared_rank(mine, r)[g]);
-    // weight = 2^(x - m) / l; a head whose keys are all -inf adds nothing
+    for (int r = 0; r < nb; ++r) a = join(a, cl.map_shared_rank(mine, r)[g], p.k);
+    // weight = 2^((x - m) k) / l; a head whose keys are all -inf adds nothing
     all[g] = a.m == -INFINITY ? MS{0.f, 0.f} : MS{a.m, 1.f / a.l};
   }
   cl.sync();  // also: no block leaves while another reads its states
@@ -224,12 +226,12 @@ __global__ void __launch_bounds__(THREADS) mass_kernel(const Params p) {
       const MS a = all[g];
       if constexpr (VEC == 4) {
         const float4 v = *reinterpret_cast<const float4 *>(s);
-        w[0] += a.l == 0.f ? 0.f : exp2f(fmaf(v.x, p.k, -a.m)) * a.l;
-        w[1] += a.l == 0.f ? 0.f : exp2f(fmaf(v.y, p.k, -a.m)) * a.l;
-        w[2] += a.l == 0.f ? 0.f : exp2f(fmaf(v.z, p.k, -a.m)) * a.l;
-        w[3] += a.l == 0.f ? 0.f : exp2f(fmaf(v.w, p.k, -a.m)) * a.l;
+        w[0] += a.l == 0.f ? 0.f : exp2f(fmaf(v.x, p.sign, -a.m) * p.k) * a.l;
+        w[1] += a.l == 0.f ? 0.f : exp2f(fmaf(v.y, p.sign, -a.m) * p.k) * a.l;
+        w[2] += a.l == 0.f ? 0.f : exp2f(fmaf(v.z, p.sign, -a.m) * p.k) * a.l;
+        w[3] += a.l == 0.f ? 0.f : exp2f(fmaf(v.w, p.sign, -a.m) * p.k) * a.l;
       } else {
-        w[0] += a.l == 0.f ? 0.f : exp2f(fmaf(s[0], p.k, -a.m)) * a.l;
+        w[0] += a.l == 0.f ? 0.f : exp2f(fmaf(s[0], p.sign, -a.m) * p.k) * a.l;
       }
     }
 #pragma unroll
@@ -264,7 +266,8 @@ cudaError_t launch_accumulate(const AccumulateArgs &a, cudaStream_t stream) {
   mass::Params p{};
   p.scores = a.scores; p.mass = a.mass; p.out = a.out; p.lens = a.seq_lens;
   p.Hq = a.Hq; p.Hkv = a.Hkv; p.G = a.Hq / a.Hkv; p.T = a.max_len;
-  p.k = a.softmax_scale * 1.44269504088896340736f;
+  p.k = fabsf(a.softmax_scale) * 1.44269504088896340736f;
+  p.sign = a.softmax_scale < 0.f ? -1.f : 1.f;
   p.decay = a.decay;
   p.err = device_error_ptr();
   if (!p.err) return cudaErrorInvalidSymbol;

@@ -15,7 +15,8 @@
 // with the code bit as its sign, so the score comes out of the product scaled.
 // A 32-bit word pairs coordinates (j, j + 16) of a code word, one shift and
 // one LOP3 each, and U has its coordinates in the same order.  U is binary16
-// with a power-of-two scale per row (2^-12 of each entry, random in sign).
+// with a power-of-two scale per row (rounded by 2^-11 of each entry at most,
+// random in sign).
 //
 // A softmax thread holds one key and all NR rows.  The rows' maxima are shared
 // through shared memory and renewed only when a weight would pass 2^8 (one vote

@@ -14,7 +14,7 @@
 // Kernels, on one stream:
 //   1. prep     the queries as binary16 with a power-of-two scale per row (its
 //               largest entry lies in [2^13, 2^14): a bf16 query stays exact
-//               down to 2^-27 of the row's largest), and the plan.
+//               down to 2^-20 of the row's largest), and the plan.
 //   2. expand   khat as binary16, from the pages (dequant_tc.cu).
 //   3. attend   the products, below.
 //
@@ -27,7 +27,7 @@
 // (16 a clock and SM) take as long as the products, so the two units share
 // the time.  Products issued by one thread execute in order, so the next
 // scores may be issued over weights that an earlier product reads.
-// P is rounded to bf16 (half a step, 2^-9 of each weight, against values that
+// P is rounded to bf16 (half a step, 2^-8 of each weight, against values that
 // are bf16 themselves); its sum is taken before the rounding, in fp32.
 // The maximum is renewed only when a row's grows by more than 2^8: until then
 // weights up to 2^8 are as exact, and the accumulator need not be rescaled.
@@ -171,7 +171,7 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 // 2^x of a pair on the multiply-add pipe, for the share of the weights that
 // the exponential unit has no time for.  x = n + f with n the nearest whole
 // number, 2^f by the cubic with the least largest relative error on
-// [-1/2, 1/2] (Remez exchange; 7.5e-5 = 2^-13.7, a twentieth of the rounding to
+// [-1/2, 1/2] (Remez exchange; 7.5e-5 = 2^-13.7, a fiftieth of the rounding to
 // bf16 that follows), n added to the exponent.  x below -126 gives 2^-126.
 __device__ __forceinline__ float2 exp2_poly(f32x2 x) {
   constexpr float BIG = 12582912.f;  // 1.5 * 2^23: adding it rounds to a whole number

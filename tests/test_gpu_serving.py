@@ -1,0 +1,703 @@
+"""The serving operators against plain float64 implementations: rotary
+positions, a chunk into the pages, attention of a chunk, accumulated weights,
+eviction, and a run of them together.
+
+Tolerances are sums of the roundings on the way, written where they are used;
+a bf16 rounding is half a step, 2^-8 of the value, a binary16 one 2^-11, an
+fp32 one 2^-24.
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import bit_jl_key_b200 as jl
+import oracle
+from tests import helpers as H
+
+pytestmark = pytest.mark.gpu
+
+U32, U16, UB = 2.0 ** -24, 2.0 ** -11, 2.0 ** -8
+DEV = "cuda"
+
+
+def _rng(seed):
+    return np.random.default_rng(seed)
+
+
+def _randn(seed, *shape, dtype=torch.float32):
+    g = torch.Generator().manual_seed(seed)
+    return torch.randn(shape, generator=g).to(dtype).to(DEV)
+
+
+def _i32(a):
+    return torch.from_numpy(np.ascontiguousarray(a)).to(DEV, torch.int32)
+
+
+# --------------------------------------------------------------------------
+# rotary
+
+def rotary64(x, pos, freq, inter, inverse, scale):
+    """float64 numpy; also the sum |a| + |b| of each entry's pair."""
+    x = np.array(x, dtype=np.float64)
+    h = len(freq)
+    e, o = (slice(0, 2 * h, 2), slice(1, 2 * h, 2)) if inter else (slice(0, h), slice(h, 2 * h))
+    ang = (np.asarray(pos, np.float64)[:, None] * np.asarray(freq, np.float64))[:, None]
+    ang = -ang if inverse else ang
+    a, b = x[..., e].copy(), x[..., o].copy()
+    mag = np.zeros_like(x)
+    mag[..., e] = mag[..., o] = np.abs(a) + np.abs(b)
+    x[..., e] = scale * (a * np.cos(ang) - b * np.sin(ang))
+    x[..., o] = scale * (a * np.sin(ang) + b * np.cos(ang))
+    return x, mag * abs(scale)
+
+
+def check_rotary(got, x, pos, freq, inter, inverse, scale):
+    want, mag = rotary64(H.f64(x), pos.cpu().numpy(), freq.cpu().numpy(), inter, inverse, scale)
+    # fp32: sin and cos are off by 2 ulp (2^-23 at most), times scale, one
+    # product and one fma: 6 roundings of |a| + |b|; then the output's own
+    tol = 6 * U32 * mag + (UB if x.dtype == torch.bfloat16 else U32) * np.abs(want)
+    err = np.abs(H.f64(got) - want)
+    assert np.all(err <= tol + 1e-38), (err - tol).max()
+    r = 2 * len(freq)
+    assert torch.equal(got[..., r:], x[..., r:])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("n,Hq,Hkv,d,rot", [(1, 8, 2, 128, 128), (77, 6, 3, 64, 32),
+                                            (5, 1, 1, 128, 20), (300, 4, 4, 64, 64),
+                                            (2500, 2, 1, 128, 64), (3, 2, 2, 6, 2)])
+def test_rotary(dtype, inter, n, Hq, Hkv, d, rot):
+    qkv = _randn(1, n, Hq + 2 * Hkv, d, dtype=dtype)
+    Q, K = qkv[:, :Hq], qkv[:, Hq:Hq + Hkv]
+    rng = _rng(n)
+    pos = _i32(rng.integers(-5, 1 << 20, size=n))
+    freq = jl.jl_rotary_frequencies(rot, scaling="banded", factor=8.0, original_len=8192)
+    for inverse, scale in ((False, 1.0), (True, 1.0), (False, -1.3)):
+        oq, ok = jl.jl_rotary(Q, pos, freq, K=K, interleaved=inter, inverse=inverse, scale=scale)
+        check_rotary(oq, Q, pos, freq, inter, inverse, scale)
+        check_rotary(ok, K, pos, freq, inter, inverse, scale)
+    # queries alone; in place; into other strides; heads ahead of tokens
+    assert torch.equal(jl.jl_rotary(Q, pos, freq, interleaved=inter),
+                       jl.jl_rotary(Q, pos, freq, K=K, interleaved=inter)[0])
+    want = jl.jl_rotary(Q, pos, freq, K=K, interleaved=inter)
+    out = torch.full((Hq + 1, n, d + 8), 7.0, dtype=dtype, device=DEV)
+    view = out[:Hq, :, :d].transpose(0, 1)
+    jl.jl_rotary(Q.transpose(0, 1).contiguous().transpose(0, 1), pos, freq, interleaved=inter,
+                 out_q=view)
+    assert torch.equal(view, want[0])
+    assert torch.all(out[Hq] == 7.0) and torch.all(out[:, :, d:] == 7.0)
+    v_part = qkv[:, Hq + Hkv:].clone()
+    jl.jl_rotary(Q, pos, freq, K=K, interleaved=inter, out_q=Q, out_k=K)
+    assert torch.equal(Q, want[0]) and torch.equal(K, want[1])
+    assert torch.equal(qkv[:, Hq + Hkv:], v_part)
+
+
+def test_rotary_unaligned_rows_and_extremes():
+    d, n = 64, 9
+    flat = _randn(2, n * 3 * (d + 1) + 1)
+    Q = flat[1:].view(n, 3, d + 1)[..., :d]                    # rows at odd 4-byte offsets
+    pos = _i32([0, 1, -1, 2 ** 31 - 1, -2 ** 31, 1 << 20, 12345678, 3, 4])
+    freq = torch.tensor([1.0, 0.7, 1e-3, 0.0] + [0.1] * 28, device=DEV)
+    got = jl.jl_rotary(Q, pos, freq)
+    check_rotary(got, Q, pos, freq, False, False, 1.0)
+    assert jl.jl_rotary(Q[:0], pos[:0], freq).shape == (0, 3, d)
+    x = Q.clone()
+    x[0, 0, 0], x[1, 0, 1] = math.inf, math.nan                # stay in their own pairs
+    y = jl.jl_rotary(x, pos, freq)
+    bad = ~torch.isfinite(y)
+    assert {tuple(i) for i in bad.nonzero().tolist()} <= {(0, 0, 0), (0, 0, 32), (1, 0, 1),
+                                                          (1, 0, 33)}
+    with pytest.raises(jl.JLError):
+        jl.jl_rotary(Q, pos, torch.zeros(33, device=DEV))      # rot_dim above d
+
+
+def test_rotary_inverse_is_the_gradient():
+    n, Hq, d = 13, 3, 64
+    x, gy = _randn(3, n, Hq, d), _randn(4, n, Hq, d)
+    pos = _i32(_rng(0).integers(0, 5000, size=n))
+    freq = jl.jl_rotary_frequencies(48)
+    gx = jl.jl_rotary(gy, pos, freq, inverse=True, scale=1.5)
+    # the formula's gradient by autograd in float64 (the copied entries are not scaled)
+    xx = x.double().requires_grad_()
+    ang = pos.double()[:, None, None] * freq.double()
+    a, b = xx[..., :24], xx[..., 24:48]
+    y = torch.cat([1.5 * (a * ang.cos() - b * ang.sin()), 1.5 * (a * ang.sin() + b * ang.cos()),
+                   xx[..., 48:]], -1)
+    y.backward(gy.double())
+    assert torch.all((gx.double() - xx.grad).abs() <= 8 * U32 * 1.5 * 2 * gy.abs().max())
+    # and by differences: the rotation is linear, so any step serves
+    e = _randn(5, n, Hq, d)
+    f = lambda t: (jl.jl_rotary(t, pos, freq, scale=1.5).double() * gy.double()).sum()
+    diff = f(x + e) - f(x - e)
+    exact = 2 * (gx.double() * e.double()).sum()
+    # each of the sum's terms carries the roundings of an fp32 rotation
+    bound = 16 * U32 * 1.5 * 2 * ((x.abs() + e.abs()).double() * 2 * gy.abs().double().max()).sum()
+    assert abs(diff - exact) <= bound
+
+
+# --------------------------------------------------------------------------
+# a paged cache made from keys with the oracle's codes
+
+def table_for(lens, P, pages, rng, width=None):
+    width = width or max(1, max(-(-int(L) // P) for L in lens))
+    perm = rng.permutation(pages)
+    tab = np.full((len(lens), width), -1, dtype=np.int32)
+    k = 0
+    for b, L in enumerate(lens):
+        p = -(-int(L) // P)
+        tab[b, :p] = perm[k:k + p]
+        k += p
+    assert k <= pages
+    return tab
+
+
+class Cache:
+    """Pools full of garbage (random codes, NaN norms and values) apart from the
+    sequences' keys, whose code bits and norms are random too."""
+
+    def __init__(self, lens, Hkv, d, m, P, seed, norm_scale=None, extra=3):
+        rng = _rng(seed)
+        self.lens, self.Hkv, self.d, self.m, self.P = list(lens), Hkv, d, m, P
+        pages = sum(-(-int(L) // P) for L in lens) + extra
+        self.table = table_for(lens, P, pages, rng)
+        self.codes = rng.integers(0, 2 ** 32, size=(pages, Hkv, P, m // 32), dtype=np.uint64
+                                  ).astype(np.uint32)
+        self.norms = np.full((pages, Hkv, P), np.nan, np.float16)
+        self.values = torch.full((pages, Hkv, P, d), math.nan, dtype=torch.bfloat16)
+        scale = math.sqrt(d) if norm_scale is None else norm_scale
+        for b, L in enumerate(lens):
+            t = np.arange(L)
+            pg, sl = self.table[b, t // P], t % P
+            self.norms[pg, :, sl] = (scale * np.exp(0.3 * rng.standard_normal((L, Hkv)))
+                                     ).astype(np.float16)
+            self.values[pg, :, sl] = torch.from_numpy(rng.standard_normal((L, Hkv, d))
+                                                      ).to(torch.bfloat16)
+        self.S = jl.jl_sketch_init(m, d, 0)
+
+    def dev(self):
+        return (torch.from_numpy(self.codes.view(np.int32)).to(DEV),
+                torch.from_numpy(self.norms).to(DEV), self.values.to(DEV), _i32(self.table))
+
+    def keys(self, b, h):
+        """(khat [L, d] and its sketch form [L, m], values [L, d]) in float64."""
+        t = np.arange(self.lens[b])
+        pg, sl = self.table[b, t // self.P], t % self.P
+        z = H.code_bits(self.codes[pg, h, sl], self.m).astype(np.float64) * 2 - 1
+        zn = z * (self.norms[pg, h, sl].astype(np.float64) * math.sqrt(math.pi / 2) / self.m)[:, None]
+        return zn @ H.f64(self.S), zn, H.f64(self.values[pg, h, sl])
+
+
+def chunk64(c, Q, counts, scale, first=0):
+    """Attention of the chunk in float64 with the tolerance of each output:
+    {(row, head): (out, tol)}."""
+    S = H.f64(c.S)
+    Hq = Q.shape[1]
+    G = Hq // c.Hkv
+    out, row = {}, first
+    for b, n in enumerate(counts):
+        for h in range(c.Hkv):
+            khat, zn, v = c.keys(b, h)
+            for i in range(n):
+                seen = max(0, c.lens[b] - n + i + 1)
+                for g in range(G):
+                    q = H.f64(Q[row + i, h * G + g])
+                    if seen == 0:
+                        out[row + i, h * G + g] = (np.zeros(c.d), np.zeros(c.d))
+                        continue
+                    s = scale * (khat[:seen] @ q)
+                    w = np.exp(s - s.max())
+                    w /= w.sum()
+                    o = w @ v[:seen]
+                    A = w @ np.abs(v[:seen])
+                    # a logit's error: the projection u = S q, or q and khat, as
+                    # binary16, and the fp32 sums of m or d products
+                    by_u = np.abs(zn[:seen]) @ np.abs(S @ q) * (U16 + (c.m + c.d) * U32)
+                    by_k = np.abs(khat[:seen]) @ np.abs(q) * 2 * (U16 + c.d * U32)
+                    delta = abs(scale) * np.maximum(by_u, by_k).max()
+                    # plus the fp32 exponent's own rounding, relative to its size
+                    delta += 4 * U32 * (np.abs(s).max() + 8)
+                    # weights: bf16 and the exponential's 2^-13; output: bf16
+                    tol = (UB + 2.0 ** -13 + 2 * delta * math.exp(2 * delta)) * 1.01 * A
+                    tol += UB * (np.abs(o) + tol) + 1e-30
+                    out[row + i, h * G + g] = (o, tol)
+        row += n
+    return out
+
+
+def run_chunk(c, Q, counts, lens=None, pad=(0, 0), scale=None, **kw):
+    """The call on a batch with pad[0] rows before and pad[1] behind."""
+    cu = pad[0] + np.concatenate([[0], np.cumsum(counts)])
+    codes, norms, values, table = c.dev()
+    lens = c.lens if lens is None else lens
+    out = torch.full((Q.shape[0], Q.shape[1], c.d), 7.0, dtype=torch.bfloat16, device=DEV)
+    return jl.jl_chunk_attention_paged(Q, c.S, codes, norms, values, table, _i32(lens), _i32(cu),
+                                       max(max(lens), 1), softmax_scale=scale, out=out, **kw)
+
+
+def check_chunk(c, Q, counts, got, scale, first=0):
+    g = H.f64(got)
+    for (r, h), (o, tol) in chunk64(c, Q, counts, scale, first).items():
+        if np.isnan(o).all():                                   # infinite norms: no answer
+            assert np.isnan(g[r, h]).all(), (r, h)
+            continue
+        err = np.abs(g[r, h] - o)
+        assert np.all(err <= tol), (r, h, (err / np.maximum(tol, 1e-30)).max())
+
+
+CHUNKS = [
+    # lens, counts, Hq, Hkv, d, m, P, dtype
+    ([1], [1], 1, 1, 64, 64, 32, torch.bfloat16),
+    ([130, 1, 64], [3, 1, 2], 8, 2, 128, 256, 32, torch.bfloat16),      # few rows, granule 32
+    ([257, 100], [5, 8], 8, 1, 128, 128, 64, torch.float32),             # 64-row tiles
+    ([300, 129, 128], [9, 2, 0], 6, 2, 64, 512, 96, torch.bfloat16),     # G = 3, no row of b = 2
+    ([40, 700], [12, 3], 10, 2, 128, 512, 128, torch.float32),           # G = 5, granule 128
+    ([200, 33], [200, 33], 4, 2, 128, 256, 64, torch.bfloat16),          # whole prompts: many rows
+    ([310], [310], 3, 3, 64, 128, 32, torch.float32),
+    ([129, 260], [129, 131], 2, 1, 64, 64, 96, torch.bfloat16),
+    ([500], [170], 16, 1, 128, 512, 128, torch.bfloat16),                # long row tiles, causal
+    ([5, 3, 140], [9, 3, 141], 4, 2, 128, 128, 32, torch.bfloat16),      # n > L: rows that see nothing
+    ([2, 0, 3], [5, 2, 1], 4, 2, 64, 64, 64, torch.bfloat16),            # and an empty cache
+]
+
+
+@pytest.mark.parametrize("lens,counts,Hq,Hkv,d,m,P,dtype", CHUNKS)
+def test_chunk_attention(lens, counts, Hq, Hkv, d, m, P, dtype):
+    c = Cache(lens, Hkv, d, m, P, seed=len(lens) + d + m)
+    N, pad = sum(counts), (2, 3)
+    Q = _randn(7, N + 5, Hq, d, dtype=dtype)
+    got = run_chunk(c, Q, counts, pad=pad)
+    check_chunk(c, Q, counts, got, d ** -0.5, first=2)
+    # rows of no sequence stay as they were
+    assert torch.all(got[:2] == 7.0) and torch.all(got[2 + N:] == 7.0)
+    # the same again, bit for bit
+    assert torch.equal(got, run_chunk(c, Q, counts, pad=pad))
+
+
+@pytest.mark.parametrize("rows", [4, 400])
+@pytest.mark.parametrize("scale", [0.0, -0.05, 0.3])
+def test_chunk_attention_scales_and_strides(rows, scale):
+    c = Cache([rows + 150], 2, 64, 128, 64, seed=3)
+    qkv = _randn(8, rows, 8, 64 + 16, dtype=torch.bfloat16)
+    Q = qkv[:, 2:6, 8:72]                                       # strided heads and tokens
+    got = run_chunk(c, Q, [rows], scale=scale)
+    check_chunk(c, Q, [rows], got, scale)
+    Qt = Q.transpose(0, 1).contiguous().transpose(0, 1)         # heads ahead of tokens
+    assert torch.equal(got, run_chunk(c, Qt, [rows], scale=scale))
+    odd = torch.zeros(rows * 4 * 64 + 1, dtype=torch.bfloat16, device=DEV)[1:].view(rows, 4, 64)
+    odd.copy_(Q)                                                # rows at odd 2-byte offsets
+    assert torch.equal(got, run_chunk(c, odd, [rows], scale=scale))
+
+
+@pytest.mark.parametrize("n", [6, 300])
+def test_chunk_attention_large_and_small_magnitudes(n):
+    """Norms and queries far from 1: peaked rows, nearly uniform ones, zeros;
+    the last scale passes binary16 for some keys, whose norms are infinite."""
+    for norm_scale, q_scale in ((300.0, 1.0), (1e-3, 1e-3), (0.05, 2e4), (6e4, 1e-4)):
+        c = Cache([n + 200], 1, 64, 128, 64, seed=5, norm_scale=norm_scale)
+        Q = _randn(9, n, 2, 64) * q_scale
+        Q[1] = 0.0
+        check_chunk(c, Q, [n], run_chunk(c, Q, [n]), 64 ** -0.5)
+
+
+@pytest.mark.parametrize("n", [5, 300])
+def test_chunk_attention_long_split_context(n):
+    """One sequence over every block of the grid, each with a state to join."""
+    c = Cache([20000], 1, 64, 64, 64, seed=6)
+    Q = _randn(10, n, 2, 64, dtype=torch.bfloat16)
+    got = run_chunk(c, Q, [n])
+    for i in (0, 1, n // 2, n - 1):                             # some rows, the last ones
+        sub = Cache.__new__(Cache)
+        sub.__dict__ = dict(c.__dict__, lens=[20000 - n + i + 1])
+        check_chunk(sub, Q[i:i + 1], [1], got[i:i + 1], 64 ** -0.5)
+
+
+def test_chunk_attention_equals_decode_steps():
+    """Row i of a chunk is a decode step over the keys it sees."""
+    Hq, Hkv, d, m, P, n, L = 8, 2, 128, 256, 64, 5, 333
+    c = Cache([L], Hkv, d, m, P, seed=11)
+    Q = _randn(12, n, Hq, d, dtype=torch.bfloat16)
+    got = run_chunk(c, Q, [n]).float()
+    codes, norms, values, table = c.dev()
+    for i in range(n):
+        step = jl.jl_decode_attention_paged(Q[i:i + 1].contiguous(), c.S, codes, norms, values,
+                                            table, _i32([L - n + i + 1]), L).float()[0]
+        # both round weights and outputs to bf16, and values are N(0, 1)
+        assert (got[i] - step).abs().max() <= 4 * UB
+
+
+def test_chunk_attention_nan_and_inf_stay_in_their_rows():
+    c = Cache([150], 1, 64, 128, 32, seed=13)
+    for n in (4, 320):
+        c.lens[0] = 150
+        Q = _randn(14, n, 2, 64)
+        ref = run_chunk(c, Q, [n])
+        Q[1, 0, 3], Q[2, 1, 5] = math.nan, math.inf
+        got = run_chunk(c, Q, [n])
+        same = torch.ones(n, 2, dtype=torch.bool)
+        same[1, 0] = same[2, 1] = False
+        assert torch.equal(got[same.to(DEV)], ref[same.to(DEV)])
+        seen = [150 - n + i + 1 > 0 for i in (1, 2)]
+        if seen[0]:
+            assert torch.isnan(got[1, 0]).all()
+        if seen[1]:
+            assert not torch.isfinite(got[2, 1].float()).any()
+    # a masked key's norm may be anything: the last key is seen by the last row alone
+    n = 4
+    pg, sl = c.table[0, 149 // 32], 149 % 32
+    for x in (math.nan, math.inf):
+        Q = _randn(15, n, 2, 64)
+        ref = run_chunk(c, Q, [n])
+        old = c.norms[pg, 0, sl]
+        c.norms[pg, 0, sl] = x
+        got = run_chunk(c, Q, [n])
+        c.norms[pg, 0, sl] = old
+        assert torch.equal(got[:n - 1], ref[:n - 1])
+
+
+def test_chunk_attention_bad_lengths_and_pages_are_reported():
+    c = Cache([100, 70], 1, 64, 64, 32, seed=16)
+    Q = _randn(17, 8, 1, 64)
+    codes, norms, values, table = c.dev()
+    ref = run_chunk(c, Q, [4, 4])
+    call = lambda lens, cu, tab=table, max_len=100: jl.jl_chunk_attention_paged(
+        Q, c.S, codes, norms, values, tab, _i32(lens), _i32(cu), max_len,
+        out=torch.zeros(8, 1, 64, dtype=torch.bfloat16, device=DEV))
+    for lens, cu in (([100, 101], [0, 4, 8]), ([100, -1], [0, 4, 8]), ([100, 70], [0, 4, 9]),
+                     ([100, 70], [0, 4, 3]), ([100, 70], [-1, 4, 8])):
+        got = call(lens, cu)
+        assert jl.jl_device_error() == jl.JL_DERR_DECODE_PLAN, (lens, cu)
+        if cu[:2] == [0, 4]:
+            assert torch.equal(got[:4], ref[:4])                # the other sequence is served
+    # rows given to two sequences: the later one is dropped
+    bad3 = jl.jl_chunk_attention_paged(Q, c.S, codes, norms, values, table[[0, 1, 0]].contiguous(),
+                                       _i32([100, 70, 100]), _i32([0, 8, 2, 8]), 100)
+    torch.cuda.synchronize()
+    assert bad3.shape == Q.shape and jl.jl_device_error() == jl.JL_DERR_DECODE_PLAN
+    for entry in (-1, codes.shape[0], 2 ** 31 - 1):
+        tab = table.clone()
+        tab[1, 1] = entry
+        got = call([100, 70], [0, 4, 8], tab)
+        assert jl.jl_device_error() == jl.JL_DERR_PAGE
+        assert torch.equal(got[:4], ref[:4])
+    assert torch.equal(call([100, 70], [0, 4, 8]), ref) and jl.jl_device_error() == 0
+
+
+@pytest.mark.parametrize("n", [7, 200])
+def test_chunk_attention_graphs_streams_and_workspaces(n):
+    c = Cache([400, 350], 2, 128, 128, 64, seed=18)
+    counts = [n, n]
+    Qs = [_randn(20 + i, 2 * n, 4, 128, dtype=torch.bfloat16) for i in range(3)]
+    refs = [run_chunk(c, q, counts) for q in Qs]
+    codes, norms, values, table = c.dev()
+    lens, cu = _i32(c.lens), _i32([0, n, 2 * n])
+    need = jl.jl_chunk_attention_workspace_bytes(2 * n, 2, 4, 2, 400, 128, 128)
+    ws = torch.full((need,), 255, dtype=torch.uint8, device=DEV)    # contents do not matter
+    call = lambda q, out=None, **k: jl.jl_chunk_attention_paged(q, c.S, codes, norms, values, table,
+                                                                lens, cu, 400, out=out, **k)
+    assert torch.equal(call(Qs[0], workspace=ws), refs[0])
+    with pytest.raises(jl.JLError) as e:
+        call(Qs[0], workspace=ws[:-256])
+    assert e.value.status == jl.JL_ERR_WORKSPACE
+    # two graphs over one workspace, replayed in turn with other queries
+    q_in, outs, graphs = [q.clone() for q in Qs[:2]], [], []
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for q in q_in:
+        g, out = torch.cuda.CUDAGraph(), torch.zeros_like(refs[0])
+        with torch.cuda.graph(g, stream=side):
+            call(q, out=out, workspace=ws)
+        graphs.append(g)
+        outs.append(out)
+    for order in ((0, 1), (1, 0)):
+        for i in order:
+            graphs[i].replay()
+    q_in[0].copy_(Qs[2])
+    graphs[0].replay()
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], refs[2]) and torch.equal(outs[1], refs[1])
+    # calls side by side on two streams, each with a workspace of its own
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(5):
+        got.append((call(Qs[0], stream=s1), call(Qs[1], stream=s2)))
+    torch.cuda.synchronize()
+    for a, b in got:
+        assert torch.equal(a, refs[0]) and torch.equal(b, refs[1])
+    raw = call(Qs[0], stream=s1.cuda_stream)                    # a stream as its handle
+    torch.cuda.synchronize()
+    assert torch.equal(raw, refs[0])
+
+
+# --------------------------------------------------------------------------
+# store
+
+@pytest.mark.parametrize("W,cn,d", [(8, 1, 128), (2, 1, 64), (12, 2, 128), (3, 2, 64)])
+def test_store(W, cn, d):
+    Hkv, P, counts, before = 3, 32, [5, 0, 40, 1], [0, 10, 60, 31]
+    N, pad = sum(counts), 2
+    rng = _rng(1)
+    tab = table_for([a + b for a, b in zip(before, counts)], P, 12, rng)
+    one = () if cn == 1 else (2,)
+    make = lambda lead, s: (_i32(rng.integers(-2 ** 31, 2 ** 31, size=(*lead, W))),
+                            _randn(s, *lead, *one).half(),
+                            _randn(s + 1, *lead, d, dtype=torch.bfloat16))
+    pools = make((12, Hkv, P), 2)
+    codes, norms, _ = make((N + pad, Hkv), 4)
+    V = _randn(6, N + pad, 2 * Hkv + 1, d, dtype=torch.bfloat16)[:, Hkv:2 * Hkv]
+    want = [t.clone() for t in pools]
+    r = 1
+    for b, n in enumerate(counts):
+        for i in range(n):
+            pg, sl = tab[b, (before[b] + i) // P], (before[b] + i) % P
+            for w, x in zip(want, (codes, norms, V)):
+                w[pg, :, sl] = x[r]
+            r += 1
+    cu = 1 + np.concatenate([[0], np.cumsum(counts)])
+    jl.jl_store_paged(codes, norms, V, _i32(cu), *pools, _i32(tab), _i32(before))
+    for w, p in zip(want, pools):
+        assert torch.equal(w, p)
+    # no row, no sequence
+    jl.jl_store_paged(codes[:0], norms[:0], V[:0], _i32([0] * 5), *pools, _i32(tab), _i32(before))
+    for w, p in zip(want, pools):
+        assert torch.equal(w, p)
+
+
+def test_store_bad_pages_skip_and_report():
+    Hkv, P, d = 2, 32, 64
+    pools = (torch.zeros(4, Hkv, P, 2, dtype=torch.int32, device=DEV),
+             torch.zeros(4, Hkv, P, dtype=torch.float16, device=DEV),
+             torch.zeros(4, Hkv, P, d, dtype=torch.bfloat16, device=DEV))
+    codes = torch.ones(6, Hkv, 2, dtype=torch.int32, device=DEV)
+    norms = torch.ones(6, Hkv, dtype=torch.float16, device=DEV)
+    V = torch.ones(6, Hkv, d, dtype=torch.bfloat16, device=DEV)
+    for tab, before in (([[0, 4]], [29]), ([[0, -1]], [29]), ([[0]], [29]), ([[0, 1]], [-3]),
+                        ([[0, 1]], [61])):
+        for p in pools:
+            p.zero_()
+        jl.jl_store_paged(codes, norms, V, _i32([0, 6]), *pools, _i32(tab), _i32(before))
+        assert jl.jl_device_error() == jl.JL_DERR_PAGE
+        assert pools[0].sum() == 3 * Hkv * 2 and pools[2].float().sum() == 3 * Hkv * d
+
+
+# --------------------------------------------------------------------------
+# accumulated weights
+
+@pytest.mark.parametrize("B,Hq,Hkv,T", [(1, 1, 1, 1), (3, 6, 2, 77), (2, 8, 8, 4096),
+                                        (2, 16, 1, 9000), (1, 4, 2, 70001)])
+@pytest.mark.parametrize("decay", [1.0, 0.5, 0.0])
+def test_accumulate(B, Hq, Hkv, T, decay):
+    rng = _rng(T)
+    lens = rng.integers(0, T + 1, size=B)
+    lens[0] = T
+    scores = _randn(1, B, Hq, T) * 20
+    for b in range(B):
+        scores[b, :, lens[b]:] = math.nan                       # never read into a result
+    mass = _randn(2, B, Hkv, T).abs()
+    scale = 0.11
+    out = torch.full_like(mass, 5.0)
+    m_in = torch.full_like(mass, math.nan) if decay == 0.0 else mass
+    got = jl.jl_accumulate_attention(scores, m_in, _i32(lens), scale, decay=decay, out=out)
+    assert got is out
+    for b, L in enumerate(lens):
+        assert torch.all(out[b, :, L:] == 5.0)
+        if L == 0:
+            continue
+        x = H.f64(scores[b, :, :L]) * scale
+        w = np.exp(x - x.max(-1, keepdims=True))
+        w /= w.sum(-1, keepdims=True)
+        W = w.reshape(Hkv, Hq // Hkv, L).sum(1)
+        old = decay * H.f64(mass[b, :, :L])
+        # exponents in fp32 (four roundings of their size, in the statistics
+        # and in the weight), exp2's 2 ulp each, sums of up to T / 2048 + 64
+        tol = W * U32 * (8 * (np.abs(x).max() * 1.5 + 1) + 80 + T / 1024) + 2 * U32 * (old + W)
+        assert np.all(np.abs(H.f64(out[b, :, :L]) - (old + W)) <= tol + 1e-37)
+    if decay:
+        again = jl.jl_accumulate_attention(scores, mass, _i32(lens), scale, decay=decay)
+        assert again is mass                                     # in place
+        for b, L in enumerate(lens):
+            assert torch.equal(mass[b, :, :L], out[b, :, :L])
+
+
+def test_accumulate_masked_rows_and_lengths():
+    B, Hq, Hkv, T = 2, 4, 2, 100
+    scores = _randn(3, B, Hq, T)
+    scores[0, 0] = -math.inf                                     # a head with nothing
+    scores[0, 1, ::2] = -math.inf
+    scores[1, 3] = torch.finfo(torch.float32).min                # the lowest value, everywhere
+    out = jl.jl_accumulate_attention(scores, torch.zeros(B, Hkv, T, device=DEV), _i32([T, T]), 1.0)
+    assert torch.isfinite(out).all()
+    assert abs(out[0, 0].sum().item() - 1) < 1e-5 and torch.all(out[0, 0, ::2] == 0)
+    assert abs(out[1, 1].sum().item() - 2) < 1e-5
+    out = jl.jl_accumulate_attention(scores, torch.zeros(B, Hkv, T, device=DEV), _i32([-1, T + 1]),
+                                     1.0)
+    assert jl.jl_device_error() == jl.JL_DERR_DECODE_PLAN
+    assert torch.all(out[0] == 0) and abs(out[1, 0].sum().item() - 2) < 1e-5
+
+
+# --------------------------------------------------------------------------
+# eviction
+
+def evict64(mass, L, keep, recent, sink):
+    if L <= keep:
+        return np.arange(L)
+    cand = np.arange(sink, L - recent)
+    rank = np.where(np.isnan(mass[cand]), -np.inf, mass[cand])
+    nan_last = np.isnan(mass[cand])
+    order = sorted(range(len(cand)), key=lambda i: (nan_last[i], -rank[i], i))
+    best = cand[order[:keep - recent - sink]]
+    return np.sort(np.concatenate([np.arange(sink), best, np.arange(L - recent, L)]))
+
+
+@pytest.mark.parametrize("lens,keep,recent,sink,W,cn,d,P", [
+    ([100, 33, 0, 64], 40, 8, 4, 8, 1, 128, 32),
+    ([1], 1, 0, 0, 2, 1, 64, 32),
+    ([5000, 4999], 777, 100, 3, 12, 2, 64, 64),
+    ([20000], 9001, 0, 0, 4, 1, 64, 128),
+    ([90, 91], 90, 40, 50, 3, 2, 128, 96),                       # nothing is chosen by mass
+    ([50, 60], 100, 10, 2, 4, 1, 64, 32),                        # everything stays
+])
+def test_evict(lens, keep, recent, sink, W, cn, d, P):
+    B, Hkv, T = len(lens), 2, max(lens) + 3
+    rng = _rng(keep)
+    new = [min(L, keep) for L in lens]
+    need = [sum(-(-x // P) for x in v) for v in (lens, new)]
+    pages = sum(need) + 2
+    both = table_for(lens + new, P, pages, rng, width=-(-max(T, keep) // P))
+    src, dst = both[:B], both[B:]
+    one = () if cn == 1 else (2,)
+    pools = (_i32(rng.integers(-2 ** 31, 2 ** 31, size=(pages, Hkv, P, W))),
+             _randn(1, pages, Hkv, P, *one).half(), _randn(2, pages, Hkv, P, d,
+                                                           dtype=torch.bfloat16))
+    mass = rng.standard_normal((B, Hkv, T)).astype(np.float32)
+    mass[mass < -0.5] = 0.0                                      # ties, and both zeros
+    mass[:, 1, ::7] = -0.0
+    mass[:, 0, 5::11] = 0.25
+    mass[:, 0, 1::50], mass[:, 1, 2::60], mass[:, 1, 3::70] = np.nan, np.inf, -np.inf
+    want = [t.clone() for t in pools]
+    m = torch.from_numpy(mass).to(DEV)
+    idx, om, ol = jl.jl_evict_paged(m, _i32(lens), keep, *pools, _i32(src), _i32(dst),
+                                    recent=recent, sink=sink)
+    assert ol.tolist() == new
+    for b, L in enumerate(lens):
+        for h in range(Hkv):
+            t = evict64(mass[b, h], L, keep, recent, sink)
+            assert np.array_equal(idx[b, h, :len(t)].cpu().numpy(), t)
+            assert torch.all(idx[b, h, len(t):] == -1) and torch.all(om[b, h, len(t):] == 0)
+            assert np.array_equal(om[b, h, :len(t)].cpu().numpy(), mass[b, h, t], equal_nan=True)
+            j = np.arange(len(t))
+            for w in want:
+                w[dst[b, j // P], h, j % P] = w[src[b, t // P], h, t % P]
+    for w, p in zip(want, pools):
+        assert torch.equal(w, p)                                 # all other rows as they were
+
+
+def test_evict_long_rows_read_from_memory():
+    """More keys than the blocks of a cluster can hold in shared memory."""
+    L, keep, P = 420000, 1000, 128
+    mass = _randn(3, 1, 1, L)
+    pages = -(-L // P) + -(-keep // P)
+    pools = (torch.arange(pages * P, dtype=torch.int32, device=DEV).view(pages, 1, P, 1),
+             torch.zeros(pages, 1, P, dtype=torch.float16, device=DEV),
+             torch.zeros(pages, 1, P, 64, dtype=torch.bfloat16, device=DEV))
+    tab = torch.arange(pages, dtype=torch.int32, device=DEV)[None]
+    src, dst = tab[:, :-(-L // P)].contiguous(), tab[:, -(-L // P):].contiguous()
+    idx, om, _ = jl.jl_evict_paged(mass, _i32([L]), keep, *pools, src, dst, recent=10, sink=1)
+    want = evict64(mass[0, 0].cpu().numpy(), L, keep, 10, 1)
+    assert np.array_equal(idx[0, 0].cpu().numpy(), want)
+    assert np.array_equal(pools[0].view(-1)[-(-L // P) * P:][:keep].cpu().numpy(), want)
+
+
+def test_evict_bad_lengths_and_pages_are_reported():
+    P, d, keep = 32, 64, 20
+    pools = (torch.ones(6, 1, P, 2, dtype=torch.int32, device=DEV),
+             torch.ones(6, 1, P, dtype=torch.float16, device=DEV),
+             torch.ones(6, 1, P, d, dtype=torch.bfloat16, device=DEV))
+    mass = _randn(4, 1, 1, 50)
+    for lens, src, dst, code in (([51], [[0, 1]], [[2]], jl.JL_DERR_DECODE_PLAN),
+                                 ([-1], [[0, 1]], [[2]], jl.JL_DERR_DECODE_PLAN),
+                                 ([50], [[0, 6]], [[2]], jl.JL_DERR_PAGE),
+                                 ([50], [[0, 1]], [[-1]], jl.JL_DERR_PAGE)):
+        _, _, ol = jl.jl_evict_paged(mass, _i32(lens), keep, *pools, _i32(src), _i32(dst))
+        assert jl.jl_device_error() == code
+        assert ol.item() == max(0, min(lens[0], keep))
+
+
+# --------------------------------------------------------------------------
+# the operators together
+
+def test_serving_loop():
+    """A prompt in pieces, drafted tokens, decode steps and an eviction over one
+    paged cache: every attention output against float64 on the codes that the
+    cache then holds, and the cache after the eviction against the kept keys."""
+    B, Hq, Hkv, d, m, P, max_len = 2, 8, 2, 128, 256, 64, 512
+    G = Hq // Hkv
+    S = jl.jl_sketch_init(m, d, 0)
+    freq = jl.jl_rotary_frequencies(d)
+    pages = 2 * B * (max_len // P)
+    pools = (torch.zeros(pages, Hkv, P, m // 32, dtype=torch.int32, device=DEV),
+             torch.full((pages, Hkv, P), math.nan, dtype=torch.float16, device=DEV),
+             torch.full((pages, Hkv, P, d), math.nan, dtype=torch.bfloat16, device=DEV))
+    perm = _rng(0).permutation(pages).astype(np.int32)
+    table = _i32(perm[:pages // 2].reshape(B, -1))
+    spare = _i32(perm[pages // 2:].reshape(B, -1))
+    lens = torch.zeros(B, dtype=torch.int32, device=DEV)
+
+    def view(lens_now, tab):
+        c = Cache.__new__(Cache)
+        c.lens, c.Hkv, c.d, c.m, c.P, c.S = lens_now.tolist(), Hkv, d, m, P, S
+        c.codes, c.norms = H.u32(pools[0]), pools[1].cpu().numpy()
+        c.values, c.table = pools[2].cpu(), tab.cpu().numpy()
+        return c
+
+    for step, counts in enumerate(([200, 150], [37, 90], [4, 1])):
+        N = sum(counts)
+        qkv = _randn(30 + step, N, Hq + 2 * Hkv, d, dtype=torch.bfloat16)
+        cu = _i32(np.concatenate([[0], np.cumsum(counts)]))
+        pos = torch.cat([lens[b] + torch.arange(n, device=DEV, dtype=torch.int32)
+                         for b, n in enumerate(counts)])
+        q, k = jl.jl_rotary(qkv[:, :Hq], pos, freq, K=qkv[:, Hq:Hq + Hkv])
+        signs, norms = jl.jl_quantize_keys(k, S)
+        jl.jl_store_paged(signs.view(N, Hkv, -1), norms.view(N, Hkv), qkv[:, Hq + Hkv:], cu,
+                          *pools, table, lens)
+        lens += cu.diff()
+        out = jl.jl_chunk_attention_paged(q, S, *pools, table, lens, cu, max_len)
+        c = view(lens, table)
+        # the rows' codes are the quantizer's, wherever they lie
+        t = c.lens[0] - 1
+        assert np.array_equal(c.codes[c.table[0, t // P], :, t % P],
+                              H.u32(signs.view(N, Hkv, -1)[counts[0] - 1]))
+        check_chunk(c, q, counts, out, d ** -0.5)
+
+    mass = torch.zeros(B, Hkv, max_len, device=DEV)
+    for step in range(3):
+        q, kn, vn = (_randn(50 + 3 * step + i, B, h, d, dtype=torch.bfloat16)
+                     for i, h in enumerate((Hq, Hkv, Hkv)))
+        q, kn = jl.jl_rotary(q, lens, freq, K=kn)
+        _, sc = jl.jl_decode_attention_paged(q, S, *pools, table, lens, max_len, K_new=kn,
+                                             V_new=vn, want_scores=True)
+        lens += 1
+        jl.jl_accumulate_attention(sc, mass, lens, d ** -0.5)
+    for b in range(B):                                           # every head gave weight 1 a step
+        assert torch.all((mass[b, :, :lens[b]].sum(-1) - 3 * G).abs() < 1e-3)
+    keep = 100
+    idx, kept, new = jl.jl_evict_paged(mass, lens, keep, *pools, table, spare, recent=16, sink=4)
+    assert new.tolist() == [keep] * B
+    before, after = view(lens, table), view(new, spare)
+    for b in range(B):
+        for h in range(Hkv):
+            t = idx[b, h].cpu().numpy()
+            assert np.array_equal(t, evict64(mass[b, h].cpu().numpy(), int(lens[b]), keep, 16, 4))
+            for x, y in zip(before.keys(b, h), after.keys(b, h)):
+                assert np.array_equal(x[t], y)
+    # and decoding goes on, over the kept keys
+    q = _randn(70, B, Hq, d, dtype=torch.bfloat16)
+    out = jl.jl_decode_attention_paged(q, S, *pools, spare, new, max_len)
+    ref = chunk64(after, q, [1, 1], d ** -0.5)
+    for (r, h), (o, tol) in ref.items():
+        # the decode kernel's projections carry 16 bits: inside the same bounds
+        assert np.all(np.abs(H.f64(out[r, h]) - o) <= tol + 2 * UB)
+    assert jl.jl_device_error() == 0

@@ -1,0 +1,227 @@
+"""Host-side checks of the serving operators (rotary, chunk store, chunk
+attention, accumulated weights, eviction): bad arguments are refused before
+anything is launched, by the C entry points and by the Python wrappers, and the
+rotary frequencies equal their formulas.  None of it needs a GPU."""
+import ctypes
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import bit_jl_key_b200 as jl
+
+NULL = ctypes.c_void_p(0)
+FAKE = ctypes.c_void_p(1 << 20)          # 16-byte aligned, never dereferenced
+FAKE2 = ctypes.c_void_p(1 << 21)
+ODD = ctypes.c_void_p((1 << 20) + 2)
+
+INVALID, UNSUPPORTED, OK, WORKSPACE = (jl.JL_ERR_INVALID_ARG, jl.JL_ERR_UNSUPPORTED, jl.JL_OK,
+                                       jl.JL_ERR_WORKSPACE)
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from bit_jl_key_b200 import build
+    build.build()
+    return jl.load()
+
+
+def caller(f, **defaults):
+    def call(**kw):
+        assert set(kw) <= set(defaults), kw
+        return f(*dict(defaults, **kw).values())
+    return call
+
+
+# --------------------------------------------------------------------------
+
+@pytest.mark.parametrize("rot", [2, 20, 64, 128])
+@pytest.mark.parametrize("base", [10000.0, 500000.0])
+def test_frequencies(lib, rot, base):
+    j = np.arange(rot // 2)
+    plain = base ** (-2.0 * j / rot)
+    get = lambda *a, **k: jl.jl_rotary_frequencies(rot, base, *a, device="cpu", **k).double().numpy()
+    # each is rounded to float once: half a step, 2^-24 of the value (and the
+    # float64 pow's own error, far below)
+    close = lambda a, b: np.all(np.abs(a - b) <= 2.0 ** -23 * np.abs(b))
+    assert close(get(), plain)
+    assert close(get("linear", factor=4.0), plain / 4.0)
+    ntk = get("ntk", factor=8.0)
+    if rot > 2:
+        assert close(ntk, (base * 8.0 ** (rot / (rot - 2))) ** (-2.0 * j / rot))
+        assert close(ntk[-1:], plain[-1:] / 8.0) and ntk[0] == 1.0
+    band = get("banded", factor=8.0, original_len=8192, low=1.0, high=4.0)
+    turns = 8192 * plain / (2 * math.pi)
+    assert close(band[turns >= 4.0], plain[turns >= 4.0])
+    assert close(band[turns <= 1.0], plain[turns <= 1.0] / 8.0)
+    mid = (turns > 1.0) & (turns < 4.0)
+    x = (turns[mid] - 1.0) / 3.0
+    assert close(band[mid], plain[mid] * (x + (1 - x) / 8.0))
+
+
+def test_frequencies_refused(lib):
+    buf = (ctypes.c_float * 64)()
+    call = caller(lib.jl_rotary_frequencies, r=64, base=1e4, sc=0, factor=2.0, L=10, low=1.0,
+                  high=4.0, out=ctypes.cast(buf, ctypes.c_void_p))
+    assert call() == OK
+    for bad in (dict(r=63), dict(r=0), dict(r=2048), dict(base=1.0), dict(base=math.nan),
+                dict(base=math.inf), dict(sc=4), dict(sc=-1), dict(out=NULL),
+                dict(sc=1, factor=0.0), dict(sc=2, factor=math.nan), dict(sc=3, L=0),
+                dict(sc=3, low=4.0), dict(sc=3, high=math.nan)):
+        assert call(**bad) == INVALID, bad
+    with pytest.raises(ValueError):
+        jl.jl_rotary_frequencies(64, scaling="other", device="cpu")
+
+
+def test_rotary_refused(lib):
+    call = caller(lib.jl_rotary, Q=FAKE, K=FAKE, dt=jl.JL_BF16, n=4, Hq=8, Hkv=2, d=128, rot=128,
+                  qt=1024, qh=128, kt=256, kh=128, pos=FAKE, freq=FAKE, inter=0, inv=0, scale=1.0,
+                  oq=FAKE2, oqt=1024, oqh=128, ok=FAKE2, okt=256, okh=128, stream=NULL)
+    assert call(n=0) == OK
+    for bad in (dict(dt=2), dict(n=-1), dict(Hq=0), dict(Hkv=0), dict(rot=127), dict(rot=0),
+                dict(rot=130), dict(Q=NULL), dict(oq=NULL), dict(ok=NULL), dict(pos=NULL),
+                dict(freq=NULL), dict(Q=ctypes.c_void_p((1 << 20) + 1)), dict(pos=ODD),
+                dict(dt=jl.JL_F32, Q=ODD), dict(inter=2), dict(inv=-1), dict(scale=math.nan),
+                dict(scale=math.inf), dict(qt=-1), dict(oqh=64), dict(oqt=0), dict(oqt=512),
+                dict(okt=128, okh=128)):
+        assert call(**bad) == INVALID, bad
+    for bad in (dict(d=129, rot=2, qh=129, oqh=129, oqt=2000, kh=129, okh=129, okt=400),
+                dict(d=2048, qh=2048, oqh=2048, oqt=1 << 20), dict(n=1 << 31)):
+        assert call(**bad) == UNSUPPORTED, bad
+
+
+POOLS = dict(codes=FAKE, norms=FAKE, values=FAKE, pages=10, P=64)
+
+
+def test_store_refused(lib):
+    call = caller(lib.jl_store_paged, c=FAKE, n=FAKE, V=FAKE, vt=256, vh=128, N=10, Hkv=2, words=8,
+                  cn=1, d=128, cu=FAKE, B=2, **POOLS, table=FAKE, mp=4, lens=FAKE, stream=NULL)
+    assert call(N=0) == OK and call(B=0) == OK
+    for bad in (dict(N=-1), dict(B=-1), dict(mp=0), dict(Hkv=0), dict(pages=0), dict(P=48),
+                dict(P=0), dict(codes=NULL), dict(norms=ODD), dict(values=ODD), dict(c=NULL),
+                dict(c=ODD), dict(n=NULL), dict(V=NULL), dict(V=ODD), dict(vt=4), dict(vh=-8),
+                dict(cu=NULL), dict(cu=ODD), dict(table=NULL), dict(lens=NULL)):
+        assert call(**bad) == INVALID, bad
+    for bad in (dict(d=96), dict(words=0), dict(words=65), dict(cn=0), dict(cn=3), dict(N=1 << 31),
+                dict(Hkv=1 << 16)):
+        assert call(**bad) == UNSUPPORTED, bad
+
+
+def test_chunk_refused(lib):
+    need = lib.jl_chunk_attention_workspace_bytes(10, 2, 8, 2, 200, 256, 128)
+    assert need > 10 * 8 * 256 * 2
+    f = lib.jl_chunk_attention_workspace_bytes
+    assert f(0, 2, 8, 2, 200, 256, 128) == 0 and f(10, 0, 8, 2, 200, 256, 128) == 0
+    assert f(10, 2, 8, 3, 200, 256, 128) == 0 and f(10, 2, 8, 2, 200, 96, 128) == 0
+    assert f(10, 2, 8, 2, 200, 256, 96) == 0 and f(1 << 30, 2, 8, 2, 200, 256, 128) == 0
+    call = caller(lib.jl_chunk_attention_paged, Q=FAKE, dt=jl.JL_BF16, qt=1024, qh=128, N=10,
+                  S=FAKE, **POOLS, table=FAKE, mp=4, lens=FAKE, cu=FAKE, B=2, Hq=8, Hkv=2,
+                  max_len=200, m=256, d=128, scale=0.1, out=FAKE, ws=FAKE, wsb=need, stream=NULL)
+    assert call(N=0) == OK and call(B=0) == OK
+    for bad in (dict(dt=3), dict(N=-1), dict(B=-1), dict(Hq=9), dict(Hkv=0), dict(max_len=0),
+                dict(pages=0), dict(mp=0), dict(P=40), dict(max_len=257), dict(scale=math.nan),
+                dict(scale=math.inf), dict(Q=NULL), dict(S=NULL), dict(S=ODD), dict(codes=NULL),
+                dict(norms=ODD), dict(values=NULL), dict(table=NULL), dict(lens=NULL),
+                dict(cu=NULL), dict(out=NULL), dict(out=ODD), dict(qt=-1),
+                dict(dt=jl.JL_F32, Q=ODD)):
+        assert call(**bad) == INVALID, bad
+    for bad in (dict(m=96), dict(d=96), dict(N=1 << 29), dict(pages=1 << 26, P=64)):
+        assert call(**bad) == UNSUPPORTED, bad
+    for bad in (dict(ws=NULL), dict(ws=ODD), dict(wsb=need - 1)):
+        assert call(**bad) == WORKSPACE, bad
+
+
+def test_accumulate_refused(lib):
+    call = caller(lib.jl_accumulate_attention, s=FAKE, m=FAKE, lens=FAKE, B=2, Hq=8, Hkv=2,
+                  max_len=100, scale=0.1, decay=1.0, out=FAKE, stream=NULL)
+    assert call(B=0) == OK
+    for bad in (dict(B=-1), dict(Hq=7), dict(Hkv=0), dict(max_len=0), dict(scale=math.nan),
+                dict(decay=math.inf), dict(s=NULL), dict(m=NULL), dict(lens=NULL), dict(out=NULL),
+                dict(s=ODD), dict(out=ODD)):
+        assert call(**bad) == INVALID, bad
+    for bad in (dict(Hq=1026, Hkv=2), dict(max_len=1 << 31), dict(B=1 << 23)):
+        assert call(**bad) == UNSUPPORTED, bad
+
+
+def test_evict_refused(lib):
+    call = caller(lib.jl_evict_paged, m=FAKE, lens=FAKE, B=2, Hkv=2, max_len=200, keep=100,
+                  recent=10, sink=4, words=8, cn=1, d=128, **POOLS, src=FAKE, sp=4, dst=FAKE,
+                  dp=2, oi=FAKE, om=FAKE2, ol=FAKE, stream=NULL)
+    assert call(B=0) == OK
+    for bad in (dict(B=-1), dict(Hkv=0), dict(max_len=0), dict(keep=0), dict(recent=-1),
+                dict(sink=-1), dict(recent=97), dict(recent=2 ** 31 - 1, sink=2 ** 31 - 1),
+                dict(sp=0), dict(dp=0), dict(dp=1), dict(sp=3), dict(P=48), dict(codes=NULL),
+                dict(m=NULL), dict(lens=NULL), dict(src=NULL), dict(dst=NULL), dict(oi=NULL),
+                dict(om=NULL), dict(ol=NULL), dict(om=FAKE), dict(om=ODD)):
+        assert call(**bad) == INVALID, bad
+    for bad in (dict(d=80), dict(words=99), dict(cn=4)):
+        assert call(**bad) == UNSUPPORTED, bad
+
+
+# --------------------------------------------------------------------------
+# the wrappers' own checks, on CPU tensors (which they refuse last)
+
+def _cache(B=2, Hkv=2, d=64, W=4, P=32, pages=6):
+    return (torch.zeros(pages, Hkv, P, W, dtype=torch.int32),
+            torch.zeros(pages, Hkv, P, dtype=torch.float16),
+            torch.zeros(pages, Hkv, P, d, dtype=torch.bfloat16),
+            torch.zeros(B, 3, dtype=torch.int32), torch.zeros(B, dtype=torch.int32))
+
+
+def test_wrappers_refuse():
+    cp, npg, vp, table, lens = _cache()
+    cu = torch.zeros(3, dtype=torch.int32)
+    Q = torch.zeros(4, 4, 64, dtype=torch.bfloat16)
+    S = torch.zeros(128, 64, dtype=torch.bfloat16)
+    pos, freq = torch.zeros(4, dtype=torch.int32), torch.zeros(32)
+    bad = (ValueError, TypeError)
+
+    def refused(f, *a, **k):
+        with pytest.raises(bad):
+            f(*a, **k)
+
+    # rotary
+    refused(jl.jl_rotary, Q.half(), pos, freq)
+    refused(jl.jl_rotary, Q[0], pos, freq)
+    refused(jl.jl_rotary, Q, pos.long(), freq)
+    refused(jl.jl_rotary, Q, pos[:3], freq)
+    refused(jl.jl_rotary, Q, pos, freq.double())
+    refused(jl.jl_rotary, Q, pos, freq, K=Q.float())
+    refused(jl.jl_rotary, Q, pos, freq, K=Q[:3])
+    refused(jl.jl_rotary, Q, pos, freq, out_q=Q[:, :2])
+    refused(jl.jl_rotary, Q, pos, freq, out_k=Q)
+    refused(jl.jl_rotary, Q.transpose(1, 2), pos, freq)
+    refused(jl.jl_rotary, Q, pos, freq)                       # not on a GPU
+    # store
+    codes, norms = torch.zeros(5, 2, 4, dtype=torch.int32), torch.zeros(5, 2, dtype=torch.float16)
+    V = torch.zeros(5, 2, 64, dtype=torch.bfloat16)
+    ok = [codes, norms, V, cu, cp, npg, vp, table, lens]
+    for i, t in ((0, codes[:4]), (0, codes.long()), (0, codes[..., :2]), (1, norms.float()),
+                 (1, norms[:, :1]), (2, V.float()), (2, V[..., :32]), (2, V.transpose(1, 2)),
+                 (3, cu[:2]), (3, cu.long()), (4, cp.long()), (4, cp[0]), (5, npg.float()),
+                 (6, vp.half()), (7, table[0]), (7, table.long()), (8, lens.long())):
+        refused(jl.jl_store_paged, *ok[:i], t, *ok[i + 1:])
+    refused(jl.jl_store_paged, *ok)                           # not on a GPU
+    # chunk attention
+    ok = [Q, S, cp, npg, vp, table, lens, cu]
+    for i, t in ((0, Q.half()), (0, Q[0]), (0, Q[..., :32]), (1, S.float()), (1, S[:64]),
+                 (2, cp[..., :2]), (3, torch.zeros(*npg.shape, 2, dtype=torch.float16)),
+                 (4, vp.float()), (5, table.long()), (6, lens.long()), (7, cu[:2])):
+        refused(jl.jl_chunk_attention_paged, *ok[:i], t, *ok[i + 1:], 90)
+    refused(jl.jl_chunk_attention_paged, *ok, 90, out=Q.float())
+    refused(jl.jl_chunk_attention_paged, *ok, 90)             # not on a GPU
+    # weights
+    sc, mass = torch.zeros(2, 4, 50), torch.zeros(2, 2, 50)
+    for a in ((sc.half(), mass, lens), (sc[0], mass, lens), (sc, mass[..., :40], lens),
+              (sc, mass.double(), lens), (sc, mass, lens.long()), (sc, mass, lens[:1])):
+        refused(jl.jl_accumulate_attention, *a, 0.1)
+    refused(jl.jl_accumulate_attention, sc, mass, lens, 0.1, out=sc)
+    refused(jl.jl_accumulate_attention, sc, mass, lens, 0.1)  # not on a GPU
+    # eviction
+    ok = [mass, lens, 20, cp, npg, vp, table, table]
+    for i, t in ((0, mass.double()), (0, mass[:, :1]), (1, lens.long()), (2, 0), (6, table[0]),
+                 (7, table.long())):
+        refused(jl.jl_evict_paged, *ok[:i], t, *ok[i + 1:])
+    refused(jl.jl_evict_paged, *ok, out_index=torch.zeros(2, 2, 19, dtype=torch.int32))
+    refused(jl.jl_evict_paged, *ok)                           # not on a GPU
