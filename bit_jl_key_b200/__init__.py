@@ -786,19 +786,31 @@ def _entered(device, stream):
             yield
 
 
+_HERE_NOW = contextlib.nullcontext()
+
+
 def _on(stream, first, *rest):
     """Context in which a call on these tensors allocates and launches: their
     device, and `stream` if one is given, so that what the call allocates is
     ordered on the stream that uses it."""
-    dev = first.device
-    if not first.is_cuda:
+    dev = first.get_device()
+    if dev < 0:
         raise ValueError("libjlkey works on CUDA tensors only (no CPU fallback)")
     for t in rest:
-        if t is not None and t.device != dev:
-            raise ValueError(f"tensors on different devices: {dev} and {t.device}")
-    if stream is None and dev.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return _entered(dev, stream)
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"tensors on different devices: {first.device} and {t.device}")
+    if stream is None and dev == torch.cuda.current_device():
+        return _HERE_NOW
+    return _entered(first.device, stream)
+
+
+def _now(first):
+    """The current stream of the tensor's device, inside _on."""
+    return torch.cuda.current_stream(first.get_device()).cuda_stream
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
 
 
 def _float_code(t: torch.Tensor, what: str) -> int:
@@ -811,9 +823,9 @@ def _float_code(t: torch.Tensor, what: str) -> int:
 
 def _want(t, what, dtype, shape):
     """A contiguous tensor of one type and shape."""
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:  # (a torch.Size compares as the tuple it is)
         raise ValueError(f"{what} must be {tuple(shape)}, got {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{what} must be contiguous")
@@ -873,10 +885,10 @@ def jl_rotary(Q, positions, inv_freq, K=None, interleaved: bool = False, inverse
             out_k = torch.empty((n, K.shape[1], d), dtype=K.dtype, device=K.device)
         kk, ko = (K, out_k) if K is not None else (Q, out_q)
         _check(load().jl_rotary(
-            _ptr(Q), _ptr(K), dt, n, Hq, kk.shape[1], d, 2 * inv_freq.shape[0], Q.stride(0),
-            Q.stride(1), kk.stride(0), kk.stride(1), _ptr(positions), _ptr(inv_freq),
-            1 if interleaved else 0, 1 if inverse else 0, scale, _ptr(out_q), out_q.stride(0),
-            out_q.stride(1), _ptr(out_k), ko.stride(0), ko.stride(1), _stream(Q, stream)),
+            _at(Q), _at(K), dt, n, Hq, kk.shape[1], d, 2 * inv_freq.shape[0], Q.stride(0),
+            Q.stride(1), kk.stride(0), kk.stride(1), _at(positions), _at(inv_freq),
+            1 if interleaved else 0, 1 if inverse else 0, scale, _at(out_q), out_q.stride(0),
+            out_q.stride(1), _at(out_k), ko.stride(0), ko.stride(1), _now(Q)),
             "jl_rotary")
     return out_q if K is None else (out_q, out_k)
 
@@ -920,10 +932,10 @@ def jl_store_paged(codes, norms, V, cu_seqlens, code_pages, norm_pages, value_pa
     with _on(stream, codes, norms, V, cu_seqlens, code_pages, norm_pages, value_pages,
              block_table, seq_lens):
         _check(load().jl_store_paged(
-            _ptr(codes), _ptr(norms), _ptr(V), V.stride(0), V.stride(1), N, Hkv, words, c, d,
-            _ptr(cu_seqlens), B, _ptr(code_pages), _ptr(norm_pages), _ptr(value_pages),
-            num_pages, P, _ptr(block_table), block_table.shape[1], _ptr(seq_lens),
-            _stream(codes, stream)), "jl_store_paged")
+            _at(codes), _at(norms), _at(V), V.stride(0), V.stride(1), N, Hkv, words, c, d,
+            _at(cu_seqlens), B, _at(code_pages), _at(norm_pages), _at(value_pages),
+            num_pages, P, _at(block_table), block_table.shape[1], _at(seq_lens),
+            _now(codes)), "jl_store_paged")
 
 
 def jl_chunk_attention_workspace_bytes(N, B, Hq, Hkv, max_len, m, d) -> int:
@@ -970,11 +982,11 @@ def jl_chunk_attention_paged(Q, S, sign_pages, norm_pages, value_pages, block_ta
             need = L.jl_chunk_attention_workspace_bytes(N, B, Hq, Hkv, max_len, m, d)
             workspace = torch.empty((max(need, 1),), dtype=torch.uint8, device=Q.device)
         _check(L.jl_chunk_attention_paged(
-            _ptr(Q), qt, Q.stride(0), Q.stride(1), N, _ptr(S), _ptr(sign_pages),
-            _ptr(norm_pages), _ptr(value_pages), num_pages, P, _ptr(block_table),
-            block_table.shape[1], _ptr(seq_lens), _ptr(cu_seqlens), B, Hq, Hkv, max_len, m, d,
-            softmax_scale, _ptr(out), _ptr(workspace),
-            workspace.numel() * workspace.element_size(), _stream(Q, stream)),
+            _at(Q), qt, Q.stride(0), Q.stride(1), N, _at(S), _at(sign_pages),
+            _at(norm_pages), _at(value_pages), num_pages, P, _at(block_table),
+            block_table.shape[1], _at(seq_lens), _at(cu_seqlens), B, Hq, Hkv, max_len, m, d,
+            softmax_scale, _at(out), _at(workspace),
+            workspace.numel() * workspace.element_size(), _now(Q)),
             "jl_chunk_attention_paged")
     return out
 
@@ -997,9 +1009,9 @@ def jl_accumulate_attention(scores, mass, seq_lens, softmax_scale: float, decay:
         out = mass
     _want(out, "out", torch.float32, (B, Hkv, T))
     with _on(stream, scores, mass, seq_lens, out):
-        _check(load().jl_accumulate_attention(_ptr(scores), _ptr(mass), _ptr(seq_lens), B, Hq, Hkv,
-                                              T, softmax_scale, decay, _ptr(out),
-                                              _stream(scores, stream)),
+        _check(load().jl_accumulate_attention(_at(scores), _at(mass), _at(seq_lens), B, Hq, Hkv,
+                                              T, softmax_scale, decay, _at(out),
+                                              _now(scores)),
                "jl_accumulate_attention")
     return out
 
@@ -1038,9 +1050,9 @@ def jl_evict_paged(mass, seq_lens, keep: int, code_pages, norm_pages, value_page
         if out_lens is None:
             out_lens = torch.empty((B,), dtype=torch.int32, device=mass.device)
         _check(load().jl_evict_paged(
-            _ptr(mass), _ptr(seq_lens), B, Hkv, T, keep, recent, sink, words, c, d,
-            _ptr(code_pages), _ptr(norm_pages), _ptr(value_pages), num_pages, P,
-            _ptr(src_table), src_table.shape[1], _ptr(dst_table), dst_table.shape[1],
-            _ptr(out_index), _ptr(out_mass), _ptr(out_lens), _stream(mass, stream)),
+            _at(mass), _at(seq_lens), B, Hkv, T, keep, recent, sink, words, c, d,
+            _at(code_pages), _at(norm_pages), _at(value_pages), num_pages, P,
+            _at(src_table), src_table.shape[1], _at(dst_table), dst_table.shape[1],
+            _at(out_index), _at(out_mass), _at(out_lens), _now(mass)),
             "jl_evict_paged")
     return out_index, out_mass, out_lens

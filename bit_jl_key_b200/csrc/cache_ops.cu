@@ -50,11 +50,62 @@ __device__ __forceinline__ int table_page(const int32_t *table, int max_pages, i
   return page;
 }
 
-// Code words and norms of one key, by the `lanes` lanes of its group.
-__device__ __forceinline__ void copy_code(const Pools &p, int64_t dst, const uint32_t *code,
-                                          const uint16_t *norm, int lane, int lanes) {
-  for (int w = lane; w < p.W; w += lanes) p.codes[dst * p.W + w] = code[w];
-  if (lane < p.c) p.norms[dst * p.c + lane] = norm[lane];
+// Moves the keys of a warp: lane i names one (its row among the sources, its
+// pool row; a negative pool row moves nothing), then d / 8 lanes move a key at
+// a time, 16 bytes of its value each, UNROLL keys' loads in flight.  Where keys
+// come from is `src`: value(row), code(row), norm(row) pointers.
+constexpr int UNROLL = 4;
+template <int D, int UNIT, typename Src>
+__device__ __forceinline__ void move_keys(const Pools &p, const Src &src, int64_t from,
+                                          int64_t to) {
+  constexpr int LANES = D / 8, PER = 32 / LANES;  // lanes of a key, keys side by side
+  const int lane = threadIdx.x & 31, g = lane / LANES, l = lane % LANES;
+  const int units = p.W / UNIT;                   // of UNIT words of a code
+#pragma unroll 1
+  for (int i0 = 0; i0 < LANES; i0 += UNROLL) {
+    int64_t f[UNROLL], t[UNROLL];
+    uint4 v[UNROLL];
+    uint32_t c[UNROLL][UNIT];
+    uint16_t n[UNROLL];
+#pragma unroll
+    for (int i = 0; i < UNROLL; ++i) {
+      const int who = (i0 + i) * PER + g;
+      f[i] = __shfl_sync(~0u, from, who);
+      t[i] = __shfl_sync(~0u, to, who);
+      if (t[i] < 0) continue;
+      v[i] = *reinterpret_cast<const uint4 *>(src.value(f[i]) + 8 * l);
+      if (l < units) {
+        const uint32_t *w = src.code(f[i]) + l * UNIT;
+        if constexpr (UNIT == 4) {
+          const uint4 x = *reinterpret_cast<const uint4 *>(w);
+          c[i][0] = x.x; c[i][1] = x.y; c[i][2] = x.z; c[i][3] = x.w;
+        } else {
+#pragma unroll
+          for (int e = 0; e < UNIT; ++e) c[i][e] = w[e];
+        }
+      }
+      if (l < p.c) n[i] = src.norm(f[i])[l];
+    }
+#pragma unroll
+    for (int i = 0; i < UNROLL; ++i) {
+      if (t[i] < 0) continue;
+      *reinterpret_cast<uint4 *>(p.values + t[i] * D + 8 * l) = v[i];
+      if (l < units) {
+        uint32_t *w = p.codes + t[i] * p.W + l * UNIT;
+        if constexpr (UNIT == 4) {
+          *reinterpret_cast<uint4 *>(w) = make_uint4(c[i][0], c[i][1], c[i][2], c[i][3]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < UNIT; ++e) w[e] = c[i][e];
+        }
+      }
+      // codes of more units than a key has lanes
+      for (int u = l + LANES; u < units; u += LANES)
+        for (int e = 0; e < UNIT; ++e)
+          p.codes[t[i] * p.W + u * UNIT + e] = src.code(f[i])[u * UNIT + e];
+      if (l < p.c) p.norms[t[i] * p.c + l] = n[i];
+    }
+  }
 }
 
 }  // namespace
@@ -64,7 +115,7 @@ __device__ __forceinline__ void copy_code(const Pools &p, int64_t dst, const uin
 
 namespace store {
 
-constexpr int THREADS = 256;
+constexpr int THREADS = 128;
 
 struct Params {
   Pools pool;
@@ -77,31 +128,37 @@ struct Params {
   int64_t N;
 };
 
-// d / 8 lanes move one key: 16 bytes of the value each, then the code words.
-// Consecutive groups take consecutive tokens of one KV head, whose rows are
-// neighbours in a page.
-__global__ void __launch_bounds__(THREADS) store_kernel(const Params p) {
-  const int lanes = p.pool.d / 8;
-  const int per_block = THREADS / lanes;
-  const int g = threadIdx.x / lanes, lane = threadIdx.x - g * lanes;
-  const int h = blockIdx.y;
-  const int64_t r = (int64_t)blockIdx.x * per_block + g;
-  if (r >= p.N) return;
-  // the sequence of row r: the last b with cu[b] <= r
-  if (r < __ldg(p.cu) || r >= __ldg(p.cu + p.B)) return;  // a row of no sequence
-  int lo = 0, hi = p.B;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (__ldg(p.cu + mid) <= r) lo = mid; else hi = mid;
+struct Chunk {
+  const Params &p;
+  int h;
+  __device__ const uint16_t *value(int64_t r) const { return p.V + r * p.v_tok + h * p.v_head; }
+  __device__ const uint32_t *code(int64_t r) const {
+    return p.codes + (r * p.pool.Hkv + h) * p.pool.W;
   }
-  const int64_t pos = (int64_t)__ldg(p.lens + lo) + (r - __ldg(p.cu + lo));
-  const int page = table_page(p.table, p.max_pages, lo, pos, p.pool);
-  if (page < 0) return;
-  const int64_t dst = pool_row(p.pool, page, h, (int)(pos % p.pool.P));
-  const int64_t src = r * p.pool.Hkv + h;
-  const uint4 v = *reinterpret_cast<const uint4 *>(p.V + r * p.v_tok + h * p.v_head + 8 * lane);
-  copy_code(p.pool, dst, p.codes + src * p.pool.W, p.norms + src * p.pool.c, lane, lanes);
-  *reinterpret_cast<uint4 *>(p.pool.values + dst * p.pool.d + 8 * lane) = v;
+  __device__ const uint16_t *norm(int64_t r) const {
+    return p.norms + (r * p.pool.Hkv + h) * p.pool.c;
+  }
+};
+
+// A warp takes 32 consecutive tokens of one KV head, whose rows are neighbours
+// in a page; each lane finds its token's sequence and place.
+template <int D, int UNIT>
+__global__ void __launch_bounds__(THREADS) store_kernel(const Params p) {
+  const int h = blockIdx.y;
+  const int64_t r = (int64_t)blockIdx.x * THREADS + threadIdx.x;
+  int64_t to = -1;
+  // (rows outside every sequence are a batch's padding)
+  if (r < p.N && r >= __ldg(p.cu) && r < __ldg(p.cu + p.B)) {
+    int lo = 0, hi = p.B;  // the last b with cu[b] <= r
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (__ldg(p.cu + mid) <= r) lo = mid; else hi = mid;
+    }
+    const int64_t pos = (int64_t)__ldg(p.lens + lo) + (r - __ldg(p.cu + lo));
+    const int page = table_page(p.table, p.max_pages, lo, pos, p.pool);
+    if (page >= 0) to = pool_row(p.pool, page, h, (int)(pos % p.pool.P));
+  }
+  move_keys<D, UNIT>(p.pool, Chunk{p, h}, r, to);
 }
 
 }  // namespace store
@@ -115,9 +172,12 @@ cudaError_t launch_store_paged(const StoreArgs &a, cudaStream_t stream) {
   p.v_tok = a.v_tok; p.v_head = a.v_head;
   p.cu = a.cu_seqlens; p.table = a.block_table; p.lens = a.seq_lens;
   p.B = a.B; p.max_pages = a.max_pages; p.N = a.N;
-  const int per_block = store::THREADS / (a.d / 8);
-  const dim3 grid((unsigned)((a.N + per_block - 1) / per_block), a.Hkv);
-  store::store_kernel<<<grid, store::THREADS, 0, stream>>>(p);
+  const dim3 grid((unsigned)((a.N + store::THREADS - 1) / store::THREADS), a.Hkv);
+  // 16 bytes of a code at a time where the chunk's codes allow it (a pool's do)
+  const bool four = a.words % 4 == 0 && (reinterpret_cast<uintptr_t>(a.codes) & 15) == 0;
+  auto kernel = a.d == 128 ? (four ? store::store_kernel<128, 4> : store::store_kernel<128, 1>)
+                           : (four ? store::store_kernel<64, 4> : store::store_kernel<64, 1>);
+  kernel<<<grid, store::THREADS, 0, stream>>>(p);
   return cudaGetLastError();
 }
 
@@ -127,6 +187,7 @@ cudaError_t launch_store_paged(const StoreArgs &a, cudaStream_t stream) {
 namespace mass {
 
 constexpr int THREADS = 256, WARPS = THREADS / 32;
+constexpr int LOADS = 4;  // of a thread, in flight
 
 struct Params {
   const float *scores;  // [B][Hq][T]
@@ -135,6 +196,7 @@ struct Params {
   const int32_t *lens;
   int Hq, Hkv, G;
   int64_t T;
+  bool out_vec;          // out is 16-byte aligned
   float k, sign, decay;  // k: |softmax_scale| log2(e); sign: of softmax_scale
   int *err;
 };
@@ -149,6 +211,22 @@ __device__ __forceinline__ MS join(MS a, MS b, float k) {
   const float m = fmaxf(a.m, b.m);
   if (m == -INFINITY) return {m, 0.f};
   return {m, a.l * exp2f((a.m - m) * k) + b.l * exp2f((b.m - m) * k)};
+}
+
+// VEC entries from t on, times `f`; -inf from t1 on.
+template <int VEC>
+__device__ __forceinline__ void load_scores(const float *s, int64_t t, int64_t t1, float f,
+                                            float (&x)[VEC]) {
+  if constexpr (VEC == 4) {
+    if (t < t1) {
+      const float4 v = *reinterpret_cast<const float4 *>(s + t);
+      x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+    }
+  } else {
+    if (t < t1) x[0] = s[t];
+  }
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) x[e] = t + e < t1 ? x[e] * f : -INFINITY;
 }
 
 // One cluster per (sequence, KV head); its blocks split the keys.  Pass one
@@ -178,24 +256,22 @@ __global__ void __launch_bounds__(THREADS) mass_kernel(const Params p) {
   for (int g = 0; g < p.G; ++g) {
     const float *s = s0 + (int64_t)g * p.T;
     MS a{-INFINITY, 0.f};
-    for (int64_t t = t0 + (int64_t)threadIdx.x * VEC; t < t1; t += THREADS * VEC) {
-      float x[VEC];
-      if constexpr (VEC == 4) {
-        const float4 v = *reinterpret_cast<const float4 *>(s + t);
-        x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
-      } else {
-        x[0] = s[t];
-      }
+    constexpr int STEP = THREADS * VEC;
+    for (int64_t t = t0 + (int64_t)threadIdx.x * VEC; t < t1; t += STEP * LOADS) {
+      float x[LOADS][VEC];
       float m = a.m;
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        x[e] = t + e < t1 ? x[e] * p.sign : -INFINITY;
-        m = fmaxf(m, x[e]);
-      }
-      if (m > -INFINITY) {
-        float l = a.l * exp2f((a.m - m) * p.k);
+      for (int q = 0; q < LOADS; ++q) load_scores<VEC>(s, t + q * STEP, t1, p.sign, x[q]);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) l += exp2f((x[e] - m) * p.k);
+      for (int q = 0; q < LOADS; ++q)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) m = fmaxf(m, x[q][e]);
+      if (m > -INFINITY) {
+        float l = a.l * fast_exp2((a.m - m) * p.k);
+#pragma unroll
+        for (int q = 0; q < LOADS; ++q)
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) l += fast_exp2((x[q][e] - m) * p.k);
         a = {m, l};
       }
     }
@@ -219,25 +295,39 @@ __global__ void __launch_bounds__(THREADS) mass_kernel(const Params p) {
   }
   cl.sync();  // also: no block leaves while another reads its states
   const int64_t row = ((int64_t)b * p.Hkv + h) * p.T;
-  for (int64_t t = t0 + (int64_t)threadIdx.x * VEC; t < t1; t += THREADS * VEC) {
-    float w[VEC] = {};
+  for (int64_t t = t0 + (int64_t)threadIdx.x * VEC; t < t1; t += THREADS * VEC * 2) {
+    float w[2][VEC] = {}, old[2][VEC] = {};
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+      if (p.decay != 0.f)
+        load_scores<VEC>(p.mass + row, t + q * THREADS * VEC, t1, p.decay, old[q]);
+#pragma unroll 2
     for (int g = 0; g < p.G; ++g) {
-      const float *s = s0 + (int64_t)g * p.T + t;
       const MS a = all[g];
-      if constexpr (VEC == 4) {
-        const float4 v = *reinterpret_cast<const float4 *>(s);
-        w[0] += a.l == 0.f ? 0.f : exp2f(fmaf(v.x, p.sign, -a.m) * p.k) * a.l;
-        w[1] += a.l == 0.f ? 0.f : exp2f(fmaf(v.y, p.sign, -a.m) * p.k) * a.l;
-        w[2] += a.l == 0.f ? 0.f : exp2f(fmaf(v.z, p.sign, -a.m) * p.k) * a.l;
-        w[3] += a.l == 0.f ? 0.f : exp2f(fmaf(v.w, p.sign, -a.m) * p.k) * a.l;
-      } else {
-        w[0] += a.l == 0.f ? 0.f : exp2f(fmaf(s[0], p.sign, -a.m) * p.k) * a.l;
-      }
+      float x[2][VEC];
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+        load_scores<VEC>(s0 + (int64_t)g * p.T, t + q * THREADS * VEC, t1, p.sign, x[q]);
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+          w[q][e] += a.l == 0.f ? 0.f : fast_exp2((x[q][e] - a.m) * p.k) * a.l;
     }
 #pragma unroll
-    for (int e = 0; e < VEC; ++e)
-      if (t + e < t1)
-        p.out[row + t + e] = p.decay == 0.f ? w[e] : fmaf(p.decay, p.mass[row + t + e], w[e]);
+    for (int q = 0; q < 2; ++q) {
+      const int64_t tq = t + q * THREADS * VEC;
+      float *o = p.out + row + tq;
+      if (VEC == 4 && p.out_vec && tq + VEC <= t1) {
+        *reinterpret_cast<float4 *>(o) =
+            make_float4(old[q][0] + w[q][0], old[q][1 % VEC] + w[q][1 % VEC],
+                        old[q][2 % VEC] + w[q][2 % VEC], old[q][3 % VEC] + w[q][3 % VEC]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+          if (tq + e < t1) o[e] = old[q][e] + w[q][e];
+      }
+    }
   }
 }
 
@@ -266,7 +356,8 @@ cudaError_t launch_accumulate(const AccumulateArgs &a, cudaStream_t stream) {
   mass::Params p{};
   p.scores = a.scores; p.mass = a.mass; p.out = a.out; p.lens = a.seq_lens;
   p.Hq = a.Hq; p.Hkv = a.Hkv; p.G = a.Hq / a.Hkv; p.T = a.max_len;
-  p.k = fabsf(a.softmax_scale) * 1.44269504088896340736f;
+  // (a scale of 0 stays above it, so that -inf times it is -inf)
+  p.k = fmaxf(fabsf(a.softmax_scale) * 1.44269504088896340736f, 1.17549435e-38f);
   p.sign = a.softmax_scale < 0.f ? -1.f : 1.f;
   p.decay = a.decay;
   p.err = device_error_ptr();
@@ -278,7 +369,8 @@ cudaError_t launch_accumulate(const AccumulateArgs &a, cudaStream_t stream) {
   while (cluster < 8 && a.max_len / (2 * cluster) >= 1024) cluster *= 2;
   const size_t smem = (size_t)p.G * (mass::WARPS + 2) * sizeof(mass::MS);  // <= 40 KB: G <= 512
   auto al = [](const void *q) { return (reinterpret_cast<uintptr_t>(q) & 15) == 0; };
-  const bool vec = a.max_len % 4 == 0 && al(a.scores);
+  const bool vec = a.max_len % 4 == 0 && al(a.scores) && (a.decay == 0.f || al(a.mass));
+  p.out_vec = al(a.out);
   return vec ? launch_cluster(mass::mass_kernel<4>, units * cluster, cluster, mass::THREADS, smem,
                               stream, p)
              : launch_cluster(mass::mass_kernel<1>, units * cluster, cluster, mass::THREADS, smem,
@@ -290,9 +382,9 @@ cudaError_t launch_accumulate(const AccumulateArgs &a, cudaStream_t stream) {
 
 namespace evict {
 
-constexpr int THREADS = 1024, WARPS = THREADS / 32;
-constexpr int BINS = 256;
-constexpr int COPY_THREADS = 256;
+constexpr int THREADS = 512, WARPS = THREADS / 32;
+constexpr int BINS = 256, COPIES = 8;  // of a histogram: equal digits in a warp are common
+constexpr int COPY_THREADS = 128;
 
 struct Params {
   Pools pool;
@@ -333,13 +425,13 @@ __device__ __forceinline__ void block_scan(int &a, int &b, int &ta, int &tb, int
   if (lane == 31) sh[warp] = make_int2(ia, ib);
   __syncthreads();
   if (warp == 0) {
-    int2 v = sh[lane];
+    int2 v = lane < WARPS ? sh[lane] : make_int2(0, 0);
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
+    for (int o = 1; o < WARPS; o <<= 1) {
       const int xa = __shfl_up_sync(~0u, v.x, o), xb = __shfl_up_sync(~0u, v.y, o);
       if (lane >= o) { v.x += xa; v.y += xb; }
     }
-    sh[lane] = v;
+    if (lane < WARPS) sh[lane] = v;
   }
   __syncthreads();
   const int2 before = warp ? sh[warp - 1] : make_int2(0, 0), tot = sh[WARPS - 1];
@@ -358,7 +450,7 @@ __device__ __forceinline__ void block_scan(int &a, int &b, int &ta, int &tb, int
 // blocks then numbers the kept keys in order.
 __global__ void __launch_bounds__(THREADS) select_kernel(const Params p) {
   extern __shared__ uint32_t cache[];  // the block's sort keys, if they fit
-  __shared__ uint32_t hist[BINS], sum[BINS];
+  __shared__ uint32_t copies[BINS * COPIES], hist[2][BINS], sum[BINS];
   __shared__ int2 scan[WARPS];
   __shared__ int2 counts;              // of this block: kept for sure, equal to the threshold
   __shared__ uint32_t s_digit;
@@ -396,21 +488,34 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const Params p) {
 
   int need = (int)(keep - p.sink - p.recent);    // of the candidates; may be 0
   uint32_t prefix = 0, mask = 0;                 // threshold digits found so far
+  for (int i = threadIdx.x; i < BINS * COPIES; i += THREADS) copies[i] = 0;
+  __syncthreads();
   for (int shift = 24; shift >= 0; shift -= 8) {
-    for (int i = threadIdx.x; i < BINS; i += THREADS) hist[i] = 0;
-    __syncthreads();
     const int64_t a = t0 > c0 ? t0 : c0, z = t1 < c1 ? t1 : c1;
     for (int64_t t = a + threadIdx.x; t < z; t += THREADS) {
       const uint32_t k = key(t);
-      if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & 255u], 1u);
+      if ((k & mask) == prefix)
+        atomicAdd(&copies[((k >> shift) & 255u) * COPIES + (threadIdx.x & (COPIES - 1))], 1u);
+    }
+    __syncthreads();
+    // two histograms in turn: a block still reading one may not see it change
+    uint32_t *mine = hist[(shift >> 3) & 1];
+    for (int i = threadIdx.x; i < BINS; i += THREADS) {
+      uint32_t v = 0;
+#pragma unroll
+      for (int c = 0; c < COPIES; ++c) {
+        v += copies[i * COPIES + c];
+        copies[i * COPIES + c] = 0;
+      }
+      mine[i] = v;
     }
     cl.sync();
     for (int i = threadIdx.x; i < BINS; i += THREADS) {
       uint32_t v = 0;
-      for (int r = 0; r < nb; ++r) v += cl.map_shared_rank(hist, r)[i];
+      for (int r = 0; r < nb; ++r) v += cl.map_shared_rank(mine, r)[i];
       sum[i] = v;
     }
-    cl.sync();  // every block has read the histograms; sum is complete
+    __syncthreads();
     if (threadIdx.x < 32) {
       // the digit where the count from above first reaches need: lane i
       // holds bins 255 - 8 i downwards
@@ -490,28 +595,31 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const Params p) {
   }
 }
 
-// Moves the kept keys: d / 8 lanes per key, neighbouring groups to
-// neighbouring slots of the new pages.
+struct Cache {
+  const Pools &p;
+  __device__ const uint16_t *value(int64_t r) const { return p.values + r * p.d; }
+  __device__ const uint32_t *code(int64_t r) const { return p.codes + r * p.W; }
+  __device__ const uint16_t *norm(int64_t r) const { return p.norms + r * p.c; }
+};
+
+// Moves the kept keys, 32 neighbouring slots of the new pages to a warp.
+template <int D, int UNIT>
 __global__ void __launch_bounds__(COPY_THREADS) move_kernel(const Params p) {
   griddep_wait();
-  const int lanes = p.pool.d / 8, per_block = COPY_THREADS / lanes;
-  const int g = threadIdx.x / lanes, lane = threadIdx.x - g * lanes;
-  const int tiles = (p.keep + per_block - 1) / per_block;
+  const int tiles = (p.keep + COPY_THREADS - 1) / COPY_THREADS;
   const int unit = blockIdx.x / tiles, b = unit / p.pool.Hkv, h = unit - b * p.pool.Hkv;
-  const int64_t j = (int64_t)(blockIdx.x - unit * tiles) * per_block + g;
-  if (j >= p.keep) return;
-  const int t = p.out_index[(int64_t)unit * p.keep + j];
-  if (t < 0) return;
-  const int sp = table_page(p.src_table, p.src_pages, b, t, p.pool);
-  const int dp = table_page(p.dst_table, p.dst_pages, b, j, p.pool);
-  if (sp < 0 || dp < 0) return;
-  const int64_t src = pool_row(p.pool, sp, h, t % p.pool.P);
-  const int64_t dst = pool_row(p.pool, dp, h, (int)(j % p.pool.P));
-  const uint4 v =
-      *reinterpret_cast<const uint4 *>(p.pool.values + src * p.pool.d + 8 * lane);
-  copy_code(p.pool, dst, p.pool.codes + src * p.pool.W, p.pool.norms + src * p.pool.c, lane,
-            lanes);
-  *reinterpret_cast<uint4 *>(p.pool.values + dst * p.pool.d + 8 * lane) = v;
+  const int64_t j = (int64_t)(blockIdx.x - unit * tiles) * COPY_THREADS + threadIdx.x;
+  int64_t from = 0, to = -1;
+  const int t = j < p.keep ? __ldcg(p.out_index + (int64_t)unit * p.keep + j) : -1;
+  if (t >= 0) {
+    const int sp = table_page(p.src_table, p.src_pages, b, t, p.pool);
+    const int dp = table_page(p.dst_table, p.dst_pages, b, j, p.pool);
+    if (sp >= 0 && dp >= 0) {
+      from = pool_row(p.pool, sp, h, t % p.pool.P);
+      to = pool_row(p.pool, dp, h, (int)(j % p.pool.P));
+    }
+  }
+  move_keys<D, UNIT>(p.pool, Cache{p.pool}, from, to);
 }
 
 }  // namespace evict
@@ -533,16 +641,16 @@ cudaError_t launch_evict_paged(const EvictArgs &a, cudaStream_t stream) {
   p.cached = share * 4 <= 192 * 1024;
   const size_t smem = p.cached ? (size_t)share * 4 : 0;
   cudaError_t e = cudaSuccess;
-  if (smem > 40 * 1024)  // beyond what a block gets without asking
+  if (smem > 32 * 1024)  // with the static part, beyond what a block gets without asking
     e = cudaFuncSetAttribute(evict::select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              192 * 1024);
   if (e != cudaSuccess) return e;
   e = launch_cluster(evict::select_kernel, (int64_t)a.B * a.Hkv * cluster, cluster,
                      evict::THREADS, smem, stream, p);
   if (e != cudaSuccess) return e;
-  const int per_block = evict::COPY_THREADS / (a.d / 8);
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)((a.keep + per_block - 1) / per_block * a.B * a.Hkv));
+  cfg.gridDim = dim3((unsigned)((a.keep + evict::COPY_THREADS - 1) / evict::COPY_THREADS * a.B *
+                                a.Hkv));
   cfg.blockDim = dim3(evict::COPY_THREADS);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -550,7 +658,12 @@ cudaError_t launch_evict_paged(const EvictArgs &a, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, evict::move_kernel, p);
+  const bool four = a.words % 4 == 0;
+  return cudaLaunchKernelEx(
+      &cfg,
+      a.d == 128 ? (four ? evict::move_kernel<128, 4> : evict::move_kernel<128, 1>)
+                 : (four ? evict::move_kernel<64, 4> : evict::move_kernel<64, 1>),
+      p);
 }
 
 }  // namespace jlk

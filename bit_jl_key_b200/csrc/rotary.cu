@@ -115,40 +115,57 @@ __global__ void __launch_bounds__(THREADS) rotary_kernel(const Params p) {
   const int h0 = blockIdx.y * p.heads_per_block;
   const int nh = p.H - h0 < p.heads_per_block ? p.H - h0 : p.heads_per_block;
   const int total = toks * nh * units;
-  for (int i = threadIdx.x; i < total; i += THREADS) {
-    const int row = i / units, u = i - row * units;
-    const int tk = row / nh, h = h0 + row - tk * nh;
-    const bool is_q = h < p.Hq;
-    const Side &s = is_q ? p.q : p.k;
-    const int hh = is_q ? h : h - p.Hq;
-    const T *x = static_cast<const T *>(s.x) + (t0 + tk) * s.x_tok + hh * s.x_head;
-    T *y = static_cast<T *>(s.y) + (t0 + tk) * s.y_tok + hh * s.y_head;
-    if (u >= ru) {
-      const int o = p.rot + (u - ru) * VEC;
-      store<T, VEC>(y + o, load<T, VEC>(x + o));
-    } else if constexpr (INTER) {
-      const int o = u * VEC;
-      Pack<T, VEC> v = load<T, VEC>(x + o);
+  constexpr int AT_ONCE = 4;  // units of a thread whose loads are in flight together
+  for (int i0 = threadIdx.x; i0 < total; i0 += THREADS * AT_ONCE) {
+    Pack<T, VEC> v[AT_ONCE], w[AT_ONCE];
+    T *y[AT_ONCE];
+    int tk[AT_ONCE], u[AT_ONCE];
 #pragma unroll
-      for (int e = 0; e < VEC; e += 2) {
-        const float2 w = cs[tk * half + ((o + e) >> 1)];
-        const float a = to_f32(v.v[e]), b = to_f32(v.v[e + 1]);
-        v.v[e] = from_f32<T>(fmaf(a, w.x, -b * w.y));
-        v.v[e + 1] = from_f32<T>(fmaf(a, w.y, b * w.x));
+    for (int q = 0; q < AT_ONCE; ++q) {
+      const int i = i0 + q * THREADS;
+      if (i >= total) {
+        u[q] = -1;
+        continue;
       }
-      store<T, VEC>(y + o, v);
-    } else {
-      const int o = u * VEC;
-      Pack<T, VEC> v = load<T, VEC>(x + o), w = load<T, VEC>(x + half + o);
+      const int row = i / units;
+      u[q] = i - row * units;
+      tk[q] = row / nh;
+      const int h = h0 + row - tk[q] * nh;
+      const bool is_q = h < p.Hq;
+      const Side &s = is_q ? p.q : p.k;
+      const int hh = is_q ? h : h - p.Hq;
+      const T *x = static_cast<const T *>(s.x) + (t0 + tk[q]) * s.x_tok + hh * s.x_head;
+      y[q] = static_cast<T *>(s.y) + (t0 + tk[q]) * s.y_tok + hh * s.y_head;
+      const int o = u[q] < ru ? u[q] * VEC : p.rot + (u[q] - ru) * VEC;
+      y[q] += o;
+      v[q] = load<T, VEC>(x + o);
+      if (!INTER && u[q] < ru) w[q] = load<T, VEC>(x + half + o);
+    }
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        const float2 r = cs[tk * half + o + e];
-        const float a = to_f32(v.v[e]), b = to_f32(w.v[e]);
-        v.v[e] = from_f32<T>(fmaf(a, r.x, -b * r.y));
-        w.v[e] = from_f32<T>(fmaf(a, r.y, b * r.x));
+    for (int q = 0; q < AT_ONCE; ++q) {
+      if (u[q] < 0) continue;
+      if (u[q] < ru) {
+        const float2 *r = cs + tk[q] * half;
+        if constexpr (INTER) {
+          r += u[q] * (VEC / 2);
+#pragma unroll
+          for (int e = 0; e < VEC; e += 2) {
+            const float a = to_f32(v[q].v[e]), b = to_f32(v[q].v[e + 1]);
+            v[q].v[e] = from_f32<T>(fmaf(a, r[e / 2].x, -b * r[e / 2].y));
+            v[q].v[e + 1] = from_f32<T>(fmaf(a, r[e / 2].y, b * r[e / 2].x));
+          }
+        } else {
+          r += u[q] * VEC;
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) {
+            const float a = to_f32(v[q].v[e]), b = to_f32(w[q].v[e]);
+            v[q].v[e] = from_f32<T>(fmaf(a, r[e].x, -b * r[e].y));
+            w[q].v[e] = from_f32<T>(fmaf(a, r[e].y, b * r[e].x));
+          }
+          store<T, VEC>(y[q] + half, w[q]);
+        }
       }
-      store<T, VEC>(y + o, v);
-      store<T, VEC>(y + half + o, w);
+      store<T, VEC>(y[q], v[q]);
     }
   }
 }
