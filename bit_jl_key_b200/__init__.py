@@ -786,27 +786,26 @@ def _entered(device, stream):
             yield
 
 
-_HERE_NOW = contextlib.nullcontext()
+# The current stream's handle by device index: what torch's own generated code
+# calls, without making a Stream object each time.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
-def _on(stream, first, *rest):
-    """Context in which a call on these tensors allocates and launches: their
-    device, and `stream` if one is given, so that what the call allocates is
+def _on(stream, tensors, run):
+    """run(handle of the stream), allocating and launching on the tensors'
+    device and on `stream` if one is given, so that what the call allocates is
     ordered on the stream that uses it."""
-    dev = first.get_device()
+    dev = tensors[0].get_device()
     if dev < 0:
         raise ValueError("libjlkey works on CUDA tensors only (no CPU fallback)")
-    for t in rest:
+    for t in tensors:
         if t is not None and t.get_device() != dev:
-            raise ValueError(f"tensors on different devices: {first.device} and {t.device}")
+            raise ValueError(f"tensors on different devices: {tensors[0].device} and {t.device}")
     if stream is None and dev == torch.cuda.current_device():
-        return _HERE_NOW
-    return _entered(first.device, stream)
-
-
-def _now(first):
-    """The current stream of the tensor's device, inside _on."""
-    return torch.cuda.current_stream(first.get_device()).cuda_stream
+        return run(_raw_stream(dev))
+    with _entered(tensors[0].device, stream):
+        return run(_raw_stream(dev))
 
 
 def _at(t):
@@ -866,31 +865,44 @@ def jl_rotary(Q, positions, inv_freq, K=None, interleaved: bool = False, inverse
     if Q.dim() != 3:
         raise ValueError("Q must be [n, Hq, d]")
     n, Hq, d = Q.shape
-    if K is not None and (K.dim() != 3 or K.shape[0] != n or K.shape[2] != d or K.dtype != Q.dtype):
-        raise ValueError(f"K must be [{n}, Hkv, {d}] {Q.dtype}, got {tuple(K.shape)} {K.dtype}")
+    q_tok, q_head, one = Q.stride()
     _want(positions, "positions", torch.int32, (n,))
     if inv_freq.dim() != 1:
         raise ValueError("inv_freq must be [r / 2]")
     _want(inv_freq, "inv_freq", torch.float32, inv_freq.shape)
-    for o, x, what in ((out_q, Q, "out_q"), (out_k, K, "out_k")):
-        if o is not None and (x is None or o.shape != x.shape or o.dtype != x.dtype):
-            raise ValueError(f"{what} must have its input's shape and type")
-    for t in (Q, K, out_q, out_k):
-        if t is not None and t.stride(2) != 1:
-            raise ValueError("heads must have unit stride along d")
-    with _on(stream, Q, K, positions, inv_freq, out_q, out_k):
-        if out_q is None:
-            out_q = torch.empty((n, Hq, d), dtype=Q.dtype, device=Q.device)
-        if K is not None and out_k is None:
-            out_k = torch.empty((n, K.shape[1], d), dtype=K.dtype, device=K.device)
-        kk, ko = (K, out_k) if K is not None else (Q, out_q)
-        _check(load().jl_rotary(
-            _at(Q), _at(K), dt, n, Hq, kk.shape[1], d, 2 * inv_freq.shape[0], Q.stride(0),
-            Q.stride(1), kk.stride(0), kk.stride(1), _at(positions), _at(inv_freq),
-            1 if interleaved else 0, 1 if inverse else 0, scale, _at(out_q), out_q.stride(0),
-            out_q.stride(1), _at(out_k), ko.stride(0), ko.stride(1), _now(Q)),
-            "jl_rotary")
-    return out_q if K is None else (out_q, out_k)
+    Hkv = k_tok = k_head = 0
+    if K is not None:
+        if K.dim() != 3 or K.shape[0] != n or K.shape[2] != d or K.dtype is not Q.dtype:
+            raise ValueError(f"K must be [{n}, Hkv, {d}] {Q.dtype}, got {tuple(K.shape)} {K.dtype}")
+        Hkv = K.shape[1]
+        k_tok, k_head, k_one = K.stride()
+        if k_one != 1:
+            one = 0
+    if out_q is not None or out_k is not None:
+        for o, x, what in ((out_q, Q, "out_q"), (out_k, K, "out_k")):
+            if o is not None:
+                if x is None or o.shape != x.shape or o.dtype is not x.dtype:
+                    raise ValueError(f"{what} must have its input's shape and type")
+                if o.stride(2) != 1:
+                    one = 0
+    if one != 1:
+        raise ValueError("heads must have unit stride along d")
+
+    def run(on):
+        oq = Q.new_empty((n, Hq, d)) if out_q is None else out_q
+        ok = K.new_empty((n, Hkv, d)) if K is not None and out_k is None else out_k
+        oq_tok, oq_head, _ = oq.stride()
+        ok_tok, ok_head, _ = (0, 0, 1) if ok is None else ok.stride()
+        st = load().jl_rotary(
+            Q.data_ptr(), _at(K), dt, n, Hq, Hkv, d, 2 * inv_freq.shape[0], q_tok, q_head, k_tok,
+            k_head, positions.data_ptr(), inv_freq.data_ptr(), 1 if interleaved else 0,
+            1 if inverse else 0, scale, oq.data_ptr(), oq_tok, oq_head, _at(ok), ok_tok, ok_head,
+            on)
+        if st:
+            raise JLError(st, "jl_rotary")
+        return oq if K is None else (oq, ok)
+
+    return _on(stream, (Q, K, positions, inv_freq, out_q, out_k), run)
 
 
 def _pools(code_pages, norm_pages, value_pages):
@@ -898,11 +910,12 @@ def _pools(code_pages, norm_pages, value_pages):
     of either kind of code."""
     if code_pages.dim() != 4 or value_pages.dim() != 4:
         raise ValueError("pools must be [pages, Hkv, page_tokens, ...]")
-    num_pages, Hkv, P, words = code_pages.shape
+    num_pages, Hkv, P, words = shape = code_pages.shape
     d = value_pages.shape[3]
     c = 1 if norm_pages.dim() == 3 else 2
-    _want(code_pages, "code pages", torch.int32, code_pages.shape)
-    _want(norm_pages, "norm pages", torch.float16, (num_pages, Hkv, P) + ((2,) if c == 2 else ()))
+    _want(code_pages, "code pages", torch.int32, shape)
+    _want(norm_pages, "norm pages", torch.float16, (num_pages, Hkv, P) if c == 1 else
+          (num_pages, Hkv, P, 2))
     _want(value_pages, "value pages", torch.bfloat16, (num_pages, Hkv, P, d))
     return num_pages, Hkv, P, words, c, d
 
@@ -919,23 +932,32 @@ def jl_store_paged(codes, norms, V, cu_seqlens, code_pages, norm_pages, value_pa
     num_pages, Hkv, P, words, c, d = _pools(code_pages, norm_pages, value_pages)
     N, B = codes.shape[0], seq_lens.shape[0]
     _want(codes, "codes", torch.int32, (N, Hkv, words))
-    _want(norms, "norms", torch.float16, (N, Hkv) + ((2,) if c == 2 else ()))
-    if V.dtype != torch.bfloat16:
+    _want(norms, "norms", torch.float16, (N, Hkv) if c == 1 else (N, Hkv, 2))
+    if V.dtype is not torch.bfloat16:
         raise TypeError(f"V must be bf16, got {V.dtype}")
-    if tuple(V.shape) != (N, Hkv, d) or V.stride(2) != 1:
-        raise ValueError(f"V must be {(N, Hkv, d)} with unit stride along d")
+    if V.shape != (N, Hkv, d):
+        raise ValueError(f"V must be {(N, Hkv, d)}, got {tuple(V.shape)}")
+    v_tok, v_head, one = V.stride()
+    if one != 1:
+        raise ValueError("V must have unit stride along d")
     _want(seq_lens, "seq_lens", torch.int32, (B,))
     _want(cu_seqlens, "cu_seqlens", torch.int32, (B + 1,))
     if block_table.dim() != 2:
         raise ValueError("block_table must be [B, max_pages]")
-    _want(block_table, "block_table", torch.int32, (B, block_table.shape[1]))
-    with _on(stream, codes, norms, V, cu_seqlens, code_pages, norm_pages, value_pages,
-             block_table, seq_lens):
-        _check(load().jl_store_paged(
-            _at(codes), _at(norms), _at(V), V.stride(0), V.stride(1), N, Hkv, words, c, d,
-            _at(cu_seqlens), B, _at(code_pages), _at(norm_pages), _at(value_pages),
-            num_pages, P, _at(block_table), block_table.shape[1], _at(seq_lens),
-            _now(codes)), "jl_store_paged")
+    pages = block_table.shape[1]
+    _want(block_table, "block_table", torch.int32, (B, pages))
+
+    def run(on):
+        st = load().jl_store_paged(
+            codes.data_ptr(), norms.data_ptr(), V.data_ptr(), v_tok, v_head, N, Hkv, words, c, d,
+            cu_seqlens.data_ptr(), B, code_pages.data_ptr(), norm_pages.data_ptr(),
+            value_pages.data_ptr(), num_pages, P, block_table.data_ptr(), pages,
+            seq_lens.data_ptr(), on)
+        if st:
+            raise JLError(st, "jl_store_paged")
+
+    _on(stream, (codes, norms, V, cu_seqlens, code_pages, norm_pages, value_pages, block_table,
+                 seq_lens), run)
 
 
 def jl_chunk_attention_workspace_bytes(N, B, Hq, Hkv, max_len, m, d) -> int:
@@ -962,33 +984,37 @@ def jl_chunk_attention_paged(Q, S, sign_pages, norm_pages, value_pages, block_ta
     if c != 1 or words * 32 != m or dv != d:
         raise ValueError(f"the pools do not hold QJL codes of S {tuple(S.shape)} and values of "
                          f"{d}")
-    if Q.stride(2) != 1:
+    q_tok, q_head, one = Q.stride()
+    if one != 1:
         raise ValueError("queries must have unit stride along d")
-    B = seq_lens.shape[0]
+    B, pages = seq_lens.shape[0], block_table.shape[1]
     _want(S, "S", torch.bfloat16, (m, d))
     _want(seq_lens, "seq_lens", torch.int32, (B,))
     _want(cu_seqlens, "cu_seqlens", torch.int32, (B + 1,))
-    _want(block_table, "block_table", torch.int32, (B, block_table.shape[1]))
+    _want(block_table, "block_table", torch.int32, (B, pages))
     if out is not None:
         _want(out, "out", torch.bfloat16, (N, Hq, d))
     if softmax_scale is None:
         softmax_scale = 1.0 / math.sqrt(d)
-    L = load()
-    with _on(stream, Q, S, sign_pages, norm_pages, value_pages, block_table, seq_lens, cu_seqlens,
-             out, workspace):
-        if out is None:
-            out = torch.empty((N, Hq, d), dtype=torch.bfloat16, device=Q.device)
-        if workspace is None:
+
+    def run(on):
+        L = load()
+        o = Q.new_empty((N, Hq, d), dtype=torch.bfloat16) if out is None else out
+        ws = workspace
+        if ws is None:
             need = L.jl_chunk_attention_workspace_bytes(N, B, Hq, Hkv, max_len, m, d)
-            workspace = torch.empty((max(need, 1),), dtype=torch.uint8, device=Q.device)
-        _check(L.jl_chunk_attention_paged(
-            _at(Q), qt, Q.stride(0), Q.stride(1), N, _at(S), _at(sign_pages),
-            _at(norm_pages), _at(value_pages), num_pages, P, _at(block_table),
-            block_table.shape[1], _at(seq_lens), _at(cu_seqlens), B, Hq, Hkv, max_len, m, d,
-            softmax_scale, _at(out), _at(workspace),
-            workspace.numel() * workspace.element_size(), _now(Q)),
-            "jl_chunk_attention_paged")
-    return out
+            ws = Q.new_empty((max(need, 1),), dtype=torch.uint8)
+        st = L.jl_chunk_attention_paged(
+            Q.data_ptr(), qt, q_tok, q_head, N, S.data_ptr(), sign_pages.data_ptr(),
+            norm_pages.data_ptr(), value_pages.data_ptr(), num_pages, P, block_table.data_ptr(),
+            pages, seq_lens.data_ptr(), cu_seqlens.data_ptr(), B, Hq, Hkv, max_len, m, d,
+            softmax_scale, o.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(), on)
+        if st:
+            raise JLError(st, "jl_chunk_attention_paged")
+        return o
+
+    return _on(stream, (Q, S, sign_pages, norm_pages, value_pages, block_table, seq_lens,
+                        cu_seqlens, out, workspace), run)
 
 
 def jl_accumulate_attention(scores, mass, seq_lens, softmax_scale: float, decay: float = 1.0,
@@ -1007,13 +1033,18 @@ def jl_accumulate_attention(scores, mass, seq_lens, softmax_scale: float, decay:
     _want(seq_lens, "seq_lens", torch.int32, (B,))
     if out is None:
         out = mass
-    _want(out, "out", torch.float32, (B, Hkv, T))
-    with _on(stream, scores, mass, seq_lens, out):
-        _check(load().jl_accumulate_attention(_at(scores), _at(mass), _at(seq_lens), B, Hq, Hkv,
-                                              T, softmax_scale, decay, _at(out),
-                                              _now(scores)),
-               "jl_accumulate_attention")
-    return out
+    else:
+        _want(out, "out", torch.float32, (B, Hkv, T))
+
+    def run(on):
+        st = load().jl_accumulate_attention(scores.data_ptr(), mass.data_ptr(),
+                                            seq_lens.data_ptr(), B, Hq, Hkv, T, softmax_scale,
+                                            decay, out.data_ptr(), on)
+        if st:
+            raise JLError(st, "jl_accumulate_attention")
+        return out
+
+    return _on(stream, (scores, mass, seq_lens, out), run)
 
 
 def jl_evict_paged(mass, seq_lens, keep: int, code_pages, norm_pages, value_pages, src_table,
@@ -1030,29 +1061,32 @@ def jl_evict_paged(mass, seq_lens, keep: int, code_pages, norm_pages, value_page
     if mass.dim() != 3 or src_table.dim() != 2 or dst_table.dim() != 2:
         raise ValueError("mass must be [B, Hkv, max_len] and the tables [B, pages]")
     B, _, T = mass.shape
+    sp, dp = src_table.shape[1], dst_table.shape[1]
     _want(mass, "mass", torch.float32, (B, Hkv, T))
     _want(seq_lens, "seq_lens", torch.int32, (B,))
-    _want(src_table, "src_table", torch.int32, (B, src_table.shape[1]))
-    _want(dst_table, "dst_table", torch.int32, (B, dst_table.shape[1]))
+    _want(src_table, "src_table", torch.int32, (B, sp))
+    _want(dst_table, "dst_table", torch.int32, (B, dp))
     if keep < 1:
         raise ValueError("keep must be at least 1")
-    for t, what, dt, shape in ((out_index, "out_index", torch.int32, (B, Hkv, keep)),
-                               (out_mass, "out_mass", torch.float32, (B, Hkv, keep)),
-                               (out_lens, "out_lens", torch.int32, (B,))):
-        if t is not None:
-            _want(t, what, dt, shape)
-    with _on(stream, mass, seq_lens, code_pages, norm_pages, value_pages, src_table, dst_table,
-             out_index, out_mass, out_lens):
-        if out_index is None:
-            out_index = torch.empty((B, Hkv, keep), dtype=torch.int32, device=mass.device)
-        if out_mass is None:
-            out_mass = torch.empty((B, Hkv, keep), dtype=torch.float32, device=mass.device)
-        if out_lens is None:
-            out_lens = torch.empty((B,), dtype=torch.int32, device=mass.device)
-        _check(load().jl_evict_paged(
-            _at(mass), _at(seq_lens), B, Hkv, T, keep, recent, sink, words, c, d,
-            _at(code_pages), _at(norm_pages), _at(value_pages), num_pages, P,
-            _at(src_table), src_table.shape[1], _at(dst_table), dst_table.shape[1],
-            _at(out_index), _at(out_mass), _at(out_lens), _now(mass)),
-            "jl_evict_paged")
-    return out_index, out_mass, out_lens
+    if out_index is not None:
+        _want(out_index, "out_index", torch.int32, (B, Hkv, keep))
+    if out_mass is not None:
+        _want(out_mass, "out_mass", torch.float32, (B, Hkv, keep))
+    if out_lens is not None:
+        _want(out_lens, "out_lens", torch.int32, (B,))
+
+    def run(on):
+        oi = (seq_lens.new_empty((B, Hkv, keep)) if out_index is None else out_index)
+        om = mass.new_empty((B, Hkv, keep)) if out_mass is None else out_mass
+        ol = seq_lens.new_empty((B,)) if out_lens is None else out_lens
+        st = load().jl_evict_paged(
+            mass.data_ptr(), seq_lens.data_ptr(), B, Hkv, T, keep, recent, sink, words, c, d,
+            code_pages.data_ptr(), norm_pages.data_ptr(), value_pages.data_ptr(), num_pages, P,
+            src_table.data_ptr(), sp, dst_table.data_ptr(), dp, oi.data_ptr(), om.data_ptr(),
+            ol.data_ptr(), on)
+        if st:
+            raise JLError(st, "jl_evict_paged")
+        return oi, om, ol
+
+    return _on(stream, (mass, seq_lens, code_pages, norm_pages, value_pages, src_table, dst_table,
+                        out_index, out_mass, out_lens), run)

@@ -186,7 +186,7 @@ cudaError_t launch_store_paged(const StoreArgs &a, cudaStream_t stream) {
 
 namespace mass {
 
-constexpr int THREADS = 256, WARPS = THREADS / 32;
+constexpr int THREADS = 512, WARPS = THREADS / 32;
 constexpr int LOADS = 4;  // of a thread, in flight
 
 struct Params {
@@ -230,13 +230,14 @@ __device__ __forceinline__ void load_scores(const float *s, int64_t t, int64_t t
 }
 
 // One cluster per (sequence, KV head); its blocks split the keys.  Pass one
-// reads the scores of the group's heads for their softmax states, which the
-// blocks exchange through distributed shared memory; pass two reads the
-// scores again (from L2: a block's share is a few tens of KB) and writes the
-// weights.
+// reads the scores of the group's heads, two at a time so that their loads are
+// in flight together, for the softmax states, which the blocks exchange through
+// distributed shared memory; pass two reads the scores again, from L2, and
+// writes the weights.  (Keeping them in shared memory in between measured no
+// faster: it costs resident blocks.)
 template <int VEC>
 __global__ void __launch_bounds__(THREADS) mass_kernel(const Params p) {
-  extern __shared__ MS ms_smem[];            // [G][WARPS], then [G] of the block
+  extern __shared__ MS ms_smem[];            // [G][WARPS], then [G] of the block, [G] of all
   MS *part = ms_smem, *mine = ms_smem + p.G * WARPS, *all = mine + p.G;
   cg::cluster_group cl = cg::this_cluster();
   const int nb = (int)cl.num_blocks(), rank = (int)cl.block_rank();
@@ -253,61 +254,85 @@ __global__ void __launch_bounds__(THREADS) mass_kernel(const Params p) {
   const int64_t t1 = t0 + share < L ? t0 + share : L;
   const float *s0 = p.scores + ((int64_t)b * p.Hq + (int64_t)h * p.G) * p.T;
 
-  for (int g = 0; g < p.G; ++g) {
+  constexpr int STEP = THREADS * VEC;
+  for (int g = 0; g < p.G; g += 2) {
     const float *s = s0 + (int64_t)g * p.T;
-    MS a{-INFINITY, 0.f};
-    constexpr int STEP = THREADS * VEC;
+    const int64_t more = g + 1 < p.G ? p.T : 0;  // an odd head out is read twice
+    MS a[2] = {{-INFINITY, 0.f}, {-INFINITY, 0.f}};
     for (int64_t t = t0 + (int64_t)threadIdx.x * VEC; t < t1; t += STEP * LOADS) {
-      float x[LOADS][VEC];
-      float m = a.m;
+      float x[2][LOADS][VEC];
 #pragma unroll
-      for (int q = 0; q < LOADS; ++q) load_scores<VEC>(s, t + q * STEP, t1, p.sign, x[q]);
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int q = 0; q < LOADS; ++q)
+        for (int q = 0; q < LOADS; ++q)
+          load_scores<VEC>(s + i * more, t + q * STEP, t1, p.sign, x[i][q]);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) m = fmaxf(m, x[q][e]);
-      if (m > -INFINITY) {
-        float l = a.l * fast_exp2((a.m - m) * p.k);
+      for (int i = 0; i < 2; ++i) {
+        float m = a[i].m;
 #pragma unroll
         for (int q = 0; q < LOADS; ++q)
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) l += fast_exp2((x[q][e] - m) * p.k);
-        a = {m, l};
+          for (int e = 0; e < VEC; ++e) m = fmaxf(m, x[i][q][e]);
+        if (m > -INFINITY) {
+          float l = a[i].l * fast_exp2((a[i].m - m) * p.k);
+#pragma unroll
+          for (int q = 0; q < LOADS; ++q)
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) l += fast_exp2((x[i][q][e] - m) * p.k);
+          a[i] = {m, l};
+        }
       }
     }
 #pragma unroll
-    for (int o = 16; o; o >>= 1)
-      a = join(a, {__shfl_xor_sync(~0u, a.m, o), __shfl_xor_sync(~0u, a.l, o)}, p.k);
-    if (lane == 0) part[g * WARPS + warp] = a;
+    for (int i = 0; i < 2; ++i) {
+#pragma unroll
+      for (int o = 16; o; o >>= 1)
+        a[i] = join(a[i], {__shfl_xor_sync(~0u, a[i].m, o), __shfl_xor_sync(~0u, a[i].l, o)}, p.k);
+      if (lane == 0 && g + i < p.G) part[(g + i) * WARPS + warp] = a[i];
+    }
   }
   __syncthreads();
-  for (int g = threadIdx.x; g < p.G; g += THREADS) {
-    MS a = part[g * WARPS];
-    for (int w = 1; w < WARPS; ++w) a = join(a, part[g * WARPS + w], p.k);
-    mine[g] = a;
+  // a warp joins a head's states, one of each of its lanes
+  for (int g = warp; g < p.G; g += WARPS) {
+    MS a = lane < WARPS ? part[g * WARPS + lane] : MS{-INFINITY, 0.f};
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+      a = join(a, {__shfl_xor_sync(~0u, a.m, o), __shfl_xor_sync(~0u, a.l, o)}, p.k);
+    if (lane == 0) mine[g] = a;
   }
+  // the older weights, on their way while the blocks meet
+  const int64_t row = ((int64_t)b * p.Hkv + h) * p.T;
+  const int64_t first = t0 + (int64_t)threadIdx.x * VEC;
+  float old[2][VEC] = {};
+  auto load_old = [&](int64_t t) {
+    if (p.decay != 0.f) {
+#pragma unroll
+      for (int q = 0; q < 2; ++q) load_scores<VEC>(p.mass + row, t + q * STEP, t1, p.decay, old[q]);
+    }
+  };
+  load_old(first);
   cl.sync();
   for (int g = threadIdx.x; g < p.G; g += THREADS) {
     MS a{-INFINITY, 0.f};
-    for (int r = 0; r < nb; ++r) a = join(a, cl.map_shared_rank(mine, r)[g], p.k);
+    MS x[8];
+#pragma unroll
+    for (int r = 0; r < 8; ++r) x[r] = r < nb ? cl.map_shared_rank(mine, r)[g] : a;
+#pragma unroll
+    for (int r = 0; r < 8; ++r) a = join(a, x[r], p.k);
     // weight = 2^((x - m) k) / l; a head whose keys are all -inf adds nothing
     all[g] = a.m == -INFINITY ? MS{0.f, 0.f} : MS{a.m, 1.f / a.l};
   }
   cl.sync();  // also: no block leaves while another reads its states
-  const int64_t row = ((int64_t)b * p.Hkv + h) * p.T;
-  for (int64_t t = t0 + (int64_t)threadIdx.x * VEC; t < t1; t += THREADS * VEC * 2) {
-    float w[2][VEC] = {}, old[2][VEC] = {};
-#pragma unroll
-    for (int q = 0; q < 2; ++q)
-      if (p.decay != 0.f)
-        load_scores<VEC>(p.mass + row, t + q * THREADS * VEC, t1, p.decay, old[q]);
-#pragma unroll 2
+  for (int64_t t = first; t < t1; t += STEP * 2) {
+    if (t != first) load_old(t);
+    float w[2][VEC] = {};
+#pragma unroll 4
     for (int g = 0; g < p.G; ++g) {
       const MS a = all[g];
       float x[2][VEC];
 #pragma unroll
       for (int q = 0; q < 2; ++q)
-        load_scores<VEC>(s0 + (int64_t)g * p.T, t + q * THREADS * VEC, t1, p.sign, x[q]);
+        load_scores<VEC>(s0 + (int64_t)g * p.T, t + q * STEP, t1, p.sign, x[q]);
 #pragma unroll
       for (int q = 0; q < 2; ++q)
 #pragma unroll
@@ -316,7 +341,7 @@ __global__ void __launch_bounds__(THREADS) mass_kernel(const Params p) {
     }
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
-      const int64_t tq = t + q * THREADS * VEC;
+      const int64_t tq = t + q * STEP;
       float *o = p.out + row + tq;
       if (VEC == 4 && p.out_vec && tq + VEC <= t1) {
         *reinterpret_cast<float4 *>(o) =
@@ -350,6 +375,16 @@ cudaError_t launch_cluster(K kernel, int64_t blocks, int cluster, int threads, s
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
+
+// Blocks per (sequence, KV head): as many as give the device 256 of them, while
+// each keeps `least` keys, up to the portable cluster size.  (64 units of 32768
+// keys: 4 blocks 20.5 and 8 blocks 28 us for the weights, 41 and 55 us for the
+// selection; 32 units of 131072 keys: 29 and 19.5 us for the weights.)
+int cluster_for(int64_t units, int64_t keys, int least) {
+  int c = 1;
+  while (c < 8 && units * c < 256 && keys / (2 * c) >= least) c *= 2;
+  return c;
+}
 }  // namespace
 
 cudaError_t launch_accumulate(const AccumulateArgs &a, cudaStream_t stream) {
@@ -363,18 +398,17 @@ cudaError_t launch_accumulate(const AccumulateArgs &a, cudaStream_t stream) {
   p.err = device_error_ptr();
   if (!p.err) return cudaErrorInvalidSymbol;
   const int64_t units = (int64_t)a.B * a.Hkv;
-  // blocks per (sequence, KV head): as many as keep 1024 keys each, up to the
-  // portable cluster size
-  int cluster = 1;
-  while (cluster < 8 && a.max_len / (2 * cluster) >= 1024) cluster *= 2;
-  const size_t smem = (size_t)p.G * (mass::WARPS + 2) * sizeof(mass::MS);  // <= 40 KB: G <= 512
+  const int cluster = cluster_for(units, a.max_len, 1024);
+  const size_t smem = (size_t)p.G * (mass::WARPS + 2) * sizeof(mass::MS);  // <= 72 KB: G <= 512
   auto al = [](const void *q) { return (reinterpret_cast<uintptr_t>(q) & 15) == 0; };
   const bool vec = a.max_len % 4 == 0 && al(a.scores) && (a.decay == 0.f || al(a.mass));
   p.out_vec = al(a.out);
-  return vec ? launch_cluster(mass::mass_kernel<4>, units * cluster, cluster, mass::THREADS, smem,
-                              stream, p)
-             : launch_cluster(mass::mass_kernel<1>, units * cluster, cluster, mass::THREADS, smem,
-                              stream, p);
+  auto kernel = vec ? mass::mass_kernel<4> : mass::mass_kernel<1>;
+  cudaError_t e = cudaSuccess;
+  if (smem > 48 * 1024)
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 80 * 1024);
+  if (e != cudaSuccess) return e;
+  return launch_cluster(kernel, units * cluster, cluster, mass::THREADS, smem, stream, p);
 }
 
 // ---------------------------------------------------------------------------
@@ -384,7 +418,7 @@ namespace evict {
 
 constexpr int THREADS = 512, WARPS = THREADS / 32;
 constexpr int BINS = 256, COPIES = 8;  // of a histogram: equal digits in a warp are common
-constexpr int COPY_THREADS = 128;
+constexpr int COPY_THREADS = 128, MAX_CLUSTER = 8;
 
 struct Params {
   Pools pool;
@@ -462,18 +496,11 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const Params p) {
   const int64_t keep = L < p.keep ? L : p.keep;
   const float *m = p.mass + (int64_t)unit * p.T;
   int32_t *idx = p.out_index + (int64_t)unit * p.keep;
-  float *om = p.out_mass + (int64_t)unit * p.keep;
   if (rank == 0 && h == 0 && threadIdx.x == 0) p.out_lens[b] = (int32_t)keep;
   const int64_t stride = (int64_t)nb * THREADS, me = (int64_t)rank * THREADS + threadIdx.x;
-  for (int64_t j = keep + me; j < p.keep; j += stride) {
-    idx[j] = -1;
-    om[j] = 0.f;
-  }
+  for (int64_t j = keep + me; j < p.keep; j += stride) idx[j] = -1;
   if (L <= p.keep) {  // every key stays (the same for the whole cluster)
-    for (int64_t j = me; j < L; j += stride) {
-      idx[j] = (int32_t)j;
-      om[j] = m[j];
-    }
+    for (int64_t j = me; j < L; j += stride) idx[j] = (int32_t)j;
     return;
   }
   const int64_t share = (L + nb - 1) / nb;
@@ -481,7 +508,16 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const Params p) {
   const int64_t t1 = t0 + share < L ? t0 + share : L;
   const int64_t c0 = p.sink, c1 = L - p.recent;  // candidates [c0, c1)
   if (p.cached) {
-    for (int64_t t = t0 + threadIdx.x; t < t1; t += THREADS) cache[t - t0] = sort_key(m[t]);
+    constexpr int AT_ONCE = 8;
+    for (int64_t t = t0 + threadIdx.x; t < t1; t += THREADS * AT_ONCE) {
+      float x[AT_ONCE];
+#pragma unroll
+      for (int q = 0; q < AT_ONCE; ++q)
+        if (t + q * THREADS < t1) x[q] = m[t + q * THREADS];
+#pragma unroll
+      for (int q = 0; q < AT_ONCE; ++q)
+        if (t + q * THREADS < t1) cache[t + q * THREADS - t0] = sort_key(x[q]);
+    }
     __syncthreads();
   }
   auto key = [&](int64_t t) { return p.cached ? cache[t - t0] : sort_key(m[t]); };
@@ -512,7 +548,9 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const Params p) {
     cl.sync();
     for (int i = threadIdx.x; i < BINS; i += THREADS) {
       uint32_t v = 0;
-      for (int r = 0; r < nb; ++r) v += cl.map_shared_rank(mine, r)[i];
+#pragma unroll
+      for (int r = 0; r < MAX_CLUSTER; ++r)
+        if (r < nb) v += cl.map_shared_rank(mine, r)[i];
       sum[i] = v;
     }
     __syncthreads();
@@ -549,20 +587,20 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const Params p) {
   }
   const uint32_t tau = prefix;  // keys above it stay, and the first `need` equal to it
 
-  // how many of the block's keys stay for sure, and how many equal tau
+  // A thread owns neighbouring keys, so that one prefix sum over the block and
+  // the cluster numbers its kept keys: those that stay for sure, and of those
+  // equal to tau the first `need`.
   auto classify = [&](int64_t t, int &sure, int &tie) {
-    sure = tie = 0;
-    if (t >= t1) return;
-    if (t < c0 || t >= c1) {
-      sure = 1;
-    } else {
-      const uint32_t k = key(t);
-      sure = k > tau;
-      tie = k == tau;
-    }
+    const uint32_t k = key(t);
+    const bool held = t < c0 || t >= c1;
+    sure = held || k > tau;
+    tie = !held && k == tau;
   };
+  const int64_t own = (share + THREADS - 1) / THREADS;
+  const int64_t a0 = t0 + threadIdx.x * own < t1 ? t0 + threadIdx.x * own : t1;
+  const int64_t a1 = a0 + own < t1 ? a0 + own : t1;
   int na = 0, nt = 0, ta, tb;
-  for (int64_t t = t0 + threadIdx.x; t < t1; t += THREADS) {
+  for (int64_t t = a0; t < a1; ++t) {
     int s, e;
     classify(t, s, e);
     na += s;
@@ -571,28 +609,21 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const Params p) {
   block_scan(na, nt, ta, tb, scan);
   if (threadIdx.x == 0) counts = make_int2(ta, tb);
   cl.sync();
-  int sure0 = 0, tie0 = 0;
-  for (int r = 0; r < rank; ++r) {
-    const int2 v = *cl.map_shared_rank(&counts, r);
-    sure0 += v.x;
-    tie0 += v.y;
-  }
-  cl.sync();  // no block leaves while another reads its counts
-  for (int64_t base = t0; base < t1; base += THREADS) {
-    const int64_t t = base + threadIdx.x;
+#pragma unroll
+  for (int r = 0; r < MAX_CLUSTER; ++r)
+    if (r < rank) {
+      const int2 v = *cl.map_shared_rank(&counts, r);
+      na += v.x;
+      nt += v.y;
+    }
+  for (int64_t t = a0; t < a1; ++t) {
     int s, e;
     classify(t, s, e);
-    int ps = s, pe = e;
-    block_scan(ps, pe, ta, tb, scan);
-    const int ties = tie0 + pe;  // equal keys before this one
-    if (s || (e && ties < need)) {
-      const int64_t j = (int64_t)sure0 + ps + (ties < need ? ties : need);
-      idx[j] = (int32_t)t;
-      om[j] = m[t];
-    }
-    sure0 += ta;
-    tie0 += tb;
+    if (s || (e && nt < need)) idx[na + (nt < need ? nt : need)] = (int32_t)t;
+    na += s;
+    nt += e;
   }
+  cl.sync();  // no block leaves while another reads its counts
 }
 
 struct Cache {
@@ -611,6 +642,8 @@ __global__ void __launch_bounds__(COPY_THREADS) move_kernel(const Params p) {
   const int64_t j = (int64_t)(blockIdx.x - unit * tiles) * COPY_THREADS + threadIdx.x;
   int64_t from = 0, to = -1;
   const int t = j < p.keep ? __ldcg(p.out_index + (int64_t)unit * p.keep + j) : -1;
+  if (j < p.keep)
+    p.out_mass[(int64_t)unit * p.keep + j] = t >= 0 ? p.mass[(int64_t)unit * p.T + t] : 0.f;
   if (t >= 0) {
     const int sp = table_page(p.src_table, p.src_pages, b, t, p.pool);
     const int dp = table_page(p.dst_table, p.dst_pages, b, j, p.pool);
@@ -633,8 +666,7 @@ cudaError_t launch_evict_paged(const EvictArgs &a, cudaStream_t stream) {
   p.src_pages = a.src_max_pages; p.dst_pages = a.dst_max_pages; p.B = a.B; p.T = a.max_len;
   p.keep = a.keep; p.recent = a.recent; p.sink = a.sink;
   p.out_index = a.out_index; p.out_mass = a.out_mass; p.out_lens = a.out_lens;
-  int cluster = 1;
-  while (cluster < 8 && a.max_len / (2 * cluster) >= evict::THREADS) cluster *= 2;
+  const int cluster = cluster_for((int64_t)a.B * a.Hkv, a.max_len, evict::THREADS);
   const int64_t share = (a.max_len + cluster - 1) / cluster;
   // 192 KB of sort keys at most: with the block's static shared memory that
   // stays inside the 227 KB a block may have
