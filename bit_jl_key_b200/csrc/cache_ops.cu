@@ -213,20 +213,21 @@ __device__ __forceinline__ MS join(MS a, MS b, float k) {
   return {m, a.l * exp2f((a.m - m) * k) + b.l * exp2f((b.m - m) * k)};
 }
 
-// VEC entries from t on, times `f`; -inf from t1 on.
+// VEC entries from place i on of the block's n, times `f`; -inf from n on.
 template <int VEC>
-__device__ __forceinline__ void load_scores(const float *s, int64_t t, int64_t t1, float f,
+__device__ __forceinline__ void load_scores(const float *s, int i, int n, float f,
                                             float (&x)[VEC]) {
-  if constexpr (VEC == 4) {
-    if (t < t1) {
-      const float4 v = *reinterpret_cast<const float4 *>(s + t);
-      x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+  if (i + VEC <= n) {
+    if constexpr (VEC == 4) {
+      const float4 v = *reinterpret_cast<const float4 *>(s + i);
+      x[0] = v.x * f; x[1] = v.y * f; x[2] = v.z * f; x[3] = v.w * f;
+    } else {
+      x[0] = s[i] * f;
     }
   } else {
-    if (t < t1) x[0] = s[t];
-  }
 #pragma unroll
-  for (int e = 0; e < VEC; ++e) x[e] = t + e < t1 ? x[e] * f : -INFINITY;
+    for (int e = 0; e < VEC; ++e) x[e] = i + e < n ? s[i + e] * f : -INFINITY;
+  }
 }
 
 // One cluster per (sequence, KV head); its blocks split the keys.  Pass one
@@ -252,20 +253,21 @@ __global__ void __launch_bounds__(THREADS) mass_kernel(const Params p) {
   share = (share + VEC - 1) / VEC * VEC;
   const int64_t t0 = rank * share < L ? rank * share : L;
   const int64_t t1 = t0 + share < L ? t0 + share : L;
-  const float *s0 = p.scores + ((int64_t)b * p.Hq + (int64_t)h * p.G) * p.T;
+  const int n = (int)(t1 - t0);
+  const float *s0 = p.scores + ((int64_t)b * p.Hq + (int64_t)h * p.G) * p.T + t0;
 
   constexpr int STEP = THREADS * VEC;
   for (int g = 0; g < p.G; g += 2) {
     const float *s = s0 + (int64_t)g * p.T;
     const int64_t more = g + 1 < p.G ? p.T : 0;  // an odd head out is read twice
     MS a[2] = {{-INFINITY, 0.f}, {-INFINITY, 0.f}};
-    for (int64_t t = t0 + (int64_t)threadIdx.x * VEC; t < t1; t += STEP * LOADS) {
+    for (int t = threadIdx.x * VEC; t < n; t += STEP * LOADS) {
       float x[2][LOADS][VEC];
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int q = 0; q < LOADS; ++q)
-          load_scores<VEC>(s + i * more, t + q * STEP, t1, p.sign, x[i][q]);
+          load_scores<VEC>(s + i * more, t + q * STEP, n, p.sign, x[i][q]);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         float m = a[i].m;
@@ -301,13 +303,13 @@ __global__ void __launch_bounds__(THREADS) mass_kernel(const Params p) {
     if (lane == 0) mine[g] = a;
   }
   // the older weights, on their way while the blocks meet
-  const int64_t row = ((int64_t)b * p.Hkv + h) * p.T;
-  const int64_t first = t0 + (int64_t)threadIdx.x * VEC;
+  const int64_t row = ((int64_t)b * p.Hkv + h) * p.T + t0;
+  const int first = threadIdx.x * VEC;
   float old[2][VEC] = {};
-  auto load_old = [&](int64_t t) {
+  auto load_old = [&](int t) {
     if (p.decay != 0.f) {
 #pragma unroll
-      for (int q = 0; q < 2; ++q) load_scores<VEC>(p.mass + row, t + q * STEP, t1, p.decay, old[q]);
+      for (int q = 0; q < 2; ++q) load_scores<VEC>(p.mass + row, t + q * STEP, n, p.decay, old[q]);
     }
   };
   load_old(first);
@@ -319,11 +321,11 @@ __global__ void __launch_bounds__(THREADS) mass_kernel(const Params p) {
     for (int r = 0; r < 8; ++r) x[r] = r < nb ? cl.map_shared_rank(mine, r)[g] : a;
 #pragma unroll
     for (int r = 0; r < 8; ++r) a = join(a, x[r], p.k);
-    // weight = 2^((x - m) k) / l; a head whose keys are all -inf adds nothing
-    all[g] = a.m == -INFINITY ? MS{0.f, 0.f} : MS{a.m, 1.f / a.l};
+    // weight = 2^((x - m) k - log2 l); a head whose keys are all -inf adds nothing
+    all[g] = a.m == -INFINITY ? MS{0.f, -INFINITY} : MS{a.m, -log2f(a.l)};
   }
   cl.sync();  // also: no block leaves while another reads its states
-  for (int64_t t = first; t < t1; t += STEP * 2) {
+  for (int t = first; t < n; t += STEP * 2) {
     if (t != first) load_old(t);
     float w[2][VEC] = {};
 #pragma unroll 4
@@ -332,25 +334,24 @@ __global__ void __launch_bounds__(THREADS) mass_kernel(const Params p) {
       float x[2][VEC];
 #pragma unroll
       for (int q = 0; q < 2; ++q)
-        load_scores<VEC>(s0 + (int64_t)g * p.T, t + q * STEP, t1, p.sign, x[q]);
+        load_scores<VEC>(s0 + (int64_t)g * p.T, t + q * STEP, n, p.sign, x[q]);
 #pragma unroll
       for (int q = 0; q < 2; ++q)
 #pragma unroll
-        for (int e = 0; e < VEC; ++e)
-          w[q][e] += a.l == 0.f ? 0.f : fast_exp2((x[q][e] - a.m) * p.k) * a.l;
+        for (int e = 0; e < VEC; ++e) w[q][e] += fast_exp2(fmaf(x[q][e] - a.m, p.k, a.l));
     }
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
-      const int64_t tq = t + q * STEP;
+      const int tq = t + q * STEP;
       float *o = p.out + row + tq;
-      if (VEC == 4 && p.out_vec && tq + VEC <= t1) {
+      if (VEC == 4 && p.out_vec && tq + VEC <= n) {
         *reinterpret_cast<float4 *>(o) =
             make_float4(old[q][0] + w[q][0], old[q][1 % VEC] + w[q][1 % VEC],
                         old[q][2 % VEC] + w[q][2 % VEC], old[q][3 % VEC] + w[q][3 % VEC]);
       } else {
 #pragma unroll
         for (int e = 0; e < VEC; ++e)
-          if (tq + e < t1) o[e] = old[q][e] + w[q][e];
+          if (tq + e < n) o[e] = old[q][e] + w[q][e];
       }
     }
   }
