@@ -21,7 +21,9 @@ namespace jlk {
 namespace chunk {
 
 constexpr int BN = 128;            // keys of a tile
-constexpr float RENEW = 8.f;       // log2 growth of a row's maximum that renews it
+// log2 of the largest weight before a row's maximum is renewed: far below what
+// a weight, a sum of them or a value times them can be, and seldom reached
+constexpr float RENEW = 16.f;
 constexpr float MIN_SCALE = 1.17549435e-38f;  // of a row: -inf times it stays -inf
 constexpr int PREP_THREADS = 256;
 constexpr int SM_COUNT = 148;      // bounds the workspace per shape

@@ -19,7 +19,7 @@
 // random in sign).
 //
 // A softmax thread holds one key and all NR rows.  The rows' maxima are shared
-// through shared memory and renewed only when a weight would pass 2^8 (one vote
+// through shared memory and renewed only when a weight would pass 2^16 (one vote
 // of the 128 threads per tile), so the common tile has no reduction at all;
 // the sums stay with the threads until the row tile ends.
 //

@@ -29,8 +29,9 @@
 // scores may be issued over weights that an earlier product reads.
 // P is rounded to bf16 (half a step, 2^-8 of each weight, against values that
 // are bf16 themselves); its sum is taken before the rounding, in fp32.
-// The maximum is renewed only when a row's grows by more than 2^8: until then
-// weights up to 2^8 are as exact, and the accumulator need not be rescaled.
+// A row's weights refer to the maximum of the first keys it met until one would
+// pass 2^RENEW: floating point keeps them as exact, no tile waits for its own
+// maximum, and the accumulator need hardly ever be rescaled.
 //
 // Warps: 0-3 and 4-7 softmax and output of a half (one row per thread), 8 MMA
 // issue and tensor memory, 9 copies (a granule of V lies in one page).
@@ -162,12 +163,6 @@ __device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
   asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;\n" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
-
 // 2^x of a pair on the multiply-add pipe, for the share of the weights that
 // the exponential unit has no time for.  x = n + f with n the nearest whole
 // number, 2^f by the cubic with the least largest relative error on
@@ -188,67 +183,60 @@ __device__ __forceinline__ float2 exp2_poly(f32x2 x) {
                      __uint_as_float(__float_as_uint(k.y) * 0x800000u + __float_as_uint(v.y)));
 }
 
-// Largest of the 128 scores of a row; those from column lim on do not count.
-// A NaN among the others is the result.
+// The exponents x rs + mm of 64 scores from column 64 * half on, -inf from
+// column lim on; returns the largest.
 template <bool MASK>
-__device__ __forceinline__ float row_max(uint32_t tS, int lim) {
-  uint32_t v[4][32];
-#pragma unroll
-  for (int c = 0; c < 4; ++c) ld32(tS + 32 * c, v[c]);
-#pragma unroll
-  for (int c = 0; c < 4; ++c) ld_wait(v[c]);
-  float t[4];
-#pragma unroll
-  for (int q = 0; q < 4; ++q) t[q] = -INFINITY;
-#pragma unroll
-  for (int c = 0; c < 4; ++c)
-#pragma unroll
-    for (int j = 0; j < 32; j += 8)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        float x = __uint_as_float(v[c][j + q]), y = __uint_as_float(v[c][j + 4 + q]);
-        if (MASK && 32 * c + j + q >= lim) x = -INFINITY;
-        if (MASK && 32 * c + j + 4 + q >= lim) y = -INFINITY;
-        t[q] = max_nan(t[q], max_nan(x, y));
-      }
-  return max_nan(max_nan(t[0], t[1]), max_nan(t[2], t[3]));
-}
-
-// Weights 2^(x rs + mm) of 64 scores from column 64 * half on, as bf16 over the
-// scores' columns 32 * half ..; their sums added to `sum`.
-template <bool MASK>
-__device__ __forceinline__ void row_weights(uint32_t tS, int half, int lim, float rs, float mm,
-                                            f32x2 &sum) {
+__device__ __forceinline__ float row_exponents(uint32_t tS, int half, int lim, float rs, float mm,
+                                               f32x2 (&x)[32]) {
   uint32_t v[2][32];
 #pragma unroll
   for (int c = 0; c < 2; ++c) ld32(tS + 64 * half + 32 * c, v[c]);
 #pragma unroll
   for (int c = 0; c < 2; ++c) ld_wait(v[c]);
   const f32x2 rs2 = pair(rs, rs), mm2 = pair(mm, mm);
+  float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-  for (int c = 0; c < 2; ++c) {
-    uint32_t w[16];
+  for (int c = 0; c < 2; ++c)
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
       float a = __uint_as_float(v[c][2 * e]), b = __uint_as_float(v[c][2 * e + 1]);
       const int col = 64 * half + 32 * c + 2 * e;
       if (MASK && col >= lim) a = -INFINITY;
       if (MASK && col + 1 >= lim) b = -INFINITY;
-      const f32x2 x = fma2(pair(a, b), rs2, mm2);
+      const f32x2 y = fma2(pair(a, b), rs2, mm2);
+      const float2 z = halves_of(y);
+      t[e & 3] = fmaxf(t[e & 3], fmaxf(z.x, z.y));
+      x[16 * c + e] = y;
+    }
+  return fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
+}
+
+// Weights 2^x of those 64, as bf16 over the scores' columns 32 * half ..;
+// returns their sum.
+template <bool MASK>
+__device__ __forceinline__ float row_weights(uint32_t tS, int half, const f32x2 (&x)[32]) {
+  f32x2 sum[2] = {0, 0};
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    uint32_t w[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
       float2 y;
       if (!MASK && e % POLY_EVERY == POLY_EVERY - 1) {
-        y = exp2_poly(x);
+        y = exp2_poly(x[16 * c + e]);
       } else {
-        y = halves_of(x);
+        y = halves_of(x[16 * c + e]);
         y.x = fast_exp2(y.x);
         y.y = fast_exp2(y.y);
       }
-      sum = add2(sum, pair(y.x, y.y));
+      sum[e & 1] = add2(sum[e & 1], pair(y.x, y.y));
       w[e] = pack_bf16x2(y.x, y.y);
     }
     st16(tS + 32 * half + 16 * c, w);
   }
   st_wait();
+  const float2 s = halves_of(add2(sum[0], sum[1]));
+  return s.x + s.y;
 }
 
 template <int D>
@@ -270,7 +258,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   };
   const uint32_t kfull = bars(C::SK), kempty = bars(C::SK), vfull = bars(C::SV),
                  vempty = bars(C::SV), sfull = bars(HALVES), pready = bars(2 * HALVES),
-                 ofree = bars(HALVES), pvdone = bars(2 * HALVES), ufull = bars(1),
+                 ofree = bars(HALVES), pvdone = bars(2 * HALVES), pvhalf = bars(HALVES), ufull = bars(1),
                  uempty = bars(1), fin = bars(1);
   // two barriers a half for the value products in turn: whoever waits for a
   // tile's knows that the tile two before it is done, not the one before
@@ -296,6 +284,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       mbar_init(pready + 16 * a + 8, SM_WARPS);
       mbar_init(ofree + 8 * a, SM_WARPS);
       mbar_init(pvdone + 16 * a, 1);
+      mbar_init(pvhalf + 8 * a, 1);
       mbar_init(pvdone + 16 * a + 8, 1);
     }
     mbar_init(ufull, 1);
@@ -342,7 +331,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int seen = live ? min(s.L, max(0, s.L - s.n + tok + 1)) : 0;
       const int64_t urow = ((int64_t)s.h * p.N + s.start) * p.G + row;
       const float rs = live ? __ldcg(p.w.rs + urow) : 0.f;
-      float m = -INFINITY, l = 0.f;
+      float m = 0.f, l = 0.f;
       for (int k = 0; k < s.nk; ++k, ++it, ++vt) {
         if (!wait_phase(sfull + 8 * a, it & 1u, abort_flag, p.err)) {
           ok = false;
@@ -371,56 +360,51 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         const int lim = seen - t0;  // columns the row sees
         const bool all = __all_sync(~0u, lim >= BN);
-        float mm = 0.f;
-        f32x2 sum = 0;
-        if (any_live) {
-          const float top = all ? row_max<false>(tS, BN) : row_max<true>(tS, lim);
-          const float cand = top == -INFINITY ? -INFINITY : top * rs;
-          if (k == 0) {
-            m = cand;
-          } else {
-            const bool grow = !(cand <= m + RENEW);  // also the first NaN of a row
-            if (__any_sync(~0u, grow)) {
-              // earlier products must have landed before the accumulator is scaled
-              if (!wait_phase(pv_bar(a, it - 1), pv_phase(it - 1), abort_flag, p.err)) ok = false;
-              __syncwarp();
-              fence_after();
-              const float mn = grow ? cand : m;
-              const float f = m == mn ? 1.f : fast_exp2(m - mn);
-              m = mn;
-              l *= f;
+        // 64 keys at a time, so that the first ones' product starts while the
+        // others' weights are computed
 #pragma unroll 1
-              for (int c = 0; c < D; c += 16) {
-                uint32_t o[16];
-                ld16(tO + c, o);
-#pragma unroll
-                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                st16(tO + c, o);
-              }
-              if (!__all_sync(~0u, ok)) {
-                ok = false;
-                break;
-              }
-            }
-          }
-          mm = m == -INFINITY ? 0.f : -m;
-        }
-        // the weights of 64 keys at a time, so that the first ones' product
-        // starts while the others are computed
-#pragma unroll
         for (int half = 0; half < 2; ++half) {
           if (any_live) {
-            if (all)
-              row_weights<false>(tS, half, BN, rs, mm, sum);
-            else
-              row_weights<true>(tS, half, lim, rs, mm, sum);
+            f32x2 x[32];
+            const float top = all ? row_exponents<false>(tS, half, BN, rs, -m, x)
+                                  : row_exponents<true>(tS, half, lim, rs, -m, x);
+            const bool begin = k == 0 && half == 0;
+            if (begin || __any_sync(~0u, top > RENEW)) {
+              // a new maximum; a row without a key so far refers to 0
+              const float up = begin ? (top == -INFINITY ? 0.f : top) : top > RENEW ? top : 0.f;
+              m += up;
+#pragma unroll
+              for (int e = 0; e < 32; ++e) x[e] = add2(x[e], pair(-up, -up));
+              if (!begin) {
+                // earlier products must have landed before the accumulator is scaled
+                if (!(half ? wait_phase(pvhalf + 8 * a, it & 1u, abort_flag, p.err)
+                           : wait_phase(pv_bar(a, it - 1), pv_phase(it - 1), abort_flag, p.err)))
+                  ok = false;
+                __syncwarp();
+                fence_after();
+                const float f = up == 0.f ? 1.f : fast_exp2(-up);
+                l *= f;
+#pragma unroll 1
+                for (int c = 0; c < D; c += 16) {
+                  uint32_t o[16];
+                  ld16(tO + c, o);
+#pragma unroll
+                  for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                  st16(tO + c, o);
+                }
+                if (!__all_sync(~0u, ok)) {
+                  ok = false;
+                  break;
+                }
+              }
+            }
+            l += all ? row_weights<false>(tS, half, x) : row_weights<true>(tS, half, x);
           }
           fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(pready + 16 * a + 8 * half);
         }
-        const float2 ss = halves_of(sum);
-        l += ss.x + ss.y;
+        if (!ok) break;
       }
       if (!ok) break;
       // output: the row itself, or its state where the row tile is split
@@ -522,8 +506,11 @@ __global__ void __launch_bounds__(THREADS, 1)
     bool ok = true;
     uint32_t kt = 0, sg = 0;            // key tiles and segments of the block
     uint32_t it0 = 0, it1 = 0, sg1 = 0; // key tiles of each half, segments of half 1
+    auto wait_copy = [&](uint32_t bar, uint32_t ph) {
+      return (bool)__all_sync(~0u, wait_phase(bar, ph, abort_flag, p.err));
+    };
     auto wait = [&](uint32_t bar, uint32_t ph) {
-      const bool w = __all_sync(~0u, wait_phase(bar, ph, abort_flag, p.err));
+      const bool w = wait_copy(bar, ph);
       fence_after();
       return w;
     };
@@ -543,8 +530,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     for (; ok && more; more = seg_next(s, p)) {
       if (s.nk == 0) continue;
       const int na = halves();
-      if (!(ok = wait(ufull, sg & 1u))) break;
-      if (!(ok = wait(kfull + 8 * (kt % C::SK), (kt / C::SK) & 1u))) break;
+      if (!(ok = wait_copy(ufull, sg & 1u))) break;
+      if (!(ok = wait_copy(kfull + 8 * (kt % C::SK), (kt / C::SK) & 1u))) break;
       for (int a = 0; a < na; ++a) scores(a, kt);
       if (elect_one()) commit(kempty + 8 * (kt % C::SK));
       __syncwarp();
@@ -552,7 +539,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         const uint32_t vs = kt % C::SV, nx = (kt + 1) % C::SK;
         for (int a = 0; a < na; ++a) {
           const uint32_t it = a ? it1 : it0, sa = a ? sg1 : sg;
-          if (a == 0 && !(ok = wait(vfull + 8 * vs, (kt / C::SV) & 1u))) break;
+          if (a == 0 && !(ok = wait_copy(vfull + 8 * vs, (kt / C::SV) & 1u))) break;
           if (k == 0 && sa > 0 && !(ok = wait(ofree + 8 * a, (sa - 1) & 1u))) break;
           const uint64_t dv = dv0 + (uint64_t)((vs * C::TILE) >> 4);
           for (int half = 0; half < 2; ++half) {  // of the tile's keys
@@ -568,13 +555,15 @@ __global__ void __launch_bounds__(THREADS, 1)
               if (half) {
                 commit(pv_bar(a, it));
                 if (a == na - 1) commit(vempty + 8 * vs);
+              } else {
+                commit(pvhalf + 8 * a);
               }
             }
             __syncwarp();
           }
           if (!ok) break;
           if (k + 1 < s.nk) {
-            if (a == 0 && !(ok = wait(kfull + 8 * nx, ((kt + 1) / C::SK) & 1u))) break;
+            if (a == 0 && !(ok = wait_copy(kfull + 8 * nx, ((kt + 1) / C::SK) & 1u))) break;
             scores(a, kt + 1);
             if (a == na - 1) {
               if (elect_one()) commit(kempty + 8 * nx);
