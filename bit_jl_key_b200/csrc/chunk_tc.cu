@@ -33,8 +33,9 @@
 // pass 2^RENEW: floating point keeps them as exact, no tile waits for its own
 // maximum, and the accumulator need hardly ever be rescaled.
 //
-// Warps: 0-3 and 4-7 softmax and output of a half (one row per thread), 8 MMA
-// issue and tensor memory, 9 copies (a granule of V lies in one page).
+// Warps: 0-7 and 8-15 softmax and output of a half, two threads per row (64 of
+// a tile's keys each: a thread alone is held up by its own latencies), 16 MMA
+// issue and tensor memory, 17 copies (a granule of V lies in one page).
 // Every wait is bounded; one that runs out records DERR_TC_WAIT_TIMEOUT.
 #include "chunk.cuh"
 #include "jl_tc.cuh"
@@ -48,7 +49,7 @@ namespace chunk {
 namespace {
 
 constexpr int BM = 128, HALVES = 2, ROWS = BM * HALVES;
-constexpr int SM_WARPS = 4;                       // of a half
+constexpr int SM_WARPS = 8;                       // of a half: four for each 64 of the keys
 constexpr int MMA_WARP = SM_WARPS * HALVES, LOAD_WARP = MMA_WARP + 1;
 constexpr int THREADS = (LOAD_WARP + 1) * 32;
 constexpr int POLY_EVERY = 4;                     // one pair of weights in so many on the FMA pipe
@@ -119,7 +120,8 @@ struct Cfg {
   static constexpr int SK = 2, SV = 3;             // K and V stages
   static constexpr int OFF_K = HALVES * TILE;
   static constexpr int OFF_V = OFF_K + SK * TILE;
-  static constexpr int OFF_BAR = OFF_V + SV * TILE;
+  static constexpr int OFF_ROW = OFF_V + SV * TILE;  // a word per row
+  static constexpr int OFF_BAR = OFF_ROW + HALVES * BM * 4;
   static constexpr int SMEM = OFF_BAR + 512 + 1024;  // + align slack
   // tensor memory columns: the halves' scores (their weights over them), then
   // their accumulators
@@ -183,56 +185,57 @@ __device__ __forceinline__ float2 exp2_poly(f32x2 x) {
                      __uint_as_float(__float_as_uint(k.y) * 0x800000u + __float_as_uint(v.y)));
 }
 
-// The exponents x rs + mm of 64 scores from column 64 * half on, -inf from
-// column lim on; returns the largest.
+// Largest of the 64 scores at tS; those from column lim on do not count.
 template <bool MASK>
-__device__ __forceinline__ float row_exponents(uint32_t tS, int half, int lim, float rs, float mm,
-                                               f32x2 (&x)[32]) {
+__device__ __forceinline__ float row_max(uint32_t tS, int lim) {
   uint32_t v[2][32];
 #pragma unroll
-  for (int c = 0; c < 2; ++c) ld32(tS + 64 * half + 32 * c, v[c]);
+  for (int c = 0; c < 2; ++c) ld32(tS + 32 * c, v[c]);
 #pragma unroll
   for (int c = 0; c < 2; ++c) ld_wait(v[c]);
-  const f32x2 rs2 = pair(rs, rs), mm2 = pair(mm, mm);
   float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
   for (int c = 0; c < 2; ++c)
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      float a = __uint_as_float(v[c][2 * e]), b = __uint_as_float(v[c][2 * e + 1]);
-      const int col = 64 * half + 32 * c + 2 * e;
-      if (MASK && col >= lim) a = -INFINITY;
-      if (MASK && col + 1 >= lim) b = -INFINITY;
-      const f32x2 y = fma2(pair(a, b), rs2, mm2);
-      const float2 z = halves_of(y);
-      t[e & 3] = fmaxf(t[e & 3], fmaxf(z.x, z.y));
-      x[16 * c + e] = y;
+    for (int e = 0; e < 32; e += 2) {
+      float x = __uint_as_float(v[c][e]), y = __uint_as_float(v[c][e + 1]);
+      if (MASK && 32 * c + e >= lim) x = -INFINITY;
+      if (MASK && 32 * c + e + 1 >= lim) y = -INFINITY;
+      t[(e >> 1) & 3] = fmaxf(t[(e >> 1) & 3], fmaxf(x, y));
     }
   return fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
 }
 
-// Weights 2^x of those 64, as bf16 over the scores' columns 32 * half ..;
-// returns their sum.
+// Weights 2^(score rs + mm) of those 64, as bf16 over the first half of their
+// columns, 32 scores at a time (each group's weights go where scores that have
+// been read lay); returns their sum.
 template <bool MASK>
-__device__ __forceinline__ float row_weights(uint32_t tS, int half, const f32x2 (&x)[32]) {
+__device__ __forceinline__ float row_weights(uint32_t tS, int lim, float rs, float mm) {
+  const f32x2 rs2 = pair(rs, rs), mm2 = pair(mm, mm);
   f32x2 sum[2] = {0, 0};
-#pragma unroll
+#pragma unroll 1
   for (int c = 0; c < 2; ++c) {
-    uint32_t w[16];
+    uint32_t v[32], w[16];
+    ld32(tS + 32 * c, v);
+    ld_wait(v);
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
+      float a = __uint_as_float(v[2 * e]), b = __uint_as_float(v[2 * e + 1]);
+      if (MASK && 32 * c + 2 * e >= lim) a = -INFINITY;
+      if (MASK && 32 * c + 2 * e + 1 >= lim) b = -INFINITY;
+      const f32x2 x = fma2(pair(a, b), rs2, mm2);
       float2 y;
       if (!MASK && e % POLY_EVERY == POLY_EVERY - 1) {
-        y = exp2_poly(x[16 * c + e]);
+        y = exp2_poly(x);
       } else {
-        y = halves_of(x[16 * c + e]);
+        y = halves_of(x);
         y.x = fast_exp2(y.x);
         y.y = fast_exp2(y.y);
       }
       sum[e & 1] = add2(sum[e & 1], pair(y.x, y.y));
       w[e] = pack_bf16x2(y.x, y.y);
     }
-    st16(tS + 32 * half + 16 * c, w);
+    st16(tS + 16 * c, w);
   }
   st_wait();
   const float2 s = halves_of(add2(sum[0], sum[1]));
@@ -258,7 +261,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   };
   const uint32_t kfull = bars(C::SK), kempty = bars(C::SK), vfull = bars(C::SV),
                  vempty = bars(C::SV), sfull = bars(HALVES), pready = bars(2 * HALVES),
-                 ofree = bars(HALVES), pvdone = bars(2 * HALVES), pvhalf = bars(HALVES), ufull = bars(1),
+                 ofree = bars(HALVES), pvdone = bars(2 * HALVES), ufull = bars(1),
                  uempty = bars(1), fin = bars(1);
   // two barriers a half for the value products in turn: whoever waits for a
   // tile's knows that the tile two before it is done, not the one before
@@ -280,11 +283,10 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     for (int a = 0; a < HALVES; ++a) {
       mbar_init(sfull + 8 * a, 1);
-      mbar_init(pready + 16 * a, SM_WARPS);
-      mbar_init(pready + 16 * a + 8, SM_WARPS);
+      mbar_init(pready + 16 * a, SM_WARPS / 2);
+      mbar_init(pready + 16 * a + 8, SM_WARPS / 2);
       mbar_init(ofree + 8 * a, SM_WARPS);
       mbar_init(pvdone + 16 * a, 1);
-      mbar_init(pvhalf + 8 * a, 1);
       mbar_init(pvdone + 16 * a + 8, 1);
     }
     mbar_init(ufull, 1);
@@ -312,45 +314,57 @@ __global__ void __launch_bounds__(THREADS, 1)
   auto halves = [&]() { return (int64_t)s.n * p.G - (int64_t)s.mt * ROWS > BM ? 2 : 1; };
 
   if (warp < MMA_WARP) {
-    // ---------------- softmax: thread = row of half a
-    const int a = warp / SM_WARPS;
-    const int r = threadIdx.x & (BM - 1);                   // row of the half
+    // ---------------- softmax: thread = row r of half a, keys 64 c .. of a tile
+    const int a = warp / SM_WARPS, c = (warp >> 2) & 1;
+    const int r = 32 * (warp & 3) + lane;
     const uint32_t trow = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     const uint32_t tS = trow + (uint32_t)(a * BN), tO = trow + (uint32_t)(C::COL_O + a * D);
+    // The two warps of the same rows meet at a barrier of their own once a
+    // tile.  A wait that ran out leaves by way of these meetings: nobody waits
+    // at a barrier for a warp that has gone.
+    const int pair_bar = 1 + 4 * a + (warp & 3), half_bar = 9 + a;
+    auto any = [](int bar, int threads, bool x) {
+      uint32_t y;
+      asm volatile(
+          "{\n .reg .pred p, q;\n setp.ne.u32 p, %3, 0;\n"
+          " bar.red.or.pred q, %1, %2, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+          : "=r"(y)
+          : "r"(bar), "r"(threads), "r"((uint32_t)x)
+          : "memory");
+      __syncwarp();
+      return y != 0;
+    };
+    // a word of the row's two threads: c = 1 leaves its part there, c = 0 what
+    // both then go by
+    volatile float *word = reinterpret_cast<volatile float *>(g + C::OFF_ROW) + a * BM + r;
     uint32_t it = 0, vt = 0;  // key tiles of this half so far; of the block
     bool ok = true;
-    for (; ok && more; more = seg_next(s, p)) {
+    for (; more; more = seg_next(s, p)) {
       if (a >= halves()) {
         vt += s.nk;
         continue;
       }
       const int64_t row = (int64_t)s.mt * ROWS + a * BM + r;  // of the (sequence, KV head)
       const bool live = row < (int64_t)s.n * p.G;
-      const bool any_live = row - lane < (int64_t)s.n * p.G;  // in this warp
+      const bool any_live = row - lane < (int64_t)s.n * p.G;  // in this warp, and its partner
       const int tok = live ? (int)(row / p.G) : 0;
       const int seen = live ? min(s.L, max(0, s.L - s.n + tok + 1)) : 0;
       const int64_t urow = ((int64_t)s.h * p.N + s.start) * p.G + row;
       const float rs = live ? __ldcg(p.w.rs + urow) : 0.f;
       float m = 0.f, l = 0.f;
       for (int k = 0; k < s.nk; ++k, ++it, ++vt) {
-        if (!wait_phase(sfull + 8 * a, it & 1u, abort_flag, p.err)) {
-          ok = false;
-          break;
-        }
+        ok = wait_phase(sfull + 8 * a, it & 1u, abort_flag, p.err);
         __syncwarp();
         fence_after();
         const int t0 = (s.k0 + k) * BN;
         // values of keys past the last one, whatever their page holds there,
         // must not meet a weight of zero
         const int left = s.L - t0;
-        if (a == 0 && left < BN) {
+        if (a == 0 && c == 0 && left < BN) {
           const int vs = vt % C::SV;
-          if (!wait_phase(vfull + 8 * vs, (vt / C::SV) & 1u, abort_flag, p.err)) {
-            ok = false;
-            break;
-          }
+          if (ok) ok = wait_phase(vfull + 8 * vs, (vt / C::SV) & 1u, abort_flag, p.err);
           uint8_t *V = g + C::OFF_V + vs * C::TILE + value_offset(r, p, D);
-          if (r >= left)
+          if (ok && r >= left)
             for (int x = 0; x < C::DB; ++x)
 #pragma unroll
               for (int e = 0; e < 8; ++e)
@@ -360,67 +374,77 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         const int lim = seen - t0;  // columns the row sees
         const bool all = __all_sync(~0u, lim >= BN);
-        // 64 keys at a time, so that the first ones' product starts while the
-        // others' weights are computed
-#pragma unroll 1
-        for (int half = 0; half < 2; ++half) {
-          if (any_live) {
-            f32x2 x[32];
-            const float top = all ? row_exponents<false>(tS, half, BN, rs, -m, x)
-                                  : row_exponents<true>(tS, half, lim, rs, -m, x);
-            const bool begin = k == 0 && half == 0;
-            if (begin || __any_sync(~0u, top > RENEW)) {
-              // a new maximum; a row without a key so far refers to 0
-              const float up = begin ? (top == -INFINITY ? 0.f : top) : top > RENEW ? top : 0.f;
-              m += up;
-#pragma unroll
-              for (int e = 0; e < 32; ++e) x[e] = add2(x[e], pair(-up, -up));
-              if (!begin) {
-                // earlier products must have landed before the accumulator is scaled
-                if (!(half ? wait_phase(pvhalf + 8 * a, it & 1u, abort_flag, p.err)
-                           : wait_phase(pv_bar(a, it - 1), pv_phase(it - 1), abort_flag, p.err)))
-                  ok = false;
-                __syncwarp();
-                fence_after();
-                const float f = up == 0.f ? 1.f : fast_exp2(-up);
-                l *= f;
-#pragma unroll 1
-                for (int c = 0; c < D; c += 16) {
-                  uint32_t o[16];
-                  ld16(tO + c, o);
-#pragma unroll
-                  for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                  st16(tO + c, o);
-                }
-                if (!__all_sync(~0u, ok)) {
-                  ok = false;
-                  break;
-                }
-              }
-            }
-            l += all ? row_weights<false>(tS, half, x) : row_weights<true>(tS, half, x);
+        const int lim_c = lim - 64 * c;
+        const uint32_t tC = tS + 64 * c;
+        float top = -INFINITY;  // of the exponents
+        if (any_live) {
+          const float x = all ? row_max<false>(tC, BN) : row_max<true>(tC, lim_c);
+          top = x == -INFINITY ? x : fmaf(x, rs, -m);
+        }
+        // both warps of the rows agree whether they need a new maximum
+        const bool begin = k == 0;
+        if (any(pair_bar, 64, begin || top > RENEW || !ok)) {
+          if (c == 1) *word = top;
+          if (any(pair_bar, 64, !ok)) {
+            ok = false;
+            break;
           }
-          fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(pready + 16 * a + 8 * half);
+          if (c == 0) {
+            top = fmaxf(top, *word);
+            // (a row without a key so far refers to 0)
+            *word = begin ? (top == -INFINITY ? 0.f : top) : top > RENEW ? top : 0.f;
+          }
+          any(pair_bar, 64, false);
+          const float up = *word;
+          m += up;
+          if (!begin) {
+            // earlier products must have landed before the accumulator is scaled
+            ok = wait_phase(pv_bar(a, it - 1), pv_phase(it - 1), abort_flag, p.err);
+            __syncwarp();
+            fence_after();
+            const float f = up == 0.f ? 1.f : fast_exp2(-up);
+            l *= f;
+#pragma unroll 1
+            for (int e0 = c * (D / 2); e0 < (c + 1) * (D / 2); e0 += 16) {
+              uint32_t o[16];
+              ld16(tO + e0, o);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              st16(tO + e0, o);
+            }
+            st_wait();
+            fence_before();
+          }
+          // (also: the words are free again)
+          if (any(pair_bar, 64, !ok)) {
+            ok = false;
+            break;
+          }
         }
-        if (!ok) break;
+        if (any_live)
+          l += all ? row_weights<false>(tC, BN, rs, -m) : row_weights<true>(tC, lim_c, rs, -m);
+        fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(pready + 16 * a + 8 * c);
       }
-      if (!ok) break;
-      // output: the row itself, or its state where the row tile is split
-      const bool whole = s.k0 == 0 && s.k1 == s.units;
-      if (s.nk > 0) {
-        if (!wait_phase(pv_bar(a, it - 1), pv_phase(it - 1), abort_flag, p.err)) {
-          ok = false;
-          break;
-        }
+      if (ok && s.nk > 0) {
+        ok = wait_phase(pv_bar(a, it - 1), pv_phase(it - 1), abort_flag, p.err);
         __syncwarp();
         fence_after();
       }
+      if (c == 1) *word = l;
+      if (any(half_bar, SM_WARPS * 32, !ok)) break;
+      if (c == 0) *word = l += *word;
+      any(pair_bar, 64, false);
+      l = *word;
+      // output: the row itself, or its state where the row tile is split; each
+      // warp the half of the dims that begins at d0
+      const int d0 = c * (D / 2);
+      const bool whole = s.k0 == 0 && s.k1 == s.units;
       const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
       uint16_t *out = p.out + ((int64_t)(s.start + tok) * p.Hq + s.h * p.G +
                                (row - (int64_t)tok * p.G)) * D;
-      auto write_out = [&](int c, const uint32_t (&o)[32], float inv) {  // 32 dims from c on
+      auto write_out = [&](int d, const uint32_t (&o)[32], float inv) {  // 32 dims from d on
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           uint4 q;
@@ -431,7 +455,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                         z = __uint_as_float(o[8 * e + 2 * x + 1]);
             qq[x] = inv == 0.f ? 0u : pack_bf16x2(y * inv, z * inv);
           }
-          *reinterpret_cast<uint4 *>(out + c + 8 * e) = q;
+          *reinterpret_cast<uint4 *>(out + d + 8 * e) = q;
         }
       };
       // states of a split row tile: [half][d + 2][128 rows], a row per lane
@@ -439,29 +463,37 @@ __global__ void __launch_bounds__(THREADS, 1)
       constexpr int HALF = (D + 2) * BM;
       const int64_t mine = (split.record(blockIdx.x) * HALVES + a) * HALF + r;
 #pragma unroll 1
-      for (int c = 0; c < D; c += 32) {
+      for (int d = d0; d < d0 + D / 2; d += 32) {
         uint32_t o[32];
         if (s.nk > 0) {
-          ld32(tO + c, o);
+          ld32(tO + d, o);
           ld_wait(o);
         } else {
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = 0;
         }
         if (whole) {
-          if (live) write_out(c, o, inv);
+          if (live) write_out(d, o, inv);
         } else {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) p.w.part[mine + (c + e) * BM] = __uint_as_float(o[e]);
+          for (int e = 0; e < 32; ++e) p.w.part[mine + (d + e) * BM] = __uint_as_float(o[e]);
         }
       }
+      if (s.nk > 0) {
+        fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(ofree + 8 * a);
+      }
       if (!whole) {
-        p.w.part[mine + D * BM] = m;
-        p.w.part[mine + (D + 1) * BM] = l;
-        if (last_to_arrive(split, p, a, 1 + a, BM, r == 0, join_flag + a)) {
+        if (c == 0) {
+          p.w.part[mine + D * BM] = m;
+          p.w.part[mine + (D + 1) * BM] = l;
+        }
+        if (last_to_arrive(split, p, a, half_bar, SM_WARPS * 32, c == 0 && r == 0,
+                           join_flag + a)) {
           float mj = -INFINITY, lj = 0.f;
-          for (int64_t c = split.c0; c <= split.c1; ++c) {
-            const float *q = p.w.part + (split.record(c) * HALVES + a) * HALF + r;
+          for (int64_t b = split.c0; b <= split.c1; ++b) {
+            const float *q = p.w.part + (split.record(b) * HALVES + a) * HALF + r;
             const float mc = __ldcg(q + D * BM), lc = __ldcg(q + (D + 1) * BM);
             if (lc == 0.f) continue;
             const float mn = fmaxf(mj, mc);
@@ -470,28 +502,25 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
           const float ij = lj > 0.f || lj != lj ? 1.f / lj : 0.f;
 #pragma unroll 1
-          for (int d0 = 0; d0 < D; d0 += 32) {
+          for (int d = d0; d < d0 + D / 2; d += 32) {
             float o[32] = {};
-            for (int64_t c = split.c0; c <= split.c1; ++c) {
-              const float *q = p.w.part + (split.record(c) * HALVES + a) * HALF + r;
+            for (int64_t b = split.c0; b <= split.c1; ++b) {
+              const float *q = p.w.part + (split.record(b) * HALVES + a) * HALF + r;
               const float lc = __ldcg(q + (D + 1) * BM);
               if (lc == 0.f) continue;
               const float w = fast_exp2(__ldcg(q + D * BM) - mj);
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = fmaf(w, __ldcg(q + (d0 + e) * BM), o[e]);
+              for (int e = 0; e < 32; ++e) o[e] = fmaf(w, __ldcg(q + (d + e) * BM), o[e]);
             }
             uint32_t ob[32];
 #pragma unroll
             for (int e = 0; e < 32; ++e) ob[e] = __float_as_uint(o[e]);
-            if (live) write_out(d0, ob, ij);
+            if (live) write_out(d, ob, ij);
           }
         }
       }
-      if (s.nk > 0) {
-        fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(ofree + 8 * a);
-      }
+      // the words are read before the next row tile's
+      asm volatile("bar.sync %0, %1;\n" ::"r"(half_bar), "n"(SM_WARPS * 32) : "memory");
     }
   } else if (warp == MMA_WARP) {
     // ---------------- MMA issue: the halves in turn, values of a tile and then
@@ -548,15 +577,13 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
               for (int i = 0; i < BN / 32; ++i) {
                 const int kk = half * (BN / 32) + i;
-                mma_ts(tmem + C::COL_O + a * D, tmem + a * BN + 8 * kk,
+                mma_ts(tmem + C::COL_O + a * D, tmem + a * BN + 64 * half + 8 * i,
                        dv + voff[kk], id_o,
                        (k > 0 || kk > 0) ? 1u : 0u);
               }
               if (half) {
                 commit(pv_bar(a, it));
                 if (a == na - 1) commit(vempty + 8 * vs);
-              } else {
-                commit(pvhalf + 8 * a);
               }
             }
             __syncwarp();
