@@ -27,6 +27,7 @@ constexpr float RENEW = 16.f;
 constexpr float MIN_SCALE = 1.17549435e-38f;  // of a row: -inf times it stays -inf
 constexpr int PREP_THREADS = 256;
 constexpr int SM_COUNT = 148;      // bounds the workspace per shape
+constexpr int MOST_RECORDS = 128;  // states of one split row tile
 
 struct Plan {
   int64_t total;      // units (key tiles, at least one per row tile)

@@ -189,6 +189,7 @@ struct Cfg {
   static_assert(ST >= 2, "stages");
   static_assert(COL_Z + ZRING * GCOLS <= TMEM && COL_O + NR <= COL_Z, "tensor memory");
   static_assert(SMEM <= 227 * 1024 && 2 * P_BYTES >= BOX, "shared memory");
+  static_assert(MOST_RECORDS * NR * 4 <= 2 * P_BYTES, "weights of the records that are joined");
 };
 
 // Operands whose rows lie along K (V^T: dims contiguous within a key; P^T: rows
@@ -221,7 +222,7 @@ struct Rows {
   float scale[NR], neg[NR];   // of a score; minus the maximum weights refer to
   float factor[NR];           // of sums and accumulators when that is renewed
   float part[SM_WARPS][NR];   // a maximum or sum of each warp
-  float weight[SM_WARPS][NR]; // of the records that are joined
+  float total[SM_WARPS][NR];  // sums, of records that are joined
   float sum[NR];
   int seen[NR];               // keys the row sees
   int out[NR];                // row of the output
@@ -557,39 +558,48 @@ __global__ void __launch_bounds__(Cfg<K, D, NR>::THREADS, 1)
             if (x.y != 0.f) ms = join(ms, x);
           }
           rows.part[gr][j] = ms.x;
-          rows.weight[gr][j] = ms.y;
+          rows.total[gr][j] = ms.y;
           sync();
           if (r < NR) {
-            ms = make_float2(rows.part[0][r], rows.weight[0][r]);
+            ms = make_float2(rows.part[0][r], rows.total[0][r]);
             for (int q = 1; q < GR; ++q)
-              ms = join(ms, make_float2(rows.part[q][r], rows.weight[q][r]));
+              ms = join(ms, make_float2(rows.part[q][r], rows.total[q][r]));
             rows.neg[r] = -ms.x;
             rows.sum[r] = ms.y;
           }
-          // the accumulators, GR records at a time, a record's loads side by side
-          float o[NR];
+          // each record's weight for each row, where P lies (nobody reads or
+          // writes it until this warp's next tile)
+          float *weight = reinterpret_cast<float *>(g + C::OFF_P);
+          const int records = (int)(split.c1 - split.c0) + 1;
+          sync();
+          for (int i = r; i < records * NR; i += SM_WARPS * 32) {
+            const float2 x = state(split.c0 + i / NR);  // (i % NR is j)
+            weight[i] = x.y == 0.f ? 0.f : fast_exp2(x.x + rows.neg[j]);
+          }
+          sync();
+          // the accumulators of eight rows, their loads side by side
+          if (r < D) {
+            for (int j0 = 0; j0 < nrow; j0 += 8) {
+              float o[8] = {};
+#pragma unroll 2
+              for (int i = 0; i < records; ++i) {
+                const float *acc = record(split.c0 + i) + r;
+                float y[8];
 #pragma unroll
-          for (int e = 0; e < NR; ++e) o[e] = 0.f;
-          for (int64_t c0 = split.c0; c0 <= split.c1; c0 += GR) {
-            const float2 x = state(c0 + gr);
-            sync();
-            rows.weight[gr][j] = x.y == 0.f ? 0.f : fast_exp2(x.x + rows.neg[j]);
-            sync();
-            for (int q = 0; q < GR && c0 + q <= split.c1; ++q) {
-              const float *acc = record(c0 + q) + r;
-              if (r < D) {
+                for (int e = 0; e < 8; ++e)
+                  asm volatile("ld.global.cg.f32 %0, [%1];\n"
+                               : "=f"(y[e])
+                               : "l"(acc + min(j0 + e, nrow - 1) * (D + 2)));
 #pragma unroll
-                for (int e = 0; e < NR; ++e) {
-                  const float y = e < nrow ? __ldcg(acc + e * (D + 2)) : 0.f;
-                  o[e] = fmaf(rows.weight[q][e], y, o[e]);
+                for (int e = 0; e < 8; ++e) {
+                  const float w = weight[i * NR + j0 + e];
+                  o[e] = w == 0.f ? o[e] : fmaf(w, y[e], o[e]);
                 }
               }
-            }
-          }
-          if (r < D) {
 #pragma unroll
-            for (int e = 0; e < NR; ++e)
-              if (e < nrow) write(e, o[e]);
+              for (int e = 0; e < 8; ++e)
+                if (j0 + e < nrow) write(j0 + e, o[e]);
+            }
           }
         }
       }
@@ -865,7 +875,9 @@ cudaError_t launch_chunk(const ChunkArgs &a, cudaStream_t stream) {
   p.scale = a.softmax_scale;
   const int sms = device_sm_count();
   p.blocks = sms < chunk::SM_COUNT ? sms : chunk::SM_COUNT;
-  p.min_units = 2;
+  // a row tile is split over MOST_RECORDS blocks at most
+  p.min_units = p.key_tiles / (chunk::MOST_RECORDS - 2) + 1;
+  if (p.min_units < 2) p.min_units = 2;
   return many(a.N, a.B, a.Hq, a.Hkv, a.max_len, a.d) ? chunk::launch_many(p, a, stream)
                                                      : chunk::launch_few(p, a, stream);
 }

@@ -242,6 +242,15 @@ __device__ __forceinline__ float row_weights(uint32_t tS, int lim, float rs, flo
   return s.x + s.y;
 }
 
+// N floats `step` apart, all on their way before the first is needed (volatile
+// loads keep their order and are not sunk to their uses).
+template <int N>
+__device__ __forceinline__ void load_column(const float *q, int step, float *x) {
+#pragma unroll
+  for (int e = 0; e < N; ++e)
+    asm volatile("ld.global.cg.f32 %0, [%1];\n" : "=f"(x[e]) : "l"(q + (int64_t)e * step));
+}
+
 template <int D>
 __global__ void __launch_bounds__(THREADS, 1)
     attend_kernel(const __grid_constant__ CUtensorMap map_u,
@@ -444,9 +453,9 @@ __global__ void __launch_bounds__(THREADS, 1)
       const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
       uint16_t *out = p.out + ((int64_t)(s.start + tok) * p.Hq + s.h * p.G +
                                (row - (int64_t)tok * p.G)) * D;
-      auto write_out = [&](int d, const uint32_t (&o)[32], float inv) {  // 32 dims from d on
+      auto write_out = [&](int d, const uint32_t (&o)[16], float inv) {  // 16 dims from d on
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
+        for (int e = 0; e < 2; ++e) {
           uint4 q;
           uint32_t *qq = reinterpret_cast<uint32_t *>(&q);
 #pragma unroll
@@ -463,20 +472,19 @@ __global__ void __launch_bounds__(THREADS, 1)
       constexpr int HALF = (D + 2) * BM;
       const int64_t mine = (split.record(blockIdx.x) * HALVES + a) * HALF + r;
 #pragma unroll 1
-      for (int d = d0; d < d0 + D / 2; d += 32) {
-        uint32_t o[32];
+      for (int d = d0; d < d0 + D / 2; d += 16) {
+        uint32_t o[16];
         if (s.nk > 0) {
-          ld32(tO + d, o);
-          ld_wait(o);
+          ld16(tO + d, o);
         } else {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = 0;
+          for (int e = 0; e < 16; ++e) o[e] = 0;
         }
         if (whole) {
           if (live) write_out(d, o, inv);
         } else {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) p.w.part[mine + (d + e) * BM] = __uint_as_float(o[e]);
+          for (int e = 0; e < 16; ++e) p.w.part[mine + (d + e) * BM] = __uint_as_float(o[e]);
         }
       }
       if (s.nk > 0) {
@@ -491,9 +499,12 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         if (last_to_arrive(split, p, a, half_bar, SM_WARPS * 32, c == 0 && r == 0,
                            join_flag + a)) {
+          auto record = [&](int64_t b) {
+            return p.w.part + (split.record(b) * HALVES + a) * HALF + r;
+          };
           float mj = -INFINITY, lj = 0.f;
           for (int64_t b = split.c0; b <= split.c1; ++b) {
-            const float *q = p.w.part + (split.record(b) * HALVES + a) * HALF + r;
+            const float *q = record(b);
             const float mc = __ldcg(q + D * BM), lc = __ldcg(q + (D + 1) * BM);
             if (lc == 0.f) continue;
             const float mn = fmaxf(mj, mc);
@@ -502,20 +513,26 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
           const float ij = lj > 0.f || lj != lj ? 1.f / lj : 0.f;
 #pragma unroll 1
-          for (int d = d0; d < d0 + D / 2; d += 32) {
-            float o[32] = {};
+          for (int d = d0; d < d0 + D / 2; d += 16) {
+            float o[16] = {};
+#pragma unroll 1
             for (int64_t b = split.c0; b <= split.c1; ++b) {
-              const float *q = p.w.part + (split.record(b) * HALVES + a) * HALF + r;
-              const float lc = __ldcg(q + (D + 1) * BM);
-              if (lc == 0.f) continue;
-              const float w = fast_exp2(__ldcg(q + D * BM) - mj);
+              const float *q = record(b);
+              float x[18];  // the row's loads side by side
+              load_column<16>(q + d * BM, BM, x);
+              load_column<1>(q + D * BM, BM, x + 16);
+              load_column<1>(q + (D + 1) * BM, BM, x + 17);
+              const bool some = x[17] != 0.f;
+              const float w = some ? fast_exp2(x[16] - mj) : 0.f;
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = fmaf(w, __ldcg(q + (d + e) * BM), o[e]);
+              for (int e = 0; e < 16; ++e) o[e] = some ? fmaf(w, x[e], o[e]) : o[e];
             }
-            uint32_t ob[32];
+            if (live) {
+              uint32_t ob[16];
 #pragma unroll
-            for (int e = 0; e < 32; ++e) ob[e] = __float_as_uint(o[e]);
-            if (live) write_out(d, ob, ij);
+              for (int e = 0; e < 16; ++e) ob[e] = __float_as_uint(o[e]);
+              write_out(d, ob, ij);
+            }
           }
         }
       }
