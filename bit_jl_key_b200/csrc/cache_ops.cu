@@ -30,6 +30,7 @@ struct Pools {
   uint16_t *norms, *values;
   int num_pages, P, Hkv, W, c, d;
   int *err;
+  __device__ __forceinline__ int64_t rows() const { return (int64_t)num_pages * Hkv * P; }
 };
 
 __device__ __forceinline__ int64_t pool_row(const Pools &p, int page, int head, int slot) {
@@ -72,6 +73,9 @@ __device__ __forceinline__ void move_keys(const Pools &p, const Src &src, int64_
       const int who = (i0 + i) * PER + g;
       f[i] = __shfl_sync(~0u, from, who);
       t[i] = __shfl_sync(~0u, to, who);
+      if (!JL_IN_RANGE(p.err, t[i] < 0 ? 0 : t[i], 1, p.rows()) ||
+          !JL_IN_RANGE(p.err, t[i] < 0 ? 0 : f[i], 1, src.rows()))
+        t[i] = -1;
       if (t[i] < 0) continue;
       v[i] = *reinterpret_cast<const uint4 *>(src.value(f[i]) + 8 * l);
       if (l < units) {
@@ -131,6 +135,7 @@ struct Params {
 struct Chunk {
   const Params &p;
   int h;
+  __device__ int64_t rows() const { return p.N; }
   __device__ const uint16_t *value(int64_t r) const { return p.V + r * p.v_tok + h * p.v_head; }
   __device__ const uint32_t *code(int64_t r) const {
     return p.codes + (r * p.pool.Hkv + h) * p.pool.W;
@@ -253,7 +258,8 @@ __global__ void __launch_bounds__(THREADS) mass_kernel(const Params p) {
   share = (share + VEC - 1) / VEC * VEC;
   const int64_t t0 = rank * share < L ? rank * share : L;
   const int64_t t1 = t0 + share < L ? t0 + share : L;
-  const int n = (int)(t1 - t0);
+  // (every access below is inside the block's n keys of its rows)
+  const int n = JL_IN_RANGE(p.err, t0, t1 - t0, p.T) ? (int)(t1 - t0) : 0;
   const float *s0 = p.scores + ((int64_t)b * p.Hq + (int64_t)h * p.G) * p.T + t0;
 
   constexpr int STEP = THREADS * VEC;
@@ -620,7 +626,8 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const Params p) {
   for (int64_t t = a0; t < a1; ++t) {
     int s, e;
     classify(t, s, e);
-    if (s || (e && nt < need)) idx[na + (nt < need ? nt : need)] = (int32_t)t;
+    const int j = na + (nt < need ? nt : need);
+    if ((s || (e && nt < need)) && JL_IN_RANGE(p.pool.err, j, 1, keep)) idx[j] = (int32_t)t;
     na += s;
     nt += e;
   }
@@ -629,6 +636,7 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const Params p) {
 
 struct Cache {
   const Pools &p;
+  __device__ int64_t rows() const { return p.rows(); }
   __device__ const uint16_t *value(int64_t r) const { return p.values + r * p.d; }
   __device__ const uint32_t *code(int64_t r) const { return p.codes + r * p.W; }
   __device__ const uint16_t *norm(int64_t r) const { return p.norms + r * p.c; }
@@ -643,7 +651,7 @@ __global__ void __launch_bounds__(COPY_THREADS) move_kernel(const Params p) {
   const int64_t j = (int64_t)(blockIdx.x - unit * tiles) * COPY_THREADS + threadIdx.x;
   int64_t from = 0, to = -1;
   const int t = j < p.keep ? __ldcg(p.out_index + (int64_t)unit * p.keep + j) : -1;
-  if (j < p.keep)
+  if (j < p.keep && JL_IN_RANGE(p.pool.err, t < 0 ? 0 : t, 1, p.T))
     p.out_mass[(int64_t)unit * p.keep + j] = t >= 0 ? p.mass[(int64_t)unit * p.T + t] : 0.f;
   if (t >= 0) {
     const int sp = table_page(p.src_table, p.src_pages, b, t, p.pool);

@@ -142,6 +142,9 @@ __device__ __forceinline__ void make_plan(const Params &p) {
       p.w.len[b] = L;
       int32_t *pre = p.w.mt_pre + tiles[threadIdx.x];
       int u = 0;
+      if (nt && !JL_IN_RANGE(p.err, tiles[threadIdx.x], nt + 1,
+                             p.N * p.G / p.rows + 2 * (int64_t)p.B + 1))
+        nt = 0;
       for (int mt = 0; mt < nt; ++mt) {
         pre[mt] = u;
         u += tile_units(mt, n, L, p.G, p.rows);

@@ -503,11 +503,13 @@ __global__ void __launch_bounds__(Cfg<K, D, NR>::THREADS, 1)
       auto write = [&](int j, float x) {  // dim r of row j
         const float sum = rows.sum[j];
         const float y = sum == 0.f ? 0.f : __fdividef(x, sum);
-        p.out[(int64_t)rows.out[j] * D + r] = __bfloat16_as_ushort(__float2bfloat16_rn(y));
+        if (JL_IN_RANGE(p.err, rows.out[j], 1, p.N * p.Hq))
+          p.out[(int64_t)rows.out[j] * D + r] = __bfloat16_as_ushort(__float2bfloat16_rn(y));
       };
       // states of a split row tile: [NR][d + 2]
       const Split split(s, p);
       float *mine = p.w.part + split.record(blockIdx.x) * (int64_t)(NR * (D + 2));
+      const bool mine_ok = JL_IN_RANGE(p.err, split.record(blockIdx.x), 1, 2 * SM_COUNT);
 #pragma unroll
       for (int q = 0; q < NR / 16; ++q) {
         if (16 * q >= nrow) break;
@@ -520,7 +522,7 @@ __global__ void __launch_bounds__(Cfg<K, D, NR>::THREADS, 1)
             if (j >= nrow) break;
             if (whole)
               write(j, __uint_as_float(o[e]));
-            else
+            else if (mine_ok)
               mine[j * (D + 2) + r] = __uint_as_float(o[e]);
           }
         }
@@ -531,8 +533,9 @@ __global__ void __launch_bounds__(Cfg<K, D, NR>::THREADS, 1)
         if (lane == 0) mbar_arrive(ofree);
       }
       if (!whole) {
-        if (r < nrow) *reinterpret_cast<float2 *>(mine + r * (D + 2) + D) =
-            make_float2(-rows.neg[r], rows.sum[r]);
+        if (r < nrow && mine_ok)
+          *reinterpret_cast<float2 *>(mine + r * (D + 2) + D) =
+              make_float2(-rows.neg[r], rows.sum[r]);
         if (last_to_arrive(split, p, 0, 1, SM_WARPS * 32, r == 0, join_flag)) {
           // the joined maximum and sum of each row: a quarter of the records
           // (half with 64 rows) to each group of NR threads

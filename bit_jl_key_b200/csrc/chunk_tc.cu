@@ -354,7 +354,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         continue;
       }
       const int64_t row = (int64_t)s.mt * ROWS + a * BM + r;  // of the (sequence, KV head)
-      const bool live = row < (int64_t)s.n * p.G;
+      const bool live = row < (int64_t)s.n * p.G &&
+                        JL_IN_RANGE(p.err, s.start + row / p.G, 1, p.N);
       const bool any_live = row - lane < (int64_t)s.n * p.G;  // in this warp, and its partner
       const int tok = live ? (int)(row / p.G) : 0;
       const int seen = live ? min(s.L, max(0, s.L - s.n + tok + 1)) : 0;
@@ -471,6 +472,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       const Split split(s, p);
       constexpr int HALF = (D + 2) * BM;
       const int64_t mine = (split.record(blockIdx.x) * HALVES + a) * HALF + r;
+      const bool mine_ok = JL_IN_RANGE(p.err, split.record(blockIdx.x), 1, 2 * SM_COUNT);
 #pragma unroll 1
       for (int d = d0; d < d0 + D / 2; d += 16) {
         uint32_t o[16];
@@ -482,7 +484,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         if (whole) {
           if (live) write_out(d, o, inv);
-        } else {
+        } else if (mine_ok) {
 #pragma unroll
           for (int e = 0; e < 16; ++e) p.w.part[mine + (d + e) * BM] = __uint_as_float(o[e]);
         }
@@ -493,7 +495,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (lane == 0) mbar_arrive(ofree + 8 * a);
       }
       if (!whole) {
-        if (c == 0) {
+        if (c == 0 && mine_ok) {
           p.w.part[mine + D * BM] = m;
           p.w.part[mine + (D + 1) * BM] = l;
         }

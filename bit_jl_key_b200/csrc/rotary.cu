@@ -40,7 +40,13 @@ struct Params {
   const int32_t *pos;
   const float *inv_freq;
   float scale, sign;
+  int *err;
 };
+
+// Elements a side's tensor spans (index checks of the debug build).
+__device__ __forceinline__ int64_t span(int64_t n, int H, int d, int64_t tok, int64_t head) {
+  return (n - 1) * tok + (H - 1) * head + d;
+}
 
 template <typename T>
 __device__ __forceinline__ float to_f32(T v);
@@ -97,6 +103,7 @@ __global__ void __launch_bounds__(THREADS) rotary_kernel(const Params p) {
   const int toks = (int)(p.n - t0 < p.tok ? p.n - t0 : p.tok);
   for (int i = threadIdx.x; i < toks * half; i += THREADS) {
     const int tk = i / half, j = i - tk * half;
+    if (!JL_IN_RANGE(p.err, t0 + tk, 1, p.n) || !JL_IN_RANGE(p.err, j, 1, half)) continue;
     const double a = (double)p.pos[t0 + tk] * (double)p.inv_freq[j];
     // a - 2 pi k with 2 pi in two parts
     const double k = rint(a * 0.15915494309189533577);
@@ -137,6 +144,15 @@ __global__ void __launch_bounds__(THREADS) rotary_kernel(const Params p) {
       const T *x = static_cast<const T *>(s.x) + (t0 + tk[q]) * s.x_tok + hh * s.x_head;
       y[q] = static_cast<T *>(s.y) + (t0 + tk[q]) * s.y_tok + hh * s.y_head;
       const int o = u[q] < ru ? u[q] * VEC : p.rot + (u[q] - ru) * VEC;
+      const int last = (!INTER && u[q] < ru ? half : 0) + o + VEC;  // of the row's entries
+      const int Hs = is_q ? p.Hq : p.H - p.Hq;
+      if (!JL_IN_RANGE(p.err, (t0 + tk[q]) * s.x_tok + hh * s.x_head, last,
+                       span(p.n, Hs, p.d, s.x_tok, s.x_head)) ||
+          !JL_IN_RANGE(p.err, (t0 + tk[q]) * s.y_tok + hh * s.y_head, last,
+                       span(p.n, Hs, p.d, s.y_tok, s.y_head))) {
+        u[q] = -1;
+        continue;
+      }
       y[q] += o;
       v[q] = load<T, VEC>(x + o);
       if (!INTER && u[q] < ru) w[q] = load<T, VEC>(x + half + o);
@@ -221,6 +237,8 @@ cudaError_t launch_rotary(const RotaryArgs &a, cudaStream_t stream) {
   p.inv_freq = a.inv_freq;
   p.scale = a.scale;
   p.sign = a.inverse ? -1.f : 1.f;
+  p.err = device_error_ptr();
+  if (!p.err) return cudaErrorInvalidSymbol;
   return a.f32 ? rope::launch_v<float>(p, a.interleaved, stream)
                : rope::launch_v<uint16_t>(p, a.interleaved, stream);
 }

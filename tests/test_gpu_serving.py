@@ -701,3 +701,23 @@ def test_serving_loop():
         # the decode kernel's projections carry 16 bits: inside the same bounds
         assert np.all(np.abs(H.f64(out[r, h]) - o) <= tol + 2 * UB)
     assert jl.jl_device_error() == 0
+
+
+def test_serving_operators_under_index_checks():
+    """These tests once more on the index-checking build: no kernel computes an
+    index outside the extents that the call's shapes give its buffers (every
+    test ends with the device error word clear)."""
+    import os
+    import subprocess
+    import sys
+
+    if jl.jl_build_flags() & jl.JL_BUILD_INDEX_CHECKS:
+        return                                                   # this is that run
+    from bit_jl_key_b200 import build
+    lib = build.build(debug_index=True)
+    r = subprocess.run([sys.executable, "-m", "pytest", "-q", "-x", "-m", "gpu", "-p",
+                        "no:cacheprovider", os.path.abspath(__file__)],
+                       env=dict(os.environ, JLKEY_LIBRARY=lib), capture_output=True, text=True,
+                       timeout=900, cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0, r.stdout[-4000:] + r.stderr[-2000:]
+    assert " passed" in r.stdout
