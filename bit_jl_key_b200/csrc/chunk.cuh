@@ -28,6 +28,7 @@ constexpr float MIN_SCALE = 1.17549435e-38f;  // of a row: -inf times it stays -
 constexpr int PREP_THREADS = 256;
 constexpr int SM_COUNT = 148;      // bounds the workspace per shape
 constexpr int MOST_RECORDS = 128;  // states of one split row tile
+constexpr int MIN_UNITS = 2;       // of a block: less is not worth another state to join
 
 struct Plan {
   int64_t total;      // units (key tiles, at least one per row tile)
@@ -61,7 +62,7 @@ struct Params {
   int64_t q_tok, q_head;
   const uint16_t *S;
   uint16_t *out;
-  int B, Hq, Hkv, G, P, max_pages, num_pages, blocks, min_units, rows;
+  int B, Hq, Hkv, G, P, max_pages, num_pages, blocks, rows;
   int key_tiles;      // of max_len
   int gran, gran_log; // keys of a tile copied at once, all in one page: 32, 64 or 128
   int64_t N, max_len;
@@ -81,11 +82,12 @@ __device__ __forceinline__ void make_plan(const Params &p) {
   __shared__ int tiles[PREP_THREADS];
   __shared__ int first[PREP_THREADS], tokens[PREP_THREADS], keys[PREP_THREADS];
   __shared__ int64_t u_done;
-  __shared__ int t_done, rows_done;
+  __shared__ int t_done, rows_done, longest;  // longest: key tiles of a sequence
   if (threadIdx.x == 0) {
     u_done = 0;
-    t_done = rows_done = 0;
+    t_done = rows_done = longest = 0;
   }
+  __syncthreads();
   for (int b0 = 0; b0 < p.B; b0 += PREP_THREADS) {
     const int b = b0 + threadIdx.x;
     int n = 0, L = 0, nt = 0;
@@ -103,6 +105,7 @@ __device__ __forceinline__ void make_plan(const Params &p) {
       L = (int)(l < 0 ? 0 : l > p.max_len ? p.max_len : l);
       nt = (int)(((int64_t)n * p.G + p.rows - 1) / p.rows);
       for (int mt = 0; mt < nt; ++mt) tot += tile_units(mt, n, L, p.G, p.rows);
+      if (nt) atomicMax(&longest, (L + BN - 1) / BN);
     }
     units[threadIdx.x] = tot;
     tiles[threadIdx.x] = nt ? nt + 1 : 0;
@@ -155,7 +158,9 @@ __device__ __forceinline__ void make_plan(const Params &p) {
   }
   const int64_t total = u_done;
   int64_t quota = (total + p.blocks - 1) / p.blocks;
-  if (quota < p.min_units) quota = p.min_units;
+  if (quota < MIN_UNITS) quota = MIN_UNITS;
+  // a row tile is split over MOST_RECORDS blocks at most
+  if (quota < longest / (MOST_RECORDS - 2) + 1) quota = longest / (MOST_RECORDS - 2) + 1;
   if (threadIdx.x == 0) {
     p.w.b_unit[p.B] = total;
     p.w.plan->total = total;

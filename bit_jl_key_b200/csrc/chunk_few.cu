@@ -878,9 +878,6 @@ cudaError_t launch_chunk(const ChunkArgs &a, cudaStream_t stream) {
   p.scale = a.softmax_scale;
   const int sms = device_sm_count();
   p.blocks = sms < chunk::SM_COUNT ? sms : chunk::SM_COUNT;
-  // a row tile is split over MOST_RECORDS blocks at most
-  p.min_units = p.key_tiles / (chunk::MOST_RECORDS - 2) + 1;
-  if (p.min_units < 2) p.min_units = 2;
   return many(a.N, a.B, a.Hq, a.Hkv, a.max_len, a.d) ? chunk::launch_many(p, a, stream)
                                                      : chunk::launch_few(p, a, stream);
 }

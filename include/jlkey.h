@@ -769,17 +769,17 @@ JL_API int jl_evict_paged(const float *mass, const int32_t *seq_lens, int B, int
  * pipeline wait ran out), JL_DERR_DECODE_PLAN (a decode work split or a
  * paged length did not fit), JL_DERR_DECODE_WAIT_TIMEOUT (a decode copy wait
  * ran out), JL_DERR_INDEX (see below), JL_DERR_PAGE (a block-table entry
- * that a call needed lies outside the pool or past the table's last column;
- * the keys of that page were skipped).
+ * that jl_store_paged, jl_chunk_attention_paged or jl_evict_paged needed lies
+ * outside the pool or past the table's last column).
  */
 enum {
     JL_DERR_TC_WAIT_TIMEOUT = 1,
     JL_DERR_DECODE_PLAN = 3,
     JL_DERR_DECODE_WAIT_TIMEOUT = 4,
-    JL_DERR_PAGE = 6,
-    JL_DERR_INDEX = 5 /* index-checking debug build only: a kernel computed an
+    JL_DERR_INDEX = 5, /* index-checking debug build only: a kernel computed an
                          index outside the extent the call's shapes give a
                          buffer, and skipped that access */
+    JL_DERR_PAGE = 6
 };
 JL_API int jl_device_error(int *code, jl_stream_t stream);
 

@@ -302,15 +302,15 @@ def test_chunk_attention_large_and_small_magnitudes(n):
         check_chunk(c, Q, [n], run_chunk(c, Q, [n]), 64 ** -0.5)
 
 
-@pytest.mark.parametrize("n", [5, 300])
-def test_chunk_attention_long_split_context(n):
+@pytest.mark.parametrize("n,L", [(5, 20000), (300, 20000), (5, 60001)])
+def test_chunk_attention_long_split_context(n, L):
     """One sequence over every block of the grid, each with a state to join."""
-    c = Cache([20000], 1, 64, 64, 64, seed=6)
+    c = Cache([L], 1, 64, 64, 64, seed=6)
     Q = _randn(10, n, 2, 64, dtype=torch.bfloat16)
     got = run_chunk(c, Q, [n])
     for i in (0, 1, n // 2, n - 1):                             # some rows, the last ones
         sub = Cache.__new__(Cache)
-        sub.__dict__ = dict(c.__dict__, lens=[20000 - n + i + 1])
+        sub.__dict__ = dict(c.__dict__, lens=[L - n + i + 1])
         check_chunk(sub, Q[i:i + 1], [1], got[i:i + 1], 64 ** -0.5)
 
 
