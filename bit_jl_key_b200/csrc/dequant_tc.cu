@@ -403,8 +403,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     constexpr int NW = C::TURBO ? 2 * TB + 3 : 2 * KP;  // words of a part's slot
     for (int64_t tile = live_tile<PAGED>(p, blockIdx.x, gridDim.x); ok && tile < ntiles;
          tile = live_tile<PAGED>(p, tile + gridDim.x, gridDim.x)) {
+      if constexpr (!PAGED) ahead = tile + (int64_t)(CODE_SLOTS - 1) * gridDim.x;
       copy_part(code_slot(cs == 0 ? CODE_SLOTS - 1 : cs - 1), row_of(ahead));
-      ahead = live_tile<PAGED>(p, ahead + gridDim.x, gridDim.x);
+      if constexpr (PAGED) ahead = live_tile<PAGED>(p, ahead + gridDim.x, gridDim.x);
       cp_async_wait<CODE_SLOTS - 1>();  // this tile's words have landed
       uint32_t cur[NW];
       {

@@ -37,11 +37,24 @@ struct Params {
   int Hq, H;  // query heads; query and key heads together
   int64_t n;
   int d, rot, tok, heads_per_block;
+  uint64_t units_inv, heads_inv;  // of a head's units and of a block's heads (see over())
   const int32_t *pos;
   const float *inv_freq;
   float scale, sign;
   int *err;
 };
+
+// a / b from ceil(2^40 / b), without a division (which per 16 bytes moved is what
+// bound this kernel): exact while a * b < 2^40, and a block has at most
+// MAX_TOK * MAX_HEADS * 1024 units of at most 1024 per head.
+constexpr int MAX_HEADS = 1024;
+static_assert((uint64_t)MAX_TOK * MAX_HEADS * 1024 * 1024 < (1ull << 40), "exact quotients");
+__host__ __device__ __forceinline__ uint64_t inverse_of(uint32_t b) {
+  return ((1ull << 40) + b - 1) / b;
+}
+__device__ __forceinline__ int over(int a, uint64_t inv) {
+  return (int)(((uint64_t)(uint32_t)a * inv) >> 40);
+}
 
 // Elements a side's tensor spans (index checks of the debug build).
 __device__ __forceinline__ int64_t span(int64_t n, int H, int d, int64_t tok, int64_t head) {
@@ -122,6 +135,8 @@ __global__ void __launch_bounds__(THREADS) rotary_kernel(const Params p) {
   const int h0 = blockIdx.y * p.heads_per_block;
   const int nh = p.H - h0 < p.heads_per_block ? p.H - h0 : p.heads_per_block;
   const int total = toks * nh * units;
+  // (the last blocks of a row have fewer heads than the others)
+  const uint64_t nh_inv = nh == p.heads_per_block ? p.heads_inv : inverse_of(nh);
   constexpr int AT_ONCE = 4;  // units of a thread whose loads are in flight together
   for (int i0 = threadIdx.x; i0 < total; i0 += THREADS * AT_ONCE) {
     Pack<T, VEC> v[AT_ONCE], w[AT_ONCE];
@@ -134,9 +149,9 @@ __global__ void __launch_bounds__(THREADS) rotary_kernel(const Params p) {
         u[q] = -1;
         continue;
       }
-      const int row = i / units;
+      const int row = over(i, p.units_inv);
       u[q] = i - row * units;
-      tk[q] = row / nh;
+      tk[q] = over(row, nh_inv);
       const int h = h0 + row - tk[q] * nh;
       const bool is_q = h < p.Hq;
       const Side &s = is_q ? p.q : p.k;
@@ -198,6 +213,10 @@ cudaError_t launch_t(Params p, cudaStream_t stream) {
   int split = 1;
   while (split < p.H && gx * split < 2 * sms && split < 64) ++split;
   p.heads_per_block = (p.H + split - 1) / split;
+  if (p.heads_per_block > MAX_HEADS) p.heads_per_block = MAX_HEADS;
+  const int ru = INTER ? p.rot / VEC : p.rot / 2 / VEC;
+  p.units_inv = inverse_of(ru + (p.d - p.rot) / VEC);
+  p.heads_inv = inverse_of(p.heads_per_block);
   const int gy = (p.H + p.heads_per_block - 1) / p.heads_per_block;
   const size_t smem = (size_t)tok * (p.rot / 2) * sizeof(float2);
   rotary_kernel<T, INTER, VEC><<<dim3((unsigned)gx, gy), THREADS, smem, stream>>>(p);
