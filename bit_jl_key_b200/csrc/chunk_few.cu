@@ -456,9 +456,10 @@ __global__ void __launch_bounds__(Cfg<K, D, NR>::THREADS, 1)
               const int j = 8 * u + 2 * e;
               const float a = fast_exp2(__uint_as_float(v[q][j])),
                           b = fast_exp2(__uint_as_float(v[q][j + 1]));
-              l[32 * q + j] += a;
-              l[32 * q + j + 1] += b;
               w[e] = pack_bf16x2(a, b);
+              // the sums are of the rounded weights: what they have in common cancels
+              l[32 * q + j] += __uint_as_float(w[e] << 16);
+              l[32 * q + j + 1] += __uint_as_float(w[e] & 0xffff0000u);
             }
             *reinterpret_cast<uint4 *>(P + (((4 * q + u) ^ swz) << 4)) =
                 make_uint4(w[0], w[1], w[2], w[3]);

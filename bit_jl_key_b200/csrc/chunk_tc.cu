@@ -28,7 +28,10 @@
 // the time.  Products issued by one thread execute in order, so the next
 // scores may be issued over weights that an earlier product reads.
 // P is rounded to bf16 (half a step, 2^-8 of each weight, against values that
-// are bf16 themselves); its sum is taken before the rounding, in fp32.
+// are bf16 themselves).  Its sum, in fp32, is of the rounded weights, so that
+// what all the weights of a row have in common cancels: a row that one key
+// dominates loses nothing.
+//
 // A row's weights refer to the maximum of the first keys it met until one would
 // pass 2^RENEW: floating point keeps them as exact, no tile waits for its own
 // maximum, and the accumulator need hardly ever be rescaled.
@@ -208,7 +211,7 @@ __device__ __forceinline__ float row_max(uint32_t tS, int lim) {
 
 // Weights 2^(score rs + mm) of those 64, as bf16 over the first half of their
 // columns, 32 scores at a time (each group's weights go where scores that have
-// been read lay); returns their sum.
+// been read lay); returns the sum of the rounded weights.
 template <bool MASK>
 __device__ __forceinline__ float row_weights(uint32_t tS, int lim, float rs, float mm) {
   const f32x2 rs2 = pair(rs, rs), mm2 = pair(mm, mm);
@@ -232,8 +235,9 @@ __device__ __forceinline__ float row_weights(uint32_t tS, int lim, float rs, flo
         y.x = fast_exp2(y.x);
         y.y = fast_exp2(y.y);
       }
-      sum[e & 1] = add2(sum[e & 1], pair(y.x, y.y));
       w[e] = pack_bf16x2(y.x, y.y);
+      sum[e & 1] = add2(sum[e & 1], pair(__uint_as_float(w[e] << 16),
+                                         __uint_as_float(w[e] & 0xffff0000u)));
     }
     st16(tS + 16 * c, w);
   }
