@@ -191,14 +191,21 @@ int validate_pools(const void *codes, const void *norms, const void *values, int
   return JL_OK;
 }
 
+bool overlap(const void *a, int64_t a_bytes, const void *b, int64_t b_bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + b_bytes && y < x + a_bytes;
+}
+
 // Strides of an n x H x d tensor that is read (any stride, entries may be
-// shared) or written (no two entries at one address).
+// shared) or written (no two entries at one address).  A stride along a single
+// token or head is not looked at.
 bool strides_ok(int64_t n, int H, int d, int64_t tok, int64_t head, bool written) {
-  if (tok < 0 || head < 0 || tok >= ((int64_t)1 << 40) || head >= ((int64_t)1 << 40)) return false;
+  constexpr int64_t most = (int64_t)1 << 40;
+  if ((n > 1 && (tok < 0 || tok >= most)) || (H > 1 && (head < 0 || head >= most))) return false;
   if (!written) return true;
   if (n == 1) return H == 1 || head >= d;
   if (H == 1) return tok >= d;
-  return (head >= d && tok >= head * (H - 1) + d) || (tok >= d && head >= tok * (n - 1) + d);
+  return (head >= d && tok >= head * (H - 1) + d) || (tok >= d && (head - d) / tok >= n - 1);
 }
 
 }  // namespace
@@ -625,8 +632,9 @@ int jl_store_paged(const uint32_t *codes, const uint16_t *norms, const uint16_t 
   if (!codes || !norms || !V || !cu_seqlens || !block_table || !seq_lens)
     return JL_ERR_INVALID_ARG;
   if (!aligned(codes, 4) || !aligned(norms, 2) || !aligned(V, 16) || !aligned(cu_seqlens, 4) ||
-      !aligned(block_table, 4) || !aligned(seq_lens, 4) || v_tok_stride % 8 != 0 ||
-      v_head_stride % 8 != 0 || !strides_ok(N, Hkv, d, v_tok_stride, v_head_stride, false))
+      !aligned(block_table, 4) || !aligned(seq_lens, 4) || (N > 1 && v_tok_stride % 8 != 0) ||
+      (Hkv > 1 && v_head_stride % 8 != 0) ||
+      !strides_ok(N, Hkv, d, v_tok_stride, v_head_stride, false))
     return JL_ERR_INVALID_ARG;
   jlk::StoreArgs a{};
   a.codes = codes; a.norms = norms; a.V = V; a.v_tok = v_tok_stride; a.v_head = v_head_stride;
@@ -720,8 +728,12 @@ int jl_evict_paged(const float *mass, const int32_t *seq_lens, int B, int Hkv, i
       (int64_t)B * Hkv * ((int64_t)keep / 16 + 1) >= ((int64_t)1 << 31))
     return JL_ERR_UNSUPPORTED;
   if (B == 0) return JL_OK;
-  if (!mass || !seq_lens || !src_table || !dst_table || !out_index || !out_mass || !out_lens ||
-      out_mass == mass)
+  if (!mass || !seq_lens || !src_table || !dst_table || !out_index || !out_mass || !out_lens)
+    return JL_ERR_INVALID_ARG;
+  // nothing may be written that the call still reads: a block's answer is out
+  // before another has read its input
+  if (overlap(out_mass, (int64_t)B * Hkv * keep * 4, mass, (int64_t)B * Hkv * max_len * 4) ||
+      overlap(out_lens, (int64_t)B * 4, seq_lens, (int64_t)B * 4) || src_table == dst_table)
     return JL_ERR_INVALID_ARG;
   if (!aligned(mass, 4) || !aligned(seq_lens, 4) || !aligned(src_table, 4) ||
       !aligned(dst_table, 4) || !aligned(out_index, 4) || !aligned(out_mass, 4) ||

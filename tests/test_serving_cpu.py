@@ -13,7 +13,7 @@ import bit_jl_key_b200 as jl
 
 NULL = ctypes.c_void_p(0)
 FAKE = ctypes.c_void_p(1 << 20)          # 16-byte aligned, never dereferenced
-FAKE2 = ctypes.c_void_p(1 << 21)
+FAKE2, FAKE3 = ctypes.c_void_p(1 << 21), ctypes.c_void_p(3 << 20)
 ODD = ctypes.c_void_p((1 << 20) + 2)
 
 INVALID, UNSUPPORTED, OK, WORKSPACE = (jl.JL_ERR_INVALID_ARG, jl.JL_ERR_UNSUPPORTED, jl.JL_OK,
@@ -146,14 +146,19 @@ def test_accumulate_refused(lib):
 
 def test_evict_refused(lib):
     call = caller(lib.jl_evict_paged, m=FAKE, lens=FAKE, B=2, Hkv=2, max_len=200, keep=100,
-                  recent=10, sink=4, words=8, cn=1, d=128, **POOLS, src=FAKE, sp=4, dst=FAKE,
-                  dp=2, oi=FAKE, om=FAKE2, ol=FAKE, stream=NULL)
+                  recent=10, sink=4, words=8, cn=1, d=128, **POOLS, src=FAKE, sp=4, dst=FAKE2,
+                  dp=2, oi=FAKE, om=FAKE2, ol=FAKE3, stream=NULL)
     assert call(B=0) == OK
     for bad in (dict(B=-1), dict(Hkv=0), dict(max_len=0), dict(keep=0), dict(recent=-1),
                 dict(sink=-1), dict(recent=97), dict(recent=2 ** 31 - 1, sink=2 ** 31 - 1),
                 dict(sp=0), dict(dp=0), dict(dp=1), dict(sp=3), dict(P=48), dict(codes=NULL),
                 dict(m=NULL), dict(lens=NULL), dict(src=NULL), dict(dst=NULL), dict(oi=NULL),
                 dict(om=NULL), dict(ol=NULL), dict(om=FAKE), dict(om=ODD)):
+        assert call(**bad) == INVALID, bad
+    # written and still read: the mass, in part too; the lengths; a cache shrunk in place
+    at = lambda p, off: ctypes.c_void_p(p.value + off)
+    for bad in (dict(om=at(FAKE, 2 * 2 * 200 * 4 - 4)), dict(om=at(FAKE, 4 - 2 * 2 * 100 * 4)),
+                dict(ol=FAKE), dict(ol=at(FAKE, 4)), dict(dst=FAKE)):
         assert call(**bad) == INVALID, bad
     for bad in (dict(d=80), dict(words=99), dict(cn=4)):
         assert call(**bad) == UNSUPPORTED, bad
