@@ -627,6 +627,101 @@ def test_evict_bad_lengths_and_pages_are_reported():
 
 
 # --------------------------------------------------------------------------
+# where they can go wrong
+
+@pytest.mark.parametrize("n", [1, 5, 300])
+def test_chunk_attention_of_one_key_is_its_value(n):
+    """A sequence of one key, and the last of n rows that alone sees it: the
+    weight cancels in full, so the value comes out as it went in."""
+    c = Cache([1, 1], 2, 128, 256, 32, seed=13)
+    Q = _randn(14, n + 1, 8, 128, dtype=torch.bfloat16)
+    got = run_chunk(c, Q, [n, 1])
+    for b, row in ((0, n - 1), (1, n)):
+        want = c.values[c.table[b, 0], :, 0].to(DEV).repeat_interleave(4, 0)
+        assert torch.equal(got[row], want)
+    assert torch.all(got[:n - 1] == 0)
+
+
+@pytest.mark.parametrize("n", [5, 200])
+def test_offsets_beyond_32_bits(n):
+    """The last pages of pools whose values pass 2^32 entries: stored, attended
+    over, evicted."""
+    P, d, m, L, keep = 128, 128, 64, 700, 200
+    c = Cache([L], 1, d, m, P, seed=15, extra=2)
+    used = c.codes.shape[0]
+    first = 2 ** 32 // (P * d) + 5 - used
+    pools = [torch.empty(first + used, *x.shape[1:], dtype=x.dtype, device=DEV)
+             for x in c.dev()[:3]]
+    for p, x in zip(pools, c.dev()[:3]):
+        p[first:] = x
+    assert pools[2].numel() > 2 ** 32
+    table = np.where(c.table >= 0, c.table + first, -1)
+    free = first + np.setdiff1d(np.arange(used), c.table)
+    # the last n keys are taken out and stored anew
+    t = np.arange(L - n, L)
+    at = torch.from_numpy(table[0, t // P]).long(), slice(None), torch.from_numpy(t % P)
+    new = [p[at[0].to(DEV), 0, at[2].to(DEV)].unsqueeze(1).contiguous() for p in pools]
+    for p in pools:
+        p[at[0].to(DEV), 0, at[2].to(DEV)] = 0
+    jl.jl_store_paged(*new, _i32([0, n]), *pools, _i32(table), _i32([L - n]))
+    for p, x in zip(pools, c.dev()[:3]):
+        assert torch.equal(p[first:].view(torch.uint8), x.view(torch.uint8))
+    Q = _randn(16, n, 2, d, dtype=torch.bfloat16)
+    got = jl.jl_chunk_attention_paged(Q, c.S, *pools, _i32(table), _i32([L]), _i32([0, n]), L)
+    assert torch.equal(got, run_chunk(c, Q, [n]))
+    mass = _randn(17, 1, 1, L)
+    idx, _, _ = jl.jl_evict_paged(mass, _i32([L]), keep, *pools, _i32(table), _i32(free[None]),
+                                  recent=7, sink=3)
+    kept = evict64(mass[0, 0].cpu().numpy(), L, keep, 7, 3)
+    assert np.array_equal(idx[0, 0].cpu().numpy(), kept)
+    j = np.arange(keep)
+    for p in pools:
+        a = p[torch.from_numpy(free[j // P]).to(DEV), 0, torch.from_numpy(j % P).to(DEV)]
+        b = p[torch.from_numpy(table[0, kept // P]).long().to(DEV), 0,
+              torch.from_numpy(kept % P).to(DEV)]
+        assert torch.equal(a, b)
+
+
+def test_rotary_and_weights_beyond_32_bits():
+    """Strides and tensors past 2^31 entries."""
+    tok, n, H_, d = 2 ** 30 + 64, 4, 2, 64
+    big = torch.empty(3 * tok + H_ * d, dtype=torch.bfloat16, device=DEV)
+    Q = big.as_strided((n, H_, d), (tok, d, 1))
+    Q.copy_(_randn(1, n, H_, d, dtype=torch.bfloat16))
+    f = jl.jl_rotary_frequencies(d)
+    pos = _i32([0, 7, 2 ** 31 - 1, -5])
+    want = jl.jl_rotary(Q.contiguous(), pos, f)
+    assert torch.equal(jl.jl_rotary(Q, pos, f), want)
+    assert jl.jl_rotary(Q, pos, f, out_q=Q) is Q and torch.equal(Q, want)
+    del big, Q
+    Hq, T = 9, 2 ** 28
+    scores = torch.empty(1, Hq, T, device=DEV)
+    scores.normal_(generator=torch.Generator(DEV).manual_seed(2))
+    mass = torch.zeros(1, Hq, T, device=DEV)
+    jl.jl_accumulate_attention(scores, mass, _i32([T]), 0.5)
+    alone = torch.zeros(1, 1, T, device=DEV)
+    jl.jl_accumulate_attention(scores[:, -1:].contiguous(), alone, _i32([T]), 0.5)
+    # both rows are split over as many blocks, so the sums have one order
+    assert torch.equal(mass[:, -1:], alone)
+    # a thread sums 2^16 of the weights, each step rounded by 2^-24 of the sum
+    assert abs(mass[0, -1].double().sum().item() - 1) < 2.0 ** -8
+
+
+def test_strides_along_a_single_token_or_head_are_not_read():
+    Hkv, P, d = 1, 32, 64
+    pools = (torch.zeros(2, Hkv, P, 2, dtype=torch.int32, device=DEV),
+             torch.zeros(2, Hkv, P, dtype=torch.float16, device=DEV),
+             torch.zeros(2, Hkv, P, d, dtype=torch.bfloat16, device=DEV))
+    V = _randn(1, 1, Hkv, d, dtype=torch.bfloat16).as_strided((1, Hkv, d), (3, 5, 1))
+    codes, norms = torch.ones(1, 1, 2, dtype=torch.int32, device=DEV), torch.ones(
+        1, 1, dtype=torch.float16, device=DEV)
+    jl.jl_store_paged(codes, norms, V, _i32([0, 1]), *pools, _i32([[1]]), _i32([3]))
+    assert torch.equal(pools[2][1, 0, 3], V[0, 0]) and pools[0].sum() == 2
+    f = jl.jl_rotary_frequencies(d)
+    assert torch.equal(jl.jl_rotary(V, _i32([9]), f), jl.jl_rotary(V.contiguous(), _i32([9]), f))
+
+
+# --------------------------------------------------------------------------
 # the operators together
 
 def test_serving_loop():
