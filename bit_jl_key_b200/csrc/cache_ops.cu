@@ -10,8 +10,9 @@
 //           `recent`, and of the others the ones with the largest mass (equal
 //           masses: the lower index) up to `keep` in all, in their order.
 //
-// All three are bound by memory; the selection of the eviction is a radix
-// select whose histograms and prefix sums are shared by a cluster of blocks.
+// All three are bound by memory, small calls by the latency of a launch; the
+// selection of the eviction is a radix select whose histograms and prefix sums
+// are shared by a cluster of blocks.
 #include "jl_common.cuh"
 #include "jl_internal.h"
 
@@ -146,7 +147,9 @@ struct Chunk {
 };
 
 // A warp takes 32 consecutive tokens of one KV head, whose rows are neighbours
-// in a page; each lane finds its token's sequence and place.
+// in a page; each lane finds its token's sequence and place.  Bound by memory:
+// 16384 tokens x 8 heads of 308 bytes are 80.7 MB read and written in 15.5 us
+// (5.2 TB/s); 40 tokens take a launch.
 template <int D, int UNIT>
 __global__ void __launch_bounds__(THREADS) store_kernel(const Params p) {
   const int h = blockIdx.y;
@@ -240,7 +243,10 @@ __device__ __forceinline__ void load_scores(const float *s, int i, int n, float 
 // in flight together, for the softmax states, which the blocks exchange through
 // distributed shared memory; pass two reads the scores again, from L2, and
 // writes the weights.  (Keeping them in shared memory in between measured no
-// faster: it costs resident blocks.)
+// faster: it costs resident blocks.)  8 sequences of up to 32768 keys, 32 over 8
+// heads, are 40 MB in 18.5-22 us, where the bytes alone would take 6.3: the rest
+// is latency, of the launch, of a first trip to memory per pass and of the
+// blocks' two meetings.
 template <int VEC>
 __global__ void __launch_bounds__(THREADS) mass_kernel(const Params p) {
   extern __shared__ MS ms_smem[];            // [G][WARPS], then [G] of the block, [G] of all
@@ -384,9 +390,9 @@ cudaError_t launch_cluster(K kernel, int64_t blocks, int cluster, int threads, s
 }
 
 // Blocks per (sequence, KV head): as many as give the device 256 of them, while
-// each keeps `least` keys, up to the portable cluster size.  (64 units of 32768
-// keys: 4 blocks 20.5 and 8 blocks 28 us for the weights, 41 and 55 us for the
-// selection; 32 units of 131072 keys: 29 and 19.5 us for the weights.)
+// each keeps `least` keys, up to the portable cluster size.  (Weights, 4 against 8
+// blocks: 64 units of 32768 keys 20.5 and 28 us, 32 units of 131072 keys 29 and
+// 19.5 us.  Selection, 64 units of 32768 keys: 41 and 55 us when this was chosen.)
 int cluster_for(int64_t units, int64_t keys, int least) {
   int c = 1;
   while (c < 8 && units * c < 256 && keys / (2 * c) >= least) c *= 2;
@@ -483,12 +489,19 @@ __device__ __forceinline__ void block_scan(int &a, int &b, int &ta, int &tb, int
   __syncthreads();
 }
 
+// Word of a block's i-th sort key: one word in 33 is left out, so that threads
+// that each read a run of neighbouring keys meet in no bank.
+__host__ __device__ __forceinline__ int64_t place(int64_t i) { return i + (i >> 5); }
+
 // Which keys stay.  A cluster per (sequence, KV head), whose blocks own
 // neighbouring ranges of keys.  The `need` largest masses of the candidates
 // (all but the first `sink` and the last `recent`) are those above the
 // threshold key found 8 bits at a time from histograms summed over the
 // cluster, and the first ones of those equal to it; a prefix sum over the
-// blocks then numbers the kept keys in order.
+// blocks then numbers the kept keys in order.  Bound by latency: of 25 us in the
+// kernel (64 units of 32768 keys) 4 go to the loads, 3.8 to each of the four
+// digits (counting 1.5, the blocks' meeting 1.2, sum and search 1.1) and 6 to
+// numbering and writing the indices.
 __global__ void __launch_bounds__(THREADS) select_kernel(const Params p) {
   extern __shared__ uint32_t cache[];  // the block's sort keys, if they fit
   __shared__ uint32_t copies[BINS * COPIES], hist[2][BINS], sum[BINS];
@@ -523,11 +536,11 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const Params p) {
         if (t + q * THREADS < t1) x[q] = m[t + q * THREADS];
 #pragma unroll
       for (int q = 0; q < AT_ONCE; ++q)
-        if (t + q * THREADS < t1) cache[t + q * THREADS - t0] = sort_key(x[q]);
+        if (t + q * THREADS < t1) cache[place(t + q * THREADS - t0)] = sort_key(x[q]);
     }
     __syncthreads();
   }
-  auto key = [&](int64_t t) { return p.cached ? cache[t - t0] : sort_key(m[t]); };
+  auto key = [&](int64_t t) { return p.cached ? cache[place(t - t0)] : sort_key(m[t]); };
 
   int need = (int)(keep - p.sink - p.recent);    // of the candidates; may be 0
   uint32_t prefix = 0, mask = 0;                 // threshold digits found so far
@@ -642,7 +655,8 @@ struct Cache {
   __device__ const uint16_t *norm(int64_t r) const { return p.norms + r * p.c; }
 };
 
-// Moves the kept keys, 32 neighbouring slots of the new pages to a warp.
+// Moves the kept keys, 32 neighbouring slots of the new pages to a warp.  Bound by
+// memory: 1.05 M keys of 290 bytes, 0.61 GB read and written, in 111 us (5.5 TB/s).
 template <int D, int UNIT>
 __global__ void __launch_bounds__(COPY_THREADS) move_kernel(const Params p) {
   griddep_wait();
@@ -679,8 +693,8 @@ cudaError_t launch_evict_paged(const EvictArgs &a, cudaStream_t stream) {
   const int64_t share = (a.max_len + cluster - 1) / cluster;
   // 192 KB of sort keys at most: with the block's static shared memory that
   // stays inside the 227 KB a block may have
-  p.cached = share * 4 <= 192 * 1024;
-  const size_t smem = p.cached ? (size_t)share * 4 : 0;
+  p.cached = evict::place(share) * 4 <= 192 * 1024;
+  const size_t smem = p.cached ? (size_t)evict::place(share) * 4 : 0;
   cudaError_t e = cudaSuccess;
   if (smem > 32 * 1024)  // with the static part, beyond what a block gets without asking
     e = cudaFuncSetAttribute(evict::select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
