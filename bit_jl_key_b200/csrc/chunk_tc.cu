@@ -509,29 +509,42 @@ __global__ void __launch_bounds__(THREADS, 1)
             return p.w.part + (split.record(b) * HALVES + a) * HALF + r;
           };
           float mj = -INFINITY, lj = 0.f;
-          for (int64_t b = split.c0; b <= split.c1; ++b) {
-            const float *q = record(b);
-            const float mc = __ldcg(q + D * BM), lc = __ldcg(q + (D + 1) * BM);
-            if (lc == 0.f) continue;
-            const float mn = fmaxf(mj, mc);
-            lj = lj * (mj == mn ? 1.f : fast_exp2(mj - mn)) + lc * fast_exp2(mc - mn);
-            mj = mn;
+          constexpr int M_AT_ONCE = 4, O_AT_ONCE = 2;  // records whose loads go side by side
+#pragma unroll 1
+          for (int64_t b = split.c0; b <= split.c1; b += M_AT_ONCE) {
+            float x[M_AT_ONCE][2];
+#pragma unroll
+            for (int i = 0; i < M_AT_ONCE; ++i)
+              load_column<2>(record(b + i < split.c1 ? b + i : split.c1) + D * BM, BM, x[i]);
+#pragma unroll
+            for (int i = 0; i < M_AT_ONCE; ++i) {
+              const float mc = x[i][0], lc = x[i][1];
+              if (b + i > split.c1 || lc == 0.f) continue;
+              const float mn = fmaxf(mj, mc);
+              lj = lj * (mj == mn ? 1.f : fast_exp2(mj - mn)) + lc * fast_exp2(mc - mn);
+              mj = mn;
+            }
           }
           const float ij = lj > 0.f || lj != lj ? 1.f / lj : 0.f;
 #pragma unroll 1
           for (int d = d0; d < d0 + D / 2; d += 16) {
             float o[16] = {};
 #pragma unroll 1
-            for (int64_t b = split.c0; b <= split.c1; ++b) {
-              const float *q = record(b);
-              float x[18];  // the row's loads side by side
-              load_column<16>(q + d * BM, BM, x);
-              load_column<1>(q + D * BM, BM, x + 16);
-              load_column<1>(q + (D + 1) * BM, BM, x + 17);
-              const bool some = x[17] != 0.f;
-              const float w = some ? fast_exp2(x[16] - mj) : 0.f;
+            for (int64_t b = split.c0; b <= split.c1; b += O_AT_ONCE) {
+              float x[O_AT_ONCE][18];
 #pragma unroll
-              for (int e = 0; e < 16; ++e) o[e] = some ? fmaf(w, x[e], o[e]) : o[e];
+              for (int i = 0; i < O_AT_ONCE; ++i) {
+                const float *q = record(b + i < split.c1 ? b + i : split.c1);
+                load_column<16>(q + d * BM, BM, x[i]);
+                load_column<2>(q + D * BM, BM, x[i] + 16);
+              }
+#pragma unroll
+              for (int i = 0; i < O_AT_ONCE; ++i) {
+                const bool some = b + i <= split.c1 && x[i][17] != 0.f;
+                const float w = some ? fast_exp2(x[i][16] - mj) : 0.f;
+#pragma unroll
+                for (int e = 0; e < 16; ++e) o[e] = some ? fmaf(w, x[i][e], o[e]) : o[e];
+              }
             }
             if (live) {
               uint32_t ob[16];

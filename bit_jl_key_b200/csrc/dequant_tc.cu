@@ -151,8 +151,8 @@ template <bool PAGED>
 __device__ __forceinline__ int64_t live_tile(const Params &p, int64_t tile, int64_t step) {
   if constexpr (PAGED) {
     while (tile < p.num_tiles) {
-      const int64_t unit = tile / p.key_tiles;  // (sequence, KV head)
-      if ((tile - unit * p.key_tiles) * BM < paged_len(p, (int)(unit / p.Hkv))) break;
+      const uint32_t unit = (uint32_t)tile / p.key_tiles;  // (sequence, KV head)
+      if ((tile - (int64_t)unit * p.key_tiles) * BM < paged_len(p, unit / p.Hkv)) break;
       tile += step;
     }
   }
@@ -162,11 +162,10 @@ __device__ __forceinline__ int64_t live_tile(const Params &p, int64_t tile, int6
 // outside the pool (recorded).
 __device__ __forceinline__ int64_t paged_row(const Params &p, int64_t tile, int r) {
   if (tile >= p.num_tiles) return -1;
-  const int64_t unit = tile / p.key_tiles;
-  const int b = (int)(unit / p.Hkv), h = (int)(unit - (int64_t)b * p.Hkv);
-  const int64_t t = (tile - unit * p.key_tiles) * BM + r;
+  const uint32_t unit = (uint32_t)tile / p.key_tiles, b = unit / p.Hkv, h = unit - b * p.Hkv;
+  const int t = ((int)tile - (int)unit * p.key_tiles) * BM + r;  // below max_len + BM
   if (t >= paged_len(p, b)) return -1;
-  const int col = (int)(t / p.P);
+  const int col = t / p.P;
   const int page = col < p.max_pages ? __ldg(p.table + (int64_t)b * p.max_pages + col) : -1;
   if (page < 0 || page >= p.num_pages) {
     record_device_error(p.err, DERR_PAGE);
