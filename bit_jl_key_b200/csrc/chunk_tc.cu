@@ -185,7 +185,8 @@ __device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
 // the exponential unit has no time for.  x = n + f with n the nearest whole
 // number, 2^f by the cubic with the least largest relative error on
 // [-1/2, 1/2] (Remez exchange; 7.5e-5 = 2^-13.7, a fiftieth of the rounding to
-// bf16 that follows), n added to the exponent.  x below -126 gives 2^-126.
+// bf16 that follows), n added to the exponent.  x below -126 gives 2^-126, and
+// so does a NaN: a row with one is made NaN through its maximum.
 __device__ __forceinline__ float2 exp2_poly(f32x2 x) {
   constexpr float BIG = 12582912.f;  // 1.5 * 2^23: adding it rounds to a whole number
   const float2 c = halves_of(x);
@@ -201,7 +202,15 @@ __device__ __forceinline__ float2 exp2_poly(f32x2 x) {
                      __uint_as_float(__float_as_uint(k.y) * 0x800000u + __float_as_uint(v.y)));
 }
 
-// Largest of the 64 scores at tS; those from column lim on do not count.
+// The larger one, or NaN where either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;\n" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+
+// Largest of the 64 scores at tS, NaN if one of them is; those from column lim
+// on do not count.
 template <bool MASK>
 __device__ __forceinline__ float row_max(uint32_t tS, int lim) {
   uint32_t v[2][32];
@@ -217,9 +226,9 @@ __device__ __forceinline__ float row_max(uint32_t tS, int lim) {
       float x = __uint_as_float(v[c][e]), y = __uint_as_float(v[c][e + 1]);
       if (MASK && 32 * c + e >= lim) x = -INFINITY;
       if (MASK && 32 * c + e + 1 >= lim) y = -INFINITY;
-      t[(e >> 1) & 3] = fmaxf(t[(e >> 1) & 3], fmaxf(x, y));
+      t[(e >> 1) & 3] = max_nan(t[(e >> 1) & 3], max_nan(x, y));
     }
-  return fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
+  return max_nan(max_nan(t[0], t[1]), max_nan(t[2], t[3]));
 }
 
 // Weights 2^(score rs + mm) of those 64, as bf16 over the first half of their
@@ -410,16 +419,19 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         // both warps of the rows agree whether they need a new maximum
         const bool begin = k == 0;
-        if (any(pair_bar, 64, begin || top > RENEW || !ok)) {
+        if (any(pair_bar, 64, begin || !(top <= RENEW) || !ok)) {
           if (c == 1) *word = top;
           if (any(pair_bar, 64, !ok)) {
             ok = false;
             break;
           }
           if (c == 0) {
-            top = fmaxf(top, *word);
+            top = max_nan(top, *word);
+            // a row that sees a NaN or an infinite score, or none that is finite,
+            // is NaN from here on, whichever of its weights would show it
+            if (top == INFINITY || (begin && lim > 0 && top == -INFINITY)) top = NAN;
             // (a row without a key so far refers to 0)
-            *word = begin ? (top == -INFINITY ? 0.f : top) : top > RENEW ? top : 0.f;
+            *word = begin ? (top == -INFINITY ? 0.f : top) : top <= RENEW ? 0.f : top;
           }
           any(pair_bar, 64, false);
           const float up = *word;

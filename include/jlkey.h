@@ -672,7 +672,8 @@ JL_API size_t jl_chunk_attention_workspace_bytes(int64_t N, int B, int Hq, int H
  * (jl_store_paged); with n = cu_seqlens[b + 1] - cu_seqlens[b] rows and
  * L = seq_lens[b] keys, row i of sequence b attends over the keys
  * t < L - n + i + 1, with the logit of jl_decode_attention_paged, so that the
- * call equals n decode steps.  A row that sees no key (n > L) gets zeros.
+ * call equals n decode steps.  A row that sees no key (n > L) gets zeros; one
+ * that sees a key whose score is not finite is NaN.
  *   Q          : in, N x Hq x d of q_dtype, token and head strides in elements,
  *                d entries contiguous; aligned to its element.
  *   S, sign_pages, norm_pages, value_pages, num_pages, page_tokens,

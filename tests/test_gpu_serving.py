@@ -357,6 +357,52 @@ def test_chunk_attention_nan_and_inf_stay_in_their_rows():
         assert torch.equal(got[:n - 1], ref[:n - 1])
 
 
+@pytest.mark.parametrize("n", [4, 320])
+@pytest.mark.parametrize("x", [math.nan, math.inf])
+def test_chunk_attention_a_key_that_is_not_finite_shows_in_every_row_that_sees_it(n, x):
+    """One key whose norm is not finite, at each place of a group of eight, in
+    the first tile, in inner ones, where some rows see it and others do not, and
+    last: rows that see it are NaN in all dims, the others as without it."""
+    L, P = 600, 32
+    c = Cache([L], 1, 64, 128, P, seed=13)
+    Q = _randn(15, n, 2, 64)
+    ref = run_chunk(c, Q, [n])
+    assert torch.isfinite(ref.float()).all()
+    for t in (*range(8), 130, 206, 207, L - n, L - n + 1, L - n // 2, L - 1):
+        at = c.table[0, t // P], 0, t % P
+        old = c.norms[at]
+        c.norms[at] = x
+        got = run_chunk(c, Q, [n])
+        c.norms[at] = old
+        sees = torch.arange(n) + L - n + 1 > t
+        assert sees.any()
+        assert torch.isnan(got[sees.to(DEV)].float()).all(), t
+        assert torch.equal(got[~sees.to(DEV)], ref[~sees.to(DEV)]), t
+
+
+def test_chunk_attention_many_rows_with_queries_that_are_not_finite():
+    """NaN and infinite queries among many rows, each over keys that it sees."""
+    n, L = 320, 600
+    c = Cache([L], 1, 64, 128, 32, seed=13)
+    Q = _randn(14, n, 2, 64)
+    ref = run_chunk(c, Q, [n])
+    Q[1, 0, 3], Q[2, 1, 5] = math.nan, math.inf
+    got = run_chunk(c, Q, [n])
+    same = torch.ones(n, 2, dtype=torch.bool)
+    same[1, 0] = same[2, 1] = False
+    assert torch.equal(got[same.to(DEV)], ref[same.to(DEV)])
+    assert torch.isnan(got[~same.to(DEV)].float()).all()
+    # a row whose only key scores -inf
+    c.lens[0] = n
+    khat = c.keys(0, 0)[0][0]
+    j = int(np.argmin(khat))
+    assert khat[j] < 0
+    Q[:] = 1.0
+    Q[0, :, j] = math.inf
+    got = run_chunk(c, Q, [n])
+    assert torch.isnan(got[0].float()).all() and torch.isfinite(got[1:].float()).all()
+
+
 def test_chunk_attention_bad_lengths_and_pages_are_reported():
     c = Cache([100, 70], 1, 64, 64, 32, seed=16)
     Q = _randn(17, 8, 1, 64)
