@@ -212,11 +212,12 @@ struct Params {
 struct MS {
   float m, l;
 };
-// Joins two softmax states; a state without keys is (-inf, 0).  The maximum is
-// of the scores themselves (times the scale's sign): only differences are
-// scaled, so a row of the type's lowest value is as uniform as any other.
+// Joins two softmax states; a state without keys is (-inf, 0), and one with a
+// NaN among them NaN in both.  The maximum is of the scores themselves (times
+// the scale's sign): only differences are scaled, so a row of the type's lowest
+// value is as uniform as any other.
 __device__ __forceinline__ MS join(MS a, MS b, float k) {
-  const float m = fmaxf(a.m, b.m);
+  const float m = max_nan(a.m, b.m);
   if (m == -INFINITY) return {m, 0.f};
   return {m, a.l * exp2f((a.m - m) * k) + b.l * exp2f((b.m - m) * k)};
 }
@@ -286,8 +287,8 @@ __global__ void __launch_bounds__(THREADS) mass_kernel(const Params p) {
 #pragma unroll
         for (int q = 0; q < LOADS; ++q)
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) m = fmaxf(m, x[i][q][e]);
-        if (m > -INFINITY) {
+          for (int e = 0; e < VEC; ++e) m = max_nan(m, x[i][q][e]);
+        if (m != -INFINITY) {
           float l = a[i].l * fast_exp2((a[i].m - m) * p.k);
 #pragma unroll
           for (int q = 0; q < LOADS; ++q)

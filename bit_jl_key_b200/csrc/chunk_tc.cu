@@ -204,13 +204,6 @@ __device__ __forceinline__ float2 exp2_poly(f32x2 x) {
                      __uint_as_float(__float_as_uint(k.y) * 0x800000u + __float_as_uint(v.y)));
 }
 
-// The larger one, or NaN where either is.
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float y;
-  asm("max.NaN.f32 %0, %1, %2;\n" : "=f"(y) : "f"(a), "f"(b));
-  return y;
-}
-
 // Largest of the 64 scores at tS, NaN if one of them is; those from column lim
 // on do not count.
 template <bool MASK>

@@ -243,4 +243,11 @@ __device__ __forceinline__ float fast_exp2(float x) {
   return y;
 }
 
+// The larger one, or NaN where either is (fmaxf gives the other one).
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;\n" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+
 }  // namespace jlk

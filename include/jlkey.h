@@ -718,8 +718,8 @@ JL_API int jl_chunk_attention_paged(
  *              seq_lens[b] on are left as they were.
  *   seq_lens : in, device, B int32; a length outside [0, max_len] records
  *              JL_DERR_DECODE_PLAN and is clipped.
- * A head whose scores are all -inf adds nothing.  Statistics and sums are
- * fp32.  B == 0 is a no-op.  Errors: JL_ERR_INVALID_ARG, JL_ERR_UNSUPPORTED
+ * A head whose scores are all -inf adds nothing; one with a NaN or +inf among
+ * them makes all of its KV head's entries NaN.  Statistics and sums are fp32.  B == 0 is a no-op.  Errors: JL_ERR_INVALID_ARG, JL_ERR_UNSUPPORTED
  * (more than 512 query heads per KV head, B * Hkv >= 2^24), JL_ERR_CUDA.
  */
 JL_API int jl_accumulate_attention(const float *scores, const float *mass,

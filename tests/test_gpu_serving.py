@@ -584,6 +584,20 @@ def test_accumulate_masked_rows_and_lengths():
     assert torch.all(out[0] == 0) and abs(out[1, 0].sum().item() - 2) < 1e-5
 
 
+@pytest.mark.parametrize("T", [1, 5, 77, 2000, 2001, 70001])
+@pytest.mark.parametrize("x", [math.nan, math.inf])
+def test_accumulate_scores_that_are_not_finite_show_in_the_whole_row(T, x):
+    """As a softmax has it: one such score, and none of its head's weights is a
+    number, however few keys the thread that meets it has besides."""
+    for t in {0, T // 2, T - 1}:
+        scores = _randn(5, 1, 4, T)
+        ref = jl.jl_accumulate_attention(scores, torch.zeros(1, 2, T, device=DEV), _i32([T]), 1.0)
+        scores[0, 1, t] = x
+        out = jl.jl_accumulate_attention(scores, torch.zeros(1, 2, T, device=DEV), _i32([T]), 1.0)
+        assert torch.isnan(out[0, 0]).all(), t
+        assert torch.equal(out[0, 1], ref[0, 1])
+
+
 # --------------------------------------------------------------------------
 # eviction
 
