@@ -205,7 +205,9 @@ struct Params {
   int Hq, Hkv, G;
   int64_t T;
   bool out_vec;          // out is 16-byte aligned
-  float k, sign, decay;  // k: |softmax_scale| log2(e); sign: of softmax_scale
+  // scores are read times `half`, softmax_scale's sign over 2, so that no
+  // difference of two overflows; k, of such a difference: 2 |softmax_scale| log2(e)
+  float k, half, decay;
   int *err;
 };
 
@@ -214,8 +216,8 @@ struct MS {
 };
 // Joins two softmax states; a state without keys is (-inf, 0), and one with a
 // NaN among them NaN in both.  The maximum is of the scores themselves (times
-// the scale's sign): only differences are scaled, so a row of the type's lowest
-// value is as uniform as any other.
+// `half`): only differences are scaled, so a row of the type's lowest value is as
+// uniform as any other.
 __device__ __forceinline__ MS join(MS a, MS b, float k) {
   const float m = max_nan(a.m, b.m);
   if (m == -INFINITY) return {m, 0.f};
@@ -280,7 +282,7 @@ __global__ void __launch_bounds__(THREADS) mass_kernel(const Params p) {
       for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int q = 0; q < LOADS; ++q)
-          load_scores<VEC>(s + i * more, t + q * STEP, n, p.sign, x[i][q]);
+          load_scores<VEC>(s + i * more, t + q * STEP, n, p.half, x[i][q]);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         float m = a[i].m;
@@ -347,7 +349,7 @@ __global__ void __launch_bounds__(THREADS) mass_kernel(const Params p) {
       float x[2][VEC];
 #pragma unroll
       for (int q = 0; q < 2; ++q)
-        load_scores<VEC>(s0 + (int64_t)g * p.T, t + q * STEP, n, p.sign, x[q]);
+        load_scores<VEC>(s0 + (int64_t)g * p.T, t + q * STEP, n, p.half, x[q]);
 #pragma unroll
       for (int q = 0; q < 2; ++q)
 #pragma unroll
@@ -405,9 +407,12 @@ cudaError_t launch_accumulate(const AccumulateArgs &a, cudaStream_t stream) {
   mass::Params p{};
   p.scores = a.scores; p.mass = a.mass; p.out = a.out; p.lens = a.seq_lens;
   p.Hq = a.Hq; p.Hkv = a.Hkv; p.G = a.Hq / a.Hkv; p.T = a.max_len;
-  // (a scale of 0 stays above it, so that -inf times it is -inf)
-  p.k = fmaxf(fabsf(a.softmax_scale) * 1.44269504088896340736f, 1.17549435e-38f);
-  p.sign = a.softmax_scale < 0.f ? -1.f : 1.f;
+  // (a scale of 0 stays above it, so that -inf times it is -inf: as the least
+  // positive number, by which no difference comes to 2^-20; and none is infinite,
+  // so that 0 times it is 0)
+  p.k = fminf(fmaxf(fabsf(a.softmax_scale) * 2.88539008177792681472f, 1.40129846e-45f),
+              3.40282347e+38f);
+  p.half = a.softmax_scale < 0.f ? -0.5f : 0.5f;
   p.decay = a.decay;
   p.err = device_error_ptr();
   if (!p.err) return cudaErrorInvalidSymbol;

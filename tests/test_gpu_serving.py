@@ -598,6 +598,28 @@ def test_accumulate_scores_that_are_not_finite_show_in_the_whole_row(T, x):
         assert torch.equal(out[0, 1], ref[0, 1])
 
 
+@pytest.mark.parametrize("scale,values", [
+    (0.0, (0.0, torch.finfo(torch.float32).min)),               # uniform, whatever the scores
+    (0.0, (3e38, -3e38)),
+    (1e-38, (3e38, -3e38)),                                     # logits 3 and -3
+    (-1e-38, (3.4e38, -3.4e38, 1e38)),
+    (1.0, (1.0, torch.finfo(torch.float32).min)),               # an additive mask
+    (3e38, (1.0, 0.0)),                                         # the larger ones alone
+])
+def test_accumulate_scales_and_scores_of_any_size(scale, values):
+    T = 600
+    scores = torch.tensor(values, device=DEV).repeat(T)[:T].view(1, 1, T).contiguous()
+    out = jl.jl_accumulate_attention(scores, torch.zeros(1, 1, T, device=DEV), _i32([T]), scale)
+    x = H.f64(scores[0, 0]) * float(np.float32(scale))
+    w = np.exp(x - x.max())
+    w /= w.sum()
+    # as in test_accumulate; a scale of 0 counts as 2^-149, which makes a
+    # difference of at most 2^129 logits of 2^-20
+    tol = w * (U32 * (8 * (min(np.abs(x).max(), 100.0) * 1.5 + 1) + 80) +
+               (2 * 2.0 ** -20 if scale == 0 else 0))
+    assert np.all(np.abs(H.f64(out[0, 0]) - w) <= tol + 1e-37)
+
+
 # --------------------------------------------------------------------------
 # eviction
 
