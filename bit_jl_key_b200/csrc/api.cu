@@ -704,6 +704,13 @@ int jl_accumulate_attention(const float *scores, const float *mass, const int32_
   if (!scores || !seq_lens || !out || (decay != 0.f && !mass)) return JL_ERR_INVALID_ARG;
   if (!aligned(scores, 4) || !aligned(mass, 4) || !aligned(seq_lens, 4) || !aligned(out, 4))
     return JL_ERR_INVALID_ARG;
+  // a block writes its keys while others read theirs: over the mass itself each
+  // key is read by the thread that writes it, over anything else it is not
+  const int64_t out_bytes = (int64_t)B * Hkv * max_len * 4;
+  if (overlap(out, out_bytes, scores, (int64_t)B * Hq * max_len * 4) ||
+      overlap(out, out_bytes, seq_lens, (int64_t)B * 4) ||
+      (decay != 0.f && out != mass && overlap(out, out_bytes, mass, out_bytes)))
+    return JL_ERR_INVALID_ARG;
   jlk::AccumulateArgs a{scores, mass, seq_lens, B, Hq, Hkv, max_len, softmax_scale, decay, out};
   return from_cuda(jlk::launch_accumulate(a, (cudaStream_t)stream));
 }

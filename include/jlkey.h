@@ -714,8 +714,9 @@ JL_API int jl_chunk_attention_paged(
  *              points return; query head h reads KV head h / (Hq / Hkv).
  *   mass     : in, B x Hkv x max_len fp32 (not read when decay is 0, and may
  *              then be NULL).
- *   out      : out, B x Hkv x max_len fp32; may be `mass` itself.  Entries from
- *              seq_lens[b] on are left as they were.
+ *   out      : out, B x Hkv x max_len fp32; may be `mass` itself, but no other
+ *              part of what is read.  Entries from seq_lens[b] on are left as
+ *              they were.
  *   seq_lens : in, device, B int32; a length outside [0, max_len] records
  *              JL_DERR_DECODE_PLAN and is clipped.
  * A head whose scores are all -inf adds nothing; one with a NaN or +inf among

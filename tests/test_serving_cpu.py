@@ -144,6 +144,26 @@ def test_accumulate_refused(lib):
         assert call(**bad) == UNSUPPORTED, bad
 
 
+def test_accumulate_refuses_an_output_over_what_it_reads(lib):
+    """Blocks write while others read, so only the mass itself may be written."""
+    B, Hq, Hkv, T = 2, 8, 2, 100
+    s, m, out, lens = (ctypes.c_void_p(i << 24) for i in (1, 2, 3, 4))
+    at = lambda p, off: ctypes.c_void_p(p.value + off)
+    call = caller(lib.jl_accumulate_attention, s=s, m=m, lens=lens, B=B, Hq=Hq, Hkv=Hkv, max_len=T,
+                  scale=0.1, decay=1.0, out=out, stream=NULL)
+    mass, all_scores = B * Hkv * T * 4, B * Hq * T * 4
+    for bad in (dict(out=s), dict(out=at(s, all_scores - 4)), dict(out=at(s, 4 - mass)),
+                dict(out=at(m, 16)), dict(out=at(m, -16)), dict(out=at(m, mass - 4)),
+                dict(out=at(lens, 4)), dict(out=at(lens, 4 - mass))):
+        assert call(**bad) == INVALID, bad
+    # beside them, over the mass itself, and over a mass that is not read: past the checks
+    # (there is no GPU here to launch on, or the launch is the caller's to make)
+    if not torch.cuda.is_available():
+        for good in (dict(), dict(out=m), dict(out=at(s, all_scores)), dict(out=at(m, mass)),
+                     dict(out=at(m, 16), decay=0.0), dict(m=NULL, decay=0.0)):
+            assert call(**good) not in (INVALID, UNSUPPORTED, OK), good
+
+
 def test_evict_refused(lib):
     call = caller(lib.jl_evict_paged, m=FAKE, lens=FAKE, B=2, Hkv=2, max_len=200, keep=100,
                   recent=10, sink=4, words=8, cn=1, d=128, **POOLS, src=FAKE, sp=4, dst=FAKE2,
