@@ -737,11 +737,22 @@ int jl_evict_paged(const float *mass, const int32_t *seq_lens, int B, int Hkv, i
   if (B == 0) return JL_OK;
   if (!mass || !seq_lens || !src_table || !dst_table || !out_index || !out_mass || !out_lens)
     return JL_ERR_INVALID_ARG;
-  // nothing may be written that the call still reads: a block's answer is out
-  // before another has read its input
-  if (overlap(out_mass, (int64_t)B * Hkv * keep * 4, mass, (int64_t)B * Hkv * max_len * 4) ||
-      overlap(out_lens, (int64_t)B * 4, seq_lens, (int64_t)B * 4) || src_table == dst_table)
-    return JL_ERR_INVALID_ARG;
+  // No output lies over what the call still reads (a block's answer is out before
+  // another has read its input), over the pools or over another output, and the
+  // tables are two.  Whether two tables name one page is not looked at: that takes
+  // every pair of their entries, on the device.
+  const int64_t rows = (int64_t)num_pages * Hkv * page_tokens, kept = (int64_t)B * Hkv * keep * 4;
+  const struct { const void *at; int64_t bytes; } range[] = {
+      {out_index, kept}, {out_mass, kept}, {out_lens, (int64_t)B * 4},
+      {mass, (int64_t)B * Hkv * max_len * 4}, {seq_lens, (int64_t)B * 4},
+      {src_table, (int64_t)B * src_max_pages * 4}, {dst_table, (int64_t)B * dst_max_pages * 4},
+      {code_pages, rows * words * 4}, {norm_pages, rows * norms_per_key * 2},
+      {value_pages, rows * d * 2}};
+  for (int i = 0; i < 3; ++i)
+    for (int j = i + 1; j < 10; ++j)
+      if (overlap(range[i].at, range[i].bytes, range[j].at, range[j].bytes))
+        return JL_ERR_INVALID_ARG;
+  if (src_table == dst_table) return JL_ERR_INVALID_ARG;
   if (!aligned(mass, 4) || !aligned(seq_lens, 4) || !aligned(src_table, 4) ||
       !aligned(dst_table, 4) || !aligned(out_index, 4) || !aligned(out_mass, 4) ||
       !aligned(out_lens, 4))

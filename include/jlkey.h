@@ -746,12 +746,14 @@ JL_API int jl_accumulate_attention(const float *scores, const float *mass,
  *   src_table  : in, B x src_max_pages: the pages that hold the keys.
  *   dst_table  : in, B x dst_max_pages, dst_max_pages * page_tokens >= keep:
  *                pages of the same pools that hold none of the call's keys (so
- *                never src_table itself: a cache is not shrunk in place).
+ *                never src_table itself: a cache is not shrunk in place).  A page
+ *                that both name is not noticed, and what it then holds is
+ *                undefined.
  *   out_index  : out, B x Hkv x keep int32: the old index of each kept key,
  *                ascending, then -1.
- *   out_mass   : out, B x Hkv x keep fp32: the kept keys' mass, then 0.  No
- *                part of `mass`.
- *   out_lens   : out, B int32: L'.  No part of `seq_lens`.
+ *   out_mass   : out, B x Hkv x keep fp32: the kept keys' mass, then 0.
+ *   out_lens   : out, B int32: L'.
+ * The outputs overlap neither each other nor anything else that is passed.
  * A key with a page outside the pool, at either end, is not moved and
  * JL_DERR_PAGE recorded.  B == 0 is a no-op.  Errors: JL_ERR_INVALID_ARG,
  * JL_ERR_UNSUPPORTED (as jl_store_paged; max_len >= 2^31), JL_ERR_CUDA.

@@ -184,6 +184,28 @@ def test_evict_refused(lib):
         assert call(**bad) == UNSUPPORTED, bad
 
 
+def test_evict_refuses_outputs_over_what_it_reads_or_writes(lib):
+    B, Hkv, T, keep, P, pages, words, d = 2, 2, 200, 100, 64, 10, 8, 128
+    ptr = {k: ctypes.c_void_p((i + 1) << 26) for i, k in enumerate(
+        ("m", "lens", "codes", "norms", "values", "src", "dst", "oi", "om", "ol"))}
+    rows = pages * Hkv * P
+    size = dict(m=B * Hkv * T * 4, lens=B * 4, codes=rows * words * 4, norms=rows * 2,
+                values=rows * d * 2, src=B * 4 * 4, dst=B * 2 * 4, oi=B * Hkv * keep * 4,
+                om=B * Hkv * keep * 4, ol=B * 4)
+    call = caller(lib.jl_evict_paged, m=ptr["m"], lens=ptr["lens"], B=B, Hkv=Hkv, max_len=T,
+                  keep=keep, recent=10, sink=4, words=words, cn=1, d=d, codes=ptr["codes"],
+                  norms=ptr["norms"], values=ptr["values"], pages=pages, P=P, src=ptr["src"], sp=4,
+                  dst=ptr["dst"], dp=2, oi=ptr["oi"], om=ptr["om"], ol=ptr["ol"], stream=NULL)
+    for out in ("oi", "om", "ol"):
+        for other in ptr:
+            if other != out:
+                for at in (ptr[other].value + size[other] - 4, ptr[other].value + 4 - size[out]):
+                    assert call(**{out: ctypes.c_void_p(at)}) == INVALID, (out, other)
+    if not torch.cuda.is_available():          # side by side: past the checks
+        assert call() not in (INVALID, UNSUPPORTED, OK)
+        assert call(om=ctypes.c_void_p(ptr["oi"].value + size["oi"])) not in (INVALID, UNSUPPORTED)
+
+
 # --------------------------------------------------------------------------
 # the wrappers' own checks, on CPU tensors (which they refuse last)
 
