@@ -730,9 +730,9 @@ int jl_evict_paged(const float *mass, const int32_t *seq_lens, int B, int Hkv, i
   if ((int64_t)dst_max_pages * page_tokens < keep ||
       (int64_t)src_max_pages * page_tokens < max_len)
     return JL_ERR_INVALID_ARG;
-  // the moved keys are one flat grid of blocks of at least 16 keys
+  // the moved keys are one flat grid
   if (max_len >= ((int64_t)1 << 31) || (int64_t)B * Hkv >= (1 << 24) ||
-      (int64_t)B * Hkv * ((int64_t)keep / 16 + 1) >= ((int64_t)1 << 31))
+      (int64_t)B * Hkv * jlk::evict_blocks(keep) >= ((int64_t)1 << 31))
     return JL_ERR_UNSUPPORTED;
   if (B == 0) return JL_OK;
   if (!mass || !seq_lens || !src_table || !dst_table || !out_index || !out_mass || !out_lens)

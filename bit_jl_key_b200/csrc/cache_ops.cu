@@ -437,7 +437,7 @@ namespace evict {
 
 constexpr int THREADS = 512, WARPS = THREADS / 32;
 constexpr int BINS = 256, COPIES = 8;  // of a histogram: equal digits in a warp are common
-constexpr int COPY_THREADS = 128, MAX_CLUSTER = 8;
+constexpr int COPY_THREADS = EVICT_KEYS, MAX_CLUSTER = 8;
 
 struct Params {
   Pools pool;
@@ -666,7 +666,7 @@ struct Cache {
 template <int D, int UNIT>
 __global__ void __launch_bounds__(COPY_THREADS) move_kernel(const Params p) {
   griddep_wait();
-  const int tiles = (p.keep + COPY_THREADS - 1) / COPY_THREADS;
+  const int tiles = (int)evict_blocks(p.keep);
   const int unit = blockIdx.x / tiles, b = unit / p.pool.Hkv, h = unit - b * p.pool.Hkv;
   const int64_t j = (int64_t)(blockIdx.x - unit * tiles) * COPY_THREADS + threadIdx.x;
   int64_t from = 0, to = -1;
@@ -710,8 +710,7 @@ cudaError_t launch_evict_paged(const EvictArgs &a, cudaStream_t stream) {
                      evict::THREADS, smem, stream, p);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)((a.keep + evict::COPY_THREADS - 1) / evict::COPY_THREADS * a.B *
-                                a.Hkv));
+  cfg.gridDim = dim3((unsigned)(evict_blocks(a.keep) * a.B * a.Hkv));
   cfg.blockDim = dim3(evict::COPY_THREADS);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];

@@ -217,6 +217,11 @@ struct EvictArgs {
   int32_t *out_index, *out_lens;
   float *out_mass;
 };
+// Keys that a block of the moving kernel takes, and its blocks for `keep` keys.
+constexpr int EVICT_KEYS = 128;
+__host__ __device__ inline int64_t evict_blocks(int64_t keep) {
+  return (keep + EVICT_KEYS - 1) / EVICT_KEYS;
+}
 cudaError_t launch_evict_paged(const EvictArgs &a, cudaStream_t stream);
 
 // Attention of a ragged chunk over a paged cache of QJL codes (chunk_tc.cu).

@@ -756,7 +756,8 @@ JL_API int jl_accumulate_attention(const float *scores, const float *mass,
  * The outputs overlap neither each other nor anything else that is passed.
  * A key with a page outside the pool, at either end, is not moved and
  * JL_DERR_PAGE recorded.  B == 0 is a no-op.  Errors: JL_ERR_INVALID_ARG,
- * JL_ERR_UNSUPPORTED (as jl_store_paged; max_len >= 2^31), JL_ERR_CUDA.
+ * JL_ERR_UNSUPPORTED (as jl_store_paged; max_len >= 2^31, B * Hkv >= 2^24 or
+ * B * Hkv * ceil(keep / 128) >= 2^31), JL_ERR_CUDA.
  */
 JL_API int jl_evict_paged(const float *mass, const int32_t *seq_lens, int B, int Hkv,
                           int64_t max_len, int keep, int recent, int sink, int words,

@@ -206,6 +206,26 @@ def test_evict_refuses_outputs_over_what_it_reads_or_writes(lib):
         assert call(om=ctypes.c_void_p(ptr["oi"].value + size["oi"])) not in (INVALID, UNSUPPORTED)
 
 
+def test_evict_largest_sizes(lib):
+    """The grid of moved keys is counted in blocks of 128 keys, in 64 bits."""
+    ptr = [ctypes.c_void_p((i + 1) << 50) for i in range(10)]
+    call = caller(lib.jl_evict_paged, m=ptr[0], lens=ptr[1], B=1, Hkv=1, max_len=200, keep=100,
+                  recent=0, sink=0, words=8, cn=1, d=128, codes=ptr[2], norms=ptr[3],
+                  values=ptr[4], pages=10, P=64, src=ptr[5], sp=4, dst=ptr[6], dp=2, oi=ptr[7],
+                  om=ptr[8], ol=ptr[9], stream=NULL)
+    most = 2 ** 31 - 1
+    wide = dict(dp=2 ** 25)                     # destination pages for any keep
+    for keep, B, Hkv, fits in ((most, 1, 1, True), (most - 126, 1, 1, True), (most, 15, 8, True),
+                               (most, 16, 8, False), (2 ** 20, 2 ** 10, 2 ** 8, False),
+                               (2 ** 20, 2 ** 10, 2 ** 8 - 1, True), (1, 2 ** 12, 2 ** 12, False),
+                               (1, 2 ** 12, 2 ** 12 - 1, True)):
+        got = call(keep=keep, B=B, Hkv=Hkv, **wide)
+        if not fits:
+            assert got == UNSUPPORTED, (keep, B, Hkv)
+        elif not torch.cuda.is_available():     # (nothing to launch on: past the checks)
+            assert got not in (INVALID, UNSUPPORTED, OK), (keep, B, Hkv)
+
+
 # --------------------------------------------------------------------------
 # the wrappers' own checks, on CPU tensors (which they refuse last)
 
