@@ -649,7 +649,9 @@ size_t jl_chunk_attention_workspace_bytes(int64_t N, int B, int Hq, int Hkv, int
                                           int m, int d) {
   if (N < 1 || B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || max_len < 1 || !supported_md(m, d))
     return 0;
-  if (N >= ((int64_t)1 << 31) / Hq || max_len >= ((int64_t)1 << 31)) return 0;
+  if (N >= ((int64_t)1 << 31) / Hq || max_len >= ((int64_t)1 << 31) ||
+      !jlk::chunk_sizes_fit(N, B, Hq, Hkv, max_len, d))
+    return 0;
   return jlk::chunk_workspace_bytes(N, B, Hq, Hkv, max_len, m, d);
 }
 
@@ -672,6 +674,7 @@ int jl_chunk_attention_paged(const void *Q, jl_dtype q_dtype, int64_t q_tok_stri
       (int64_t)num_pages * Hkv >= ((int64_t)1 << 31) / page_tokens)
     return JL_ERR_UNSUPPORTED;
   if (N == 0 || B == 0) return JL_OK;
+  if (!jlk::chunk_sizes_fit(N, B, Hq, Hkv, max_len, d)) return JL_ERR_UNSUPPORTED;
   if (!Q || !S || !sign_pages || !norm_pages || !value_pages || !block_table || !seq_lens ||
       !cu_seqlens || !out)
     return JL_ERR_INVALID_ARG;

@@ -420,6 +420,7 @@ size_t many_workspace(int64_t N, int B, int Hq, int Hkv, int64_t max_len, int d,
 cudaError_t launch_few(Params p, const ChunkArgs &a, cudaStream_t stream);
 cudaError_t launch_many(Params p, const ChunkArgs &a, cudaStream_t stream);
 int few_rows(int64_t N, int B, int G);  // rows of a row tile of the kernel for few rows
+constexpr int MANY_ROWS = 256;          // and of the one for many
 
 }  // namespace chunk
 }  // namespace jlk

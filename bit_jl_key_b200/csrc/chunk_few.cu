@@ -864,6 +864,15 @@ static bool many(int64_t N, int B, int Hq, int Hkv, int64_t max_len, int d) {
          tiles < ((int64_t)1 << 31) / chunk::BN;
 }
 
+bool chunk_sizes_fit(int64_t N, int B, int Hq, int Hkv, int64_t max_len, int d) {
+  constexpr int64_t most = ((int64_t)1 << 31) - 1;
+  if (max_len > most + 1 - chunk::BN) return false;  // a length rounded up to a tile
+  // a sequence has at most this many row tiles, each of at most all key tiles
+  const int G = Hq / Hkv;
+  const int rows = many(N, B, Hq, Hkv, max_len, d) ? chunk::MANY_ROWS : chunk::few_rows(N, B, G);
+  return (N * G / rows + 1) * ((max_len + chunk::BN - 1) / chunk::BN) <= most;
+}
+
 size_t chunk_workspace_bytes(int64_t N, int B, int Hq, int Hkv, int64_t max_len, int m, int d) {
   return many(N, B, Hq, Hkv, max_len, d)
              ? chunk::many_workspace(N, B, Hq, Hkv, max_len, d, nullptr, nullptr)

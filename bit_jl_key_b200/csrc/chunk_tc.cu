@@ -66,6 +66,7 @@ namespace chunk {
 namespace {
 
 constexpr int BM = 128, HALVES = 2, ROWS = BM * HALVES;
+static_assert(ROWS == MANY_ROWS, "rows of a row tile");
 constexpr int SM_WARPS = 8;                       // of a half: four for each 64 of the keys
 constexpr int MMA_WARP = SM_WARPS * HALVES, LOAD_WARP = MMA_WARP + 1;
 constexpr int THREADS = (LOAD_WARP + 1) * 32;

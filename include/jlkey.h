@@ -692,8 +692,10 @@ JL_API size_t jl_chunk_attention_workspace_bytes(int64_t N, int B, int Hq, int H
  * JL_DERR_PAGE is recorded and the sequence's rows are undefined.  The queries'
  * projections are rounded to binary16 under a power-of-two scale per row and
  * the weights to bf16; sums are fp32.  N == 0 or B == 0 is a no-op.
- * Errors: JL_ERR_INVALID_ARG, JL_ERR_UNSUPPORTED (m, d; N * Hq, the pools'
- * rows or max_len at or above 2^31), JL_ERR_WORKSPACE, JL_ERR_CUDA.
+ * Errors: JL_ERR_INVALID_ARG, JL_ERR_UNSUPPORTED (m, d; N * Hq or the pools'
+ * rows at or above 2^31, max_len above 2^31 - 128, or so many rows over so many
+ * keys that the 32-row tiles of a head times the 128-key tiles of max_len may
+ * pass 2^31), JL_ERR_WORKSPACE, JL_ERR_CUDA.
  */
 JL_API int jl_chunk_attention_paged(
     const void *Q, jl_dtype q_dtype, int64_t q_tok_stride, int64_t q_head_stride, int64_t N,

@@ -132,6 +132,26 @@ def test_chunk_refused(lib):
         assert call(**bad) == WORKSPACE, bad
 
 
+def test_chunk_largest_sizes(lib):
+    """Keys of a tile past the last one, and the units (row tile, key tile) of a
+    head, are counted in 32 bits: what would pass them is refused."""
+    f = lib.jl_chunk_attention_workspace_bytes
+    call = caller(lib.jl_chunk_attention_paged, Q=FAKE, dt=jl.JL_BF16, qt=1024, qh=128, N=10,
+                  S=FAKE, codes=FAKE, norms=FAKE, values=FAKE, pages=10, P=64, table=FAKE,
+                  mp=2 ** 26, lens=FAKE, cu=FAKE, B=2, Hq=8, Hkv=2, max_len=200, m=256, d=128,
+                  scale=0.1, out=FAKE, ws=NULL, wsb=0, stream=NULL)
+    for N, B, Hq, Hkv, max_len, fits in (
+            (10, 2, 8, 2, 2 ** 31 - 128, True), (10, 2, 8, 2, 2 ** 31 - 127, False),
+            (10, 2, 8, 2, 2 ** 31 - 1, False),
+            (2 ** 11, 1, 32, 8, 2 ** 20, True),            # a long prompt over a million keys
+            (2 ** 17, 1, 32, 8, 2 ** 20, True),
+            (2 ** 20, 1, 8, 8, 2 ** 20, True),             # and a million tokens over them
+            (2 ** 11, 1, 64, 8, 2 ** 30, False)):          # 256 row tiles of 2^23 key tiles
+        assert (f(N, B, Hq, Hkv, max_len, 256, 128) > 0) == fits, (N, max_len)
+        got = call(N=N, B=B, Hq=Hq, Hkv=Hkv, max_len=max_len)
+        assert got == (WORKSPACE if fits else UNSUPPORTED), (N, max_len)
+
+
 def test_accumulate_refused(lib):
     call = caller(lib.jl_accumulate_attention, s=FAKE, m=FAKE, lens=FAKE, B=2, Hq=8, Hkv=2,
                   max_len=100, scale=0.1, decay=1.0, out=FAKE, stream=NULL)
