@@ -804,6 +804,9 @@ def _on(stream, tensors, run):
             raise ValueError(f"tensors on different devices: {tensors[0].device} and {t.device}")
     if stream is None and dev == torch.cuda.current_device():
         return run(_raw_stream(dev))
+    at = getattr(stream, "device", None)  # (a bare handle does not tell)
+    if at is not None and at.index != dev:
+        raise ValueError(f"the stream is on {at}, the tensors on {tensors[0].device}")
     with _entered(tensors[0].device, stream):
         return run(_raw_stream(dev))
 

@@ -312,3 +312,23 @@ def test_wrappers_refuse():
         refused(jl.jl_evict_paged, *ok[:i], t, *ok[i + 1:])
     refused(jl.jl_evict_paged, *ok, out_index=torch.zeros(2, 2, 19, dtype=torch.int32))
     refused(jl.jl_evict_paged, *ok)                           # not on a GPU
+
+
+def test_a_stream_of_another_device_is_refused(monkeypatch):
+    """Launched there, the kernels would read this device's memory from the other."""
+    class On:
+        def __init__(self, index):
+            self.device = torch.device("cuda", index)
+            self.cuda_stream = 0
+
+        def get_device(self):
+            return self.device.index
+
+    def no_entry(*a):
+        raise AssertionError("the call went on")
+
+    monkeypatch.setattr(torch.cuda, "device", no_entry)
+    monkeypatch.setattr(torch.cuda, "stream", no_entry)
+    for stream, tensor in ((On(1), On(0)), (On(0), On(1))):
+        with pytest.raises(ValueError, match="device"):
+            jl._on(stream, (tensor,), no_entry)
