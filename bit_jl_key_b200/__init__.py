@@ -806,7 +806,7 @@ def _on(stream, tensors, run):
         return run(_raw_stream(dev))
     at = getattr(stream, "device", None)  # (a bare handle does not tell)
     if at is not None and at.index != dev:
-        raise ValueError(f"the stream is on {at}, the tensors on {tensors[0].device}")
+        raise ValueError(f"stream and tensors on different devices: {at} and {tensors[0].device}")
     with _entered(tensors[0].device, stream):
         return run(_raw_stream(dev))
 
