@@ -68,7 +68,8 @@ EXPORTED = ("jl_status_string", "jl_sketch_init", "jl_quantize_keys",
             "jl_turbo_dequantize_keys", "jl_test_drop_copies", "jl_build_flags",
             "jl_decode_attention_state", "jl_merge_attention_states",
             "jl_rotary_frequencies", "jl_rotary", "jl_store_paged", "jl_accumulate_attention",
-            "jl_evict_paged", "jl_chunk_attention_workspace_bytes", "jl_chunk_attention_paged")
+            "jl_evict_paged", "jl_chunk_attention_workspace_bytes",
+            "jl_chunk_attention_workspace_bound", "jl_chunk_attention_paged")
 
 # device error codes (jl_device_error)
 JL_DERR_TC_WAIT_TIMEOUT = 1
@@ -167,6 +168,8 @@ def load():
                                  vp, i32, i32, vp, i32, vp, vp]
     L.jl_chunk_attention_workspace_bytes.restype = sz
     L.jl_chunk_attention_workspace_bytes.argtypes = [i64, i32, i32, i32, i64, i32, i32]
+    L.jl_chunk_attention_workspace_bound.restype = sz
+    L.jl_chunk_attention_workspace_bound.argtypes = [i64, i32, i32, i32, i64, i32, i32]
     L.jl_chunk_attention_paged.restype = i32
     L.jl_chunk_attention_paged.argtypes = [vp, i32, i64, i64, i64, vp, vp, vp, vp, i32, i32, vp,
                                            i32, vp, vp, i32, i32, i32, i64, i32, i32, f32, vp,
@@ -964,7 +967,16 @@ def jl_store_paged(codes, norms, V, cu_seqlens, code_pages, norm_pages, value_pa
 
 
 def jl_chunk_attention_workspace_bytes(N, B, Hq, Hkv, max_len, m, d) -> int:
+    """Device scratch of one call of these shapes.  Not more for larger shapes
+    than for smaller ones: a workspace kept for calls of many shapes is
+    jl_chunk_attention_workspace_bound."""
     return int(load().jl_chunk_attention_workspace_bytes(N, B, Hq, Hkv, max_len, m, d))
+
+
+def jl_chunk_attention_workspace_bound(N, B, Hq, Hkv, max_len, m, d) -> int:
+    """Device scratch that serves every call of at most N rows, B sequences and
+    max_len (with these heads, m and d)."""
+    return int(load().jl_chunk_attention_workspace_bound(N, B, Hq, Hkv, max_len, m, d))
 
 
 def jl_chunk_attention_paged(Q, S, sign_pages, norm_pages, value_pages, block_table, seq_lens,
@@ -977,7 +989,12 @@ def jl_chunk_attention_paged(Q, S, sign_pages, norm_pages, value_pages, block_ta
     chunk's own included (jl_store_paged them first); cu_seqlens int32 [B + 1]:
     sequence b's rows.  Row i of its n sees the keys t < seq_lens[b] - n + i +
     1.  Returns out [N, Hq, d] bf16, in which rows of no sequence stay as they
-    were (undefined in a tensor made here)."""
+    were (undefined in a tensor made here).
+
+    Without ``workspace`` the call allocates its own, which for many rows per
+    sequence holds the keys expanded: 2 d bytes per key of max_len and KV head,
+    up to 8 GiB.  One kept over calls of several shapes has
+    jl_chunk_attention_workspace_bound bytes for the largest of them."""
     if Q.dim() != 3 or S.dim() != 2 or block_table.dim() != 2:
         raise ValueError("Q must be [N, Hq, d], S [m, d] and block_table [B, max_pages]")
     qt = _float_code(Q, "Q")

@@ -655,6 +655,14 @@ size_t jl_chunk_attention_workspace_bytes(int64_t N, int B, int Hq, int Hkv, int
   return jlk::chunk_workspace_bytes(N, B, Hq, Hkv, max_len, m, d);
 }
 
+size_t jl_chunk_attention_workspace_bound(int64_t N, int B, int Hq, int Hkv, int64_t max_len,
+                                          int m, int d) {
+  if (N < 1 || B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || max_len < 1 || !supported_md(m, d))
+    return 0;
+  if (N >= ((int64_t)1 << 31) / Hq || max_len >= ((int64_t)1 << 31)) return 0;
+  return jlk::chunk_workspace_bound(N, B, Hq, Hkv, max_len, m, d);
+}
+
 int jl_chunk_attention_paged(const void *Q, jl_dtype q_dtype, int64_t q_tok_stride,
                              int64_t q_head_stride, int64_t N, const uint16_t *S,
                              const uint32_t *sign_pages, const uint16_t *norm_pages,

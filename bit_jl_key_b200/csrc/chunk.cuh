@@ -419,8 +419,8 @@ size_t many_workspace(int64_t N, int B, int Hq, int Hkv, int64_t max_len, int d,
                       void *base);
 cudaError_t launch_few(Params p, const ChunkArgs &a, cudaStream_t stream);
 cudaError_t launch_many(Params p, const ChunkArgs &a, cudaStream_t stream);
-int few_rows(int64_t N, int B, int G);  // rows of a row tile of the kernel for few rows
-constexpr int MANY_ROWS = 256;          // and of the one for many
+constexpr int FEW_ROWS_LEAST = 32, FEW_ROWS_MOST = 64, MANY_ROWS = 256;  // of a row tile
+int few_rows(int64_t N, int B, int G);  // which of the first two
 
 }  // namespace chunk
 }  // namespace jlk

@@ -830,7 +830,9 @@ cudaError_t launch_t(const Params &p, const ChunkArgs &a, cudaStream_t stream) {
 
 // 32 rows where the sequences have that many on average, 64 where they have
 // more: the products and weights of rows that are not there cost as much.
-int few_rows(int64_t N, int B, int G) { return N * G <= (int64_t)32 * B ? 32 : 64; }
+int few_rows(int64_t N, int B, int G) {
+  return N * G <= (int64_t)FEW_ROWS_LEAST * B ? FEW_ROWS_LEAST : FEW_ROWS_MOST;
+}
 
 size_t few_workspace(int64_t N, int B, int Hq, int Hkv, int m, int d, Work *w, void *base) {
   const int rows = few_rows(N, B, Hq / Hkv);
@@ -877,6 +879,18 @@ size_t chunk_workspace_bytes(int64_t N, int B, int Hq, int Hkv, int64_t max_len,
   return many(N, B, Hq, Hkv, max_len, d)
              ? chunk::many_workspace(N, B, Hq, Hkv, max_len, d, nullptr, nullptr)
              : chunk::few_workspace(N, B, Hq, Hkv, m, d, nullptr, nullptr);
+}
+
+// The most that shapes up to these need: of either kernel's parts the larger, with
+// the expanded keys of as many sequences as `many` lets in.
+size_t chunk_workspace_bound(int64_t N, int B, int Hq, int Hkv, int64_t max_len, int m, int d) {
+  const int64_t most = N * (Hq / Hkv) / MANY, seqs = B < most ? B : most;
+  const int64_t tiles = (max_len + chunk::BN - 1) / chunk::BN * seqs * Hkv;
+  const int64_t tile = (int64_t)chunk::BN * d * 2;
+  const int64_t keys = tiles < MAX_KEYS / tile ? tiles * tile : MAX_KEYS;
+  const int rows = seqs > 0 ? chunk::MANY_ROWS : chunk::FEW_ROWS_MOST;
+  return chunk::lay_out(nullptr, nullptr, N, B, Hq, Hkv, chunk::FEW_ROWS_LEAST, m > d ? m : d,
+                        (size_t)rows * (d + 2), (size_t)keys);
 }
 
 cudaError_t launch_chunk(const ChunkArgs &a, cudaStream_t stream) {

@@ -243,6 +243,7 @@ struct ChunkArgs {
 // Whether the kernels' 32-bit counts (keys of tiles, units of a head) hold these shapes.
 bool chunk_sizes_fit(int64_t N, int B, int Hq, int Hkv, int64_t max_len, int d);
 size_t chunk_workspace_bytes(int64_t N, int B, int Hq, int Hkv, int64_t max_len, int m, int d);
+size_t chunk_workspace_bound(int64_t N, int B, int Hq, int Hkv, int64_t max_len, int m, int d);
 cudaError_t launch_chunk(const ChunkArgs &a, cudaStream_t stream);
 
 }  // namespace jlk

@@ -658,11 +658,21 @@ JL_API int jl_store_paged(const uint32_t *codes, const uint16_t *norms, const ui
 
 /*
  * jl_chunk_attention_workspace_bytes -- device scratch that
- * jl_chunk_attention_paged needs for these shapes (the projected queries, the
- * work split and the states of split rows).  Depends on the shapes only;
- * 0 for unsupported shapes and for N == 0 or B == 0.
+ * jl_chunk_attention_paged needs for these shapes: the converted queries, the
+ * work split and the states of split rows, and from 160 rows per sequence and KV
+ * head on (N * Hq / Hkv >= 160 B, padding rows included) the keys expanded to 2 d
+ * bytes per key of max_len and KV head, while those stay within 8 GiB.  Depends
+ * on the shapes only, and a call is refused that brings less.  It may be more
+ * for fewer sequences or a shorter cache; see the bound below.  0 for
+ * unsupported shapes and for N == 0 or B == 0.
+ *
+ * jl_chunk_attention_workspace_bound -- scratch that serves every call of at most
+ * N rows, B sequences and max_len, with these heads, m and d: what a serving loop
+ * allocates once.  0 as above.
  */
 JL_API size_t jl_chunk_attention_workspace_bytes(int64_t N, int B, int Hq, int Hkv,
+                                                 int64_t max_len, int m, int d);
+JL_API size_t jl_chunk_attention_workspace_bound(int64_t N, int B, int Hq, int Hkv,
                                                  int64_t max_len, int m, int d);
 
 /*

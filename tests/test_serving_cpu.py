@@ -132,6 +132,39 @@ def test_chunk_refused(lib):
         assert call(**bad) == WORKSPACE, bad
 
 
+def test_chunk_workspace_for_a_range_of_shapes(lib):
+    """The bytes of a call do not grow with its shapes (few and many rows have
+    kernels of their own); the bound for the largest shapes holds all smaller ones."""
+    import random
+    need = lib.jl_chunk_attention_workspace_bytes
+    bound = lib.jl_chunk_attention_workspace_bound
+    assert jl.jl_chunk_attention_workspace_bound(2048, 64, 32, 8, 32768, 256, 128) == bound(
+        2048, 64, 32, 8, 32768, 256, 128)
+    # fewer sequences, or a shorter cache, of as many rows: the kernel for many rows
+    for big, small in (((2048, 64, 32768), (2048, 32, 32768)), ((8192, 16, 524288), (8192, 16, 131072))):
+        a, b = need(*big[:2], 32, 8, big[2], 256, 128), need(*small[:2], 32, 8, small[2], 256, 128)
+        assert 0 < a < b <= bound(*big[:2], 32, 8, big[2], 256, 128)
+    rng = random.Random(4)
+    log = lambda hi: int(math.exp(rng.uniform(0, math.log(hi))))
+    reached = 0
+    for _ in range(300):
+        N, B, L = log(20000), log(64), log(300000)
+        Hkv, G = rng.choice([1, 2, 8]), rng.choice([1, 3, 4, 8])
+        m, d = rng.choice([64, 128, 256, 512]), rng.choice([64, 128])
+        top = bound(N, B, Hkv * G, Hkv, L, m, d)
+        most = 0
+        for _ in range(60):
+            n, b, t = (x if rng.random() < 0.3 else log(x) for x in (N, B, L))
+            most = max(most, need(n, b, Hkv * G, Hkv, t, m, d))
+            assert most <= top, (N, B, Hkv, G, L, m, d, n, b, t)
+        reached += most > top / 2
+        # and it is no more than the largest keys that the rule admits, beside the rest
+        assert top <= 8 * 2 ** 30 + 2 * N * Hkv * G * (max(m, d) + 8) + 2 ** 26
+    assert reached > 150                        # not a bound for its own sake
+    assert bound(0, 2, 8, 2, 200, 256, 128) == 0 and bound(10, 0, 8, 2, 200, 256, 128) == 0
+    assert bound(10, 2, 8, 3, 200, 256, 128) == 0 and bound(10, 2, 8, 2, 200, 96, 128) == 0
+
+
 def test_chunk_largest_sizes(lib):
     """Keys of a tile past the last one, and the units (row tile, key tile) of a
     head, are counted in 32 bits: what would pass them is refused."""
