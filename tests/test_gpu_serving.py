@@ -276,6 +276,41 @@ def test_chunk_attention(lens, counts, Hq, Hkv, d, m, P, dtype):
     assert torch.equal(got, run_chunk(c, Q, counts, pad=pad))
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("m", [64, 128, 256, 512])
+@pytest.mark.parametrize("n,n2,G", [(3, 7, 4), (11, 23, 3), (97, 5, 4)])
+def test_chunk_attention_every_kernel(d, m, n, n2, G):
+    """Each sketch size and head size on 32-row tiles, on 64-row tiles (more than
+    32 rows a sequence on average, ends inside a tile) and on expanded keys."""
+    c = Cache([n + 130, 290], 2, d, m, 32 if d == 64 else 64, seed=d + m + n)
+    dtype = torch.float32 if m in (64, 256) else torch.bfloat16
+    Q = _randn(21, n + n2 + 1, 2 * G, d, dtype=dtype)
+    got = run_chunk(c, Q, [n, n2], pad=(1, 0))
+    check_chunk(c, Q, [n, n2], got, d ** -0.5, first=1)
+    assert torch.all(got[0] == 7.0)
+    assert torch.equal(got, run_chunk(c, Q, [n, n2], pad=(1, 0)))
+
+
+@pytest.mark.parametrize("n", [60, 700])
+def test_chunk_attention_prompt_beside_single_tokens(n):
+    """A prompt's chunk and decode steps in one batch: whichever kernel its rows
+    choose, in one workspace that serves every smaller batch too."""
+    lens, counts, Hq, Hkv, d, m = [n + 40, 300, 1, 129, 500, 33], [n, 1, 1, 1, 0, 1], 8, 2, 128, 256
+    c = Cache(lens, Hkv, d, m, 64, seed=22)
+    N, most = sum(counts), max(lens)
+    ws = torch.full((jl.jl_chunk_attention_workspace_bound(N, 6, Hq, Hkv, most, m, d),), 255,
+                    dtype=torch.uint8, device=DEV)
+    Q = _randn(23, N, Hq, d, dtype=torch.bfloat16)
+    check_chunk(c, Q, counts, run_chunk(c, Q, counts, workspace=ws), d ** -0.5)
+    for k in (1, 3, 6):                                         # the first k sequences alone
+        sub = Cache.__new__(Cache)
+        sub.__dict__ = dict(c.__dict__, lens=lens[:k], table=c.table[:k])
+        few = counts[:k]
+        for part in (few, [min(x, 2) for x in few], [min(x, 45) for x in few]):
+            q = Q[:sum(part)]
+            check_chunk(sub, q, part, run_chunk(sub, q, part, workspace=ws), d ** -0.5)
+
+
 @pytest.mark.parametrize("rows", [4, 400])
 @pytest.mark.parametrize("scale", [0.0, -0.05, 0.3])
 def test_chunk_attention_scales_and_strides(rows, scale):
