@@ -31,8 +31,7 @@ constexpr int MOST_RECORDS = 128;  // states of one split row tile
 constexpr int MIN_UNITS = 2;       // of a block: less is not worth another state to join
 
 struct Plan {
-  int64_t total;      // units (key tiles, at least one per row tile)
-  int64_t quota;      // units per block
+  int64_t quota;      // units (key tiles, at least one per row tile) per block
 };
 struct Start {        // where a block's run begins
   int64_t u, end;     // units [u, end); none where u >= end
@@ -163,7 +162,6 @@ __device__ __forceinline__ void make_plan(const Params &p) {
   if (quota < longest / (MOST_RECORDS - 2) + 1) quota = longest / (MOST_RECORDS - 2) + 1;
   if (threadIdx.x == 0) {
     p.w.b_unit[p.B] = total;
-    p.w.plan->total = total;
     p.w.plan->quota = quota;
   }
   __threadfence_block();
