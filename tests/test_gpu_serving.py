@@ -838,8 +838,124 @@ def test_strides_along_a_single_token_or_head_are_not_read():
     assert torch.equal(jl.jl_rotary(V, _i32([9]), f), jl.jl_rotary(V.contiguous(), _i32([9]), f))
 
 
+@pytest.mark.parametrize("n,Hq,Hkv,d,rot", [(1, 65536, 0, 2, 2), (2, 2500, 1700, 6, 4),
+                                            (1300, 70, 3, 1024, 1024)])
+def test_rotary_of_many_heads(n, Hq, Hkv, d, rot):
+    """More heads than a block takes at once, and the widest head."""
+    Q = _randn(2, n, Hq, d, dtype=torch.bfloat16)
+    K = _randn(3, n, Hkv, d, dtype=torch.bfloat16) if Hkv else None
+    pos, freq = _i32(np.arange(n) * 1000 + 7), jl.jl_rotary_frequencies(rot)
+    got = jl.jl_rotary(Q, pos, freq, K=K)
+    for y, x in ((got[0], Q), (got[1], K)) if Hkv else ((got, Q),):
+        some = sorted({0, n // 2, n - 1})                       # (in float64, not all of them)
+        check_rotary(y[some], x[some], pos[some], freq, False, False, 1.0)
+        assert torch.equal(y[:, -1:], jl.jl_rotary(x[:, -1:], pos, freq))
+
+
+@pytest.mark.parametrize("G", [1, 2, 3, 511, 512])
+def test_accumulate_heads_of_a_group(G):
+    T, Hkv = 130, 2
+    scores = _randn(6, 1, G * Hkv, T)
+    out = jl.jl_accumulate_attention(scores, torch.zeros(1, Hkv, T, device=DEV), _i32([T]), 0.7)
+    x = H.f64(scores[0]) * float(np.float32(0.7))
+    w = np.exp(x - x.max(-1, keepdims=True))
+    w = (w / w.sum(-1, keepdims=True)).reshape(Hkv, G, T).sum(1)
+    # as in test_accumulate, with a sum over the group's heads
+    tol = w * U32 * (8 * (np.abs(x).max() * 1.5 + 1) + 80 + G)
+    assert np.all(np.abs(H.f64(out[0]) - w) <= tol)
+
+
+@pytest.mark.parametrize("W", [64, 33, 17])
+@pytest.mark.parametrize("d", [64, 128])
+def test_store_and_evict_codes_of_more_words_than_a_key_has_lanes(W, d):
+    Hkv, P, n, keep = 2, 32, 75, 41
+    rng = _rng(W)
+    pools = (torch.zeros(6, Hkv, P, W, dtype=torch.int32, device=DEV),
+             torch.zeros(6, Hkv, P, 2, dtype=torch.float16, device=DEV),
+             torch.zeros(6, Hkv, P, d, dtype=torch.bfloat16, device=DEV))
+    codes = _i32(rng.integers(-2 ** 31, 2 ** 31, size=(n, Hkv, W)))
+    norms, V = _randn(7, n, Hkv, 2).half(), _randn(8, n, Hkv, d, dtype=torch.bfloat16)
+    src, dst = np.array([[4, 0, 3]]), np.array([[1, 5]])
+    jl.jl_store_paged(codes, norms, V, _i32([0, n]), *pools, _i32(src), _i32([0]))
+    t = np.arange(n)
+    for p, x in zip(pools, (codes, norms, V)):
+        assert torch.equal(p[src[0, t // P], :, t % P], x)
+        assert torch.all(p[[1, 2, 5]] == 0)
+    mass = _randn(9, 1, Hkv, n)
+    idx, _, _ = jl.jl_evict_paged(mass, _i32([n]), keep, *pools, _i32(src), _i32(dst), recent=3)
+    for h in range(Hkv):
+        t = evict64(mass[0, h].cpu().numpy(), n, keep, 3, 0)
+        assert np.array_equal(idx[0, h].cpu().numpy(), t)
+        j = np.arange(keep)
+        for p, x in zip(pools, (codes, norms, V)):
+            assert torch.equal(p[dst[0, j // P], h, j % P], x[t, h])
+
+
 # --------------------------------------------------------------------------
 # the operators together
+
+@pytest.mark.parametrize("n", [3, 200])
+def test_a_step_captured_and_on_another_stream(n):
+    """Rotary, quantizer, store, attention, weights and eviction as one graph,
+    replayed on other inputs, and on a stream of their own: bit for bit what the
+    calls give one by one."""
+    Hq, Hkv, d, m, P, L, keep = 8, 2, 64, 128, 32, 200 + n, 64
+    S, freq = jl.jl_sketch_init(m, d, 0), jl.jl_rotary_frequencies(d)
+    pages = -(-L // P) + keep // P
+    i32 = lambda *a: _i32(np.array(a))
+    table = _i32(np.arange(-(-L // P))[None])
+    spare = _i32(np.arange(-(-L // P), pages)[None])
+    inputs = [(_randn(80 + s, n, Hq + 2 * Hkv, d, dtype=torch.bfloat16), _randn(90 + s, 1, Hq, L))
+              for s in range(3)]
+
+    def fresh():
+        g = _rng(5)
+        return (_i32(g.integers(-2 ** 31, 2 ** 31, size=(pages, Hkv, P, m // 32))),
+                _randn(6, pages, Hkv, P).abs().half() * 8,
+                _randn(7, pages, Hkv, P, d, dtype=torch.bfloat16))
+
+    def step(qkv, scores, pools, mass, **k):
+        q, kk = jl.jl_rotary(qkv[:, :Hq], pos, freq, K=qkv[:, Hq:Hq + Hkv], **k)
+        signs, norms = jl.jl_quantize_keys(kk, S, **k)
+        jl.jl_store_paged(signs.view(n, Hkv, -1), norms.view(n, Hkv), qkv[:, Hq + Hkv:], cu,
+                          *pools, table, before, **k)
+        out = jl.jl_chunk_attention_paged(q, S, *pools, table, lens, cu, L, **k)
+        jl.jl_accumulate_attention(scores, mass, lens, 0.3, decay=0.9, **k)
+        return out, mass, *jl.jl_evict_paged(mass, lens, keep, *pools, table, spare, recent=8,
+                                             sink=2, **k)
+
+    pos, cu = _i32(200 + np.arange(n)), i32(0, n)
+    before, lens = i32(200), i32(L)
+    mass0 = _randn(8, 1, Hkv, L).abs()
+    want = []
+    for x in inputs:
+        pools, mass = fresh(), mass0.clone()
+        want.append([t.clone() for t in (*step(*x, pools, mass), *pools)])
+    # a graph
+    pools, mass = fresh(), mass0.clone()
+    x_in = [t.clone() for t in inputs[0]]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = step(*x_in, pools, mass)
+    for i in (1, 2, 0, 0):
+        for a, b in zip((*x_in, *pools, mass), (*inputs[i], *fresh(), mass0)):
+            a.copy_(b)
+        graph.replay()
+        for a, b in zip((*outs, *pools), want[i]):
+            assert torch.equal(a, b), i
+    # another stream, given to each call, while the current one is at work
+    side = torch.cuda.Stream()
+    for i in range(3):
+        pools, mass = fresh(), mass0.clone()
+        side.wait_stream(torch.cuda.current_stream())
+        torch.cuda._sleep(2_000_000)                            # (about a millisecond)
+        got = step(*inputs[i], pools, mass, stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+        for a, b in zip((*got, *pools), want[i]):
+            assert torch.equal(a, b), i
+    torch.cuda.synchronize()
+    del graph
+
 
 def test_serving_loop():
     """A prompt in pieces, drafted tokens, decode steps and an eviction over one
