@@ -149,7 +149,7 @@ struct Chunk {
 // A warp takes 32 consecutive tokens of one KV head, whose rows are neighbours
 // in a page; each lane finds its token's sequence and place.  Bound by memory:
 // 16384 tokens x 8 heads of 308 bytes are 80.7 MB read and written in 15.5 us
-// (5.2 TB/s); 40 tokens take a launch.
+// (5.2 TB/s; 18.6 us as called, 17.1 in a graph); 40 tokens take 7 us in a graph.
 template <int D, int UNIT>
 __global__ void __launch_bounds__(THREADS) store_kernel(const Params p) {
   const int h = blockIdx.y;
@@ -247,9 +247,11 @@ __device__ __forceinline__ void load_scores(const float *s, int i, int n, float 
 // distributed shared memory; pass two reads the scores again, from L2, and
 // writes the weights.  (Keeping them in shared memory in between measured no
 // faster: it costs resident blocks.)  8 sequences of up to 32768 keys, 32 over 8
-// heads, are 40 MB in 18.5-22 us, where the bytes alone would take 6.3: the rest
-// is latency, of the launch, of a first trip to memory per pass and of the
-// blocks' two meetings.
+// heads, are 40 MB in 22.4 us as called and 17.9 in a graph, where the bytes alone
+// would take 6.3.  The rest is this form's latency: a first trip to memory in each
+// of two passes and the blocks' two meetings between them, all for a maximum and a
+// sum per head.  A caller that had those, as a decode step does inside, would need
+// one pass.
 template <int VEC>
 __global__ void __launch_bounds__(THREADS) mass_kernel(const Params p) {
   extern __shared__ MS ms_smem[];            // [G][WARPS], then [G] of the block, [G] of all

@@ -25,9 +25,11 @@
 // stay with the threads until the row tile ends.
 //
 // Measured: 2 to 8 tokens each of 8 sequences of up to 32768 keys, 32 heads over
-// 8 (d = 128, m = 256), are 0.49 GB in 122 us, 4.0 TB/s.  A key tile takes 1740
-// clocks of an SM where its bytes alone would take 1590; the rest of the time is
-// prep (12 us, latency), the first tiles' arrival and the joining of split rows.
+// 8 (d = 128, m = 256), are 0.49 GB in 125 us, 3.9 TB/s (attend alone 117 to 119
+// from cold caches, DRAM 51% busy, issue slots 39%).  A key tile takes 1740 clocks
+// of an SM where its bytes alone would take 1590; the rest of the time is prep (8
+// to 12 us, latency, for all of which attend waits although its first copies need
+// only the plan), the first tiles' arrival and the joining of split rows.
 //
 // Kernels: prep (u and the plan, chunk.cuh), attend.  Warps of attend: 0-3
 // softmax and output; then 8 (4 with 64 rows) that expand, a quarter of the
@@ -854,10 +856,21 @@ cudaError_t launch_few(Params p, const ChunkArgs &a, cudaStream_t stream) {
 
 // Which kernel: expanding the keys costs what one reading and one writing of
 // 2 d bytes per key cost and then makes a row cheap, so it pays from about
-// MANY rows per (sequence, KV head) on (4 sequences of 16384 keys, 32 query and
-// 8 KV heads, d = 128, m = 256: 128 rows 147 us here and 170 us there, 256 rows
-// 233 and 184 us; of 2048 keys: 62 and 54 us, 84 and 60 us), and only while the
-// expanded keys stay inside MAX_KEYS bytes of workspace.
+// MANY rows per (sequence, KV head) on, and only while the expanded keys stay
+// inside MAX_KEYS bytes of workspace.  Microseconds here / there, 4 sequences of 8
+// KV heads, bf16 queries, all sequences with as many rows and keys:
+//   d, m, G      rows   512 keys   2048      8192        32768
+//   128, 256, 4   128    40 / 32   60 / 46    98 / 100   225 / 253
+//                 160    57 / 35   68 / 49   119 / 106   303 / 270
+//                 512    89 / 38  120 / 64   246 / 134   794 / 423
+//   64, 128, 1    128    32 / 30   52 / 41    80 / 77    200 / 211
+//                 160    42 / 34   58 / 42    99 / 83    276 / 228
+//                 512    73 / 32   93 / 52   206 / 109   664 / 339
+// m = 128 at d = 128 and m = 64 at d = 64, G = 4 turn at the same rows.  Below 160
+// rows and 8192 keys the rule takes the slower one, by up to a quarter.  It goes by
+// the average over the batch, padding rows included, and decides for all of it: a
+// chunk of 2048 tokens beside 31 single ones over 32768 keys each takes 2916 us
+// in one call, 1627 as two (beside 63 over 8192: 1170 and 527).
 constexpr int MANY = 160;
 constexpr int64_t MAX_KEYS = (int64_t)8 << 30;
 static bool many(int64_t N, int B, int Hq, int Hkv, int64_t max_len, int d) {

@@ -40,15 +40,15 @@
 // point keeps them as exact, and the accumulator need hardly ever be rescaled.
 //
 // Measured: 2048 tokens of 32 heads over 32768 keys of 8 (d = 128) are 1.07
-// TFLOP of products in 1.01 to 1.19 ms, 1.05 to 0.90 PFLOP/s, the latter once the
-// power limit holds the clock down; over 8192 keys attend alone takes 252 us,
-// tensor pipe 51% busy, exponential unit 39%, issue slots 46%.  What bounds it is
-// the round trip of a half's tile: of 2.6 us (two halves in turn) about 1.0 is
+// TFLOP of products in 1.06 to 1.24 ms, 1.00 to 0.86 PFLOP/s, the latter once the
+// power limit holds the clock down; over 8192 keys attend alone takes 272 us,
+// tensor pipe 47% busy, exponential unit 36%, issue slots 48%.  What bounds it is
+// the round trip of a half's tile: of 2.8 us (two halves in turn) about 1.0 is
 // softmax (maximum 0.25, vote 0.1, weights 0.65), 0.55 the half's two products,
-// S at the rate shared memory feeds its operands, and 1.0 the handing over
+// S at the rate shared memory feeds its operands, and 1.2 the handing over
 // between the warps and the tensor core.  Scores ahead in parts of 64 keys, which
 // hide the round trip, cost more in narrow products than they hide (d = 128: 258
-// to 342 us).
+// to 342 us, when the whole took that).
 //
 // Warps: 0-7 and 8-15 softmax and output of a half, two threads per row (64 of
 // a tile's keys each: a thread alone is held up by its own latencies), 16 MMA

@@ -17,8 +17,8 @@
 // for all its heads.  A block takes `tok` tokens and a range of heads, puts
 // their (cos, sin) into shared memory, then streams the heads with 16-byte
 // loads and stores.  Measured: 16384 tokens of 40 heads (d = 128, 64 of them
-// turned, bf16) are 336 MB in 63.5 us, 5.3 TB/s; a decode step of 8 tokens is one
-// launch.
+// turned, bf16) are 336 MB in 63.9 us, 5.25 TB/s; a decode step of 8 tokens is one
+// launch, 2.2 us in a graph.
 #include "jl_common.cuh"
 #include "jl_internal.h"
 

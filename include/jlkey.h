@@ -682,8 +682,8 @@ JL_API size_t jl_chunk_attention_workspace_bound(int64_t N, int B, int Hq, int H
  * (jl_store_paged); with n = cu_seqlens[b + 1] - cu_seqlens[b] rows and
  * L = seq_lens[b] keys, row i of sequence b attends over the keys
  * t < L - n + i + 1, with the logit of jl_decode_attention_paged, so that the
- * call equals n decode steps.  A row that sees no key (n > L) gets zeros; one
- * that sees a key whose score is not finite is NaN.
+ * call equals n decode steps up to the roundings below.  A row that sees no key
+ * (n > L) gets zeros; one that sees a key whose score is not finite is NaN.
  *   Q          : in, N x Hq x d of q_dtype, token and head strides in elements,
  *                d entries contiguous; aligned to its element.
  *   S, sign_pages, norm_pages, value_pages, num_pages, page_tokens,
@@ -699,9 +699,16 @@ JL_API size_t jl_chunk_attention_workspace_bound(int64_t N, int B, int Hq, int H
  * they hold; a value that some rows of the call see must be finite.  A length
  * outside [0, max_len] is clipped and rows outside [0, N) are dropped, and
  * JL_DERR_DECODE_PLAN recorded; where the table gives no page inside the pool
- * JL_DERR_PAGE is recorded and the sequence's rows are undefined.  The queries'
- * projections are rounded to binary16 under a power-of-two scale per row and
- * the weights to bf16; sums are fp32.  N == 0 or B == 0 is a no-op.
+ * JL_DERR_PAGE is recorded and the sequence's rows are undefined.
+ * Roundings: the weights to bf16, as decode's; one in four first to 2^-13.7 where
+ * there are many rows.  With few rows the queries' projections S q, with many
+ * the queries (fp32 ones too), to binary16 under a power-of-two scale per row,
+ * 2^-11 of each entry (decode keeps 16 bits of the projections); with many rows
+ * also the expanded keys, to binary16.  Sums are fp32.
+ * Few or many (see the workspace) goes by the average over the batch and holds
+ * for all of it, and many rows expand the keys of every sequence: a prompt's
+ * chunk and decode steps of other sequences are faster as two calls.
+ * N == 0 or B == 0 is a no-op.
  * Errors: JL_ERR_INVALID_ARG, JL_ERR_UNSUPPORTED (m, d; N * Hq or the pools'
  * rows at or above 2^31, max_len above 2^31 - 128, or so many rows over so many
  * keys that the 32-row tiles of a head times the 128-key tiles of max_len may
