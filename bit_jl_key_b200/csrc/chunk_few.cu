@@ -25,7 +25,7 @@
 // stay with the threads until the row tile ends.
 //
 // Measured: 2 to 8 tokens each of 8 sequences of up to 32768 keys, 32 heads over
-// 8 (d = 128, m = 256), are 0.49 GB in 125 us, 3.9 TB/s (attend alone 117 to 119
+// 8 (d = 128, m = 256), are 0.49 GB in 120 to 125 us, 4 TB/s (attend alone 117 to 119
 // from cold caches, DRAM 51% busy, issue slots 39%).  A key tile takes 1740 clocks
 // of an SM where its bytes alone would take 1590; the rest of the time is prep (8
 // to 12 us, latency, for all of which attend waits although its first copies need

@@ -609,10 +609,11 @@ JL_API int jl_rotary_frequencies(int rot_dim, double base, jl_rope_scaling scali
  *   inv_freq  : in, device, rot_dim / 2 floats.
  *   interleaved : 0: pair j is entries (j, j + rot_dim/2); 1: (2j, 2j + 1).
  *   scale     : finite factor of the rotated entries (1 for a pure rotation).
- *   out_q, out_k : out, same shapes, each its own strides; no two of their
- *               entries may share an address.  out may be the input itself with
- *               the same strides (in place); any other overlap is an error of
- *               the caller.
+ *   out_q, out_k : out, same shapes, each its own strides, with a token's heads
+ *               next to each other or a head's tokens (no entry of one between
+ *               entries of another); no two entries may share an address.  out
+ *               may be the input itself with the same strides (in place); any
+ *               other overlap is an error of the caller.
  * Angles are formed and reduced in float64; the rotation is fp32, rounded to
  * nearest.  n == 0 is a no-op.  Errors: JL_ERR_INVALID_ARG (null or misaligned
  * pointer, bad size or stride, scale not finite), JL_ERR_UNSUPPORTED (d, n
@@ -632,7 +633,8 @@ JL_API int jl_rotary(const void *Q, const void *K, jl_dtype dtype, int64_t n, in
  * seq_lens[b] + i, in page block_table[b][t / page_tokens], slot
  * t % page_tokens.  Serves QJL and TurboQuant-prod codes alike: what
  * jl_quantize_keys or jl_turbo_quantize_keys wrote for the chunk's keys is
- * moved bit for bit.
+ * moved bit for bit.  The chunk may lie in the pools themselves, but not in rows
+ * that the call writes.
  *   codes      : in, N x Hkv x words uint32, 4-byte aligned.
  *   norms      : in, N x Hkv x norms_per_key binary16 (1: QJL, 2: TurboQuant).
  *   V          : in, N x Hkv x d bf16, token and head strides in elements,

@@ -291,6 +291,43 @@ def test_chunk_attention_every_kernel(d, m, n, n2, G):
     assert torch.equal(got, run_chunk(c, Q, [n, n2], pad=(1, 0)))
 
 
+@pytest.mark.parametrize("counts,G", [([1], 100), ([1, 0, 0, 0], 100), ([2, 1], 71), ([3], 97)])
+def test_chunk_attention_more_heads_than_rows_of_a_tile(counts, G):
+    """A token's heads over several row tiles, of each height."""
+    lens = [150 + 20 * i for i in range(len(counts))]
+    c = Cache(lens, 2, 64, 64, 32, seed=24)
+    Q = _randn(25, sum(counts), 2 * G, 64, dtype=torch.bfloat16)
+    check_chunk(c, Q, counts, run_chunk(c, Q, counts), 64 ** -0.5)
+
+
+@pytest.mark.parametrize("longest,others,G", [(1, 1, 2), (900, 1, 4), (40, 12, 16)])
+def test_chunk_attention_more_sequences_than_the_plan_takes_at_once(longest, others, G):
+    """300 sequences: of single tokens, with a long chunk among them (more row
+    tiles than are counted one by one), and with many rows each; some empty."""
+    B, d, m = 300, 64, 64
+    rng = _rng(26)
+    counts = rng.integers(0, others + 1, size=B) if others > 1 else (rng.random(B) < 0.8) * 1
+    counts = counts + (others if others > 1 else 0)
+    counts[[0, 7, 299]] = 0, 0, others
+    counts[260] = longest
+    lens = (counts + rng.integers(0, 40, size=B)).tolist()
+    counts = counts.tolist()
+    c = Cache(lens, 1, d, m, 32, seed=27)
+    N = sum(counts)
+    assert (N * G >= 160 * B) == (others > 1)
+    Q = _randn(28, N, G, d, dtype=torch.bfloat16)
+    got = run_chunk(c, Q, counts)
+    first = np.concatenate([[0], np.cumsum(counts)])
+    for b in (1, 100, 255, 256, 257, 259, 260, 261, 298, 299):
+        sub = Cache.__new__(Cache)
+        sub.__dict__ = dict(c.__dict__, lens=[lens[b]], table=c.table[b:b + 1])
+        part = slice(int(first[b]), int(first[b + 1]))
+        if counts[b] > 50:                                      # its last rows stand for it
+            part = slice(part.stop - 20, part.stop)
+        check_chunk(sub, Q[part], [part.stop - part.start], got[part], d ** -0.5)
+    assert torch.isfinite(got.float()).all() and torch.equal(got, run_chunk(c, Q, counts))
+
+
 @pytest.mark.parametrize("n", [60, 700])
 def test_chunk_attention_prompt_beside_single_tokens(n):
     """A prompt's chunk and decode steps in one batch: whichever kernel its rows
